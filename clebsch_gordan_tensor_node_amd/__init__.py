@@ -9,6 +9,9 @@ built library or a gfx950 device the calls raise.
     plan = Plan("128x0e+128x1o+128x2e", "1x0e+1x1o+1x2e+1x3o", 3, "parity")
     row_ptr, col, shift = neighbors_build(pos, box, cutoff)
     out = conv_forward(plan, pos, cell, row_ptr, col, shift, x, w, mask)
+
+The operators that train a network around it (layer and irreps normalisation, AdamW) are
+in train.py and exported here.
 """
 from __future__ import annotations
 
@@ -19,9 +22,13 @@ import torch
 
 from . import _lib
 from ._lib import CGTP_PATHS_ALL, CGTP_PATHS_PARITY, CgtpError, check, load
+from .train import (NormPlan, ParamSet, adamw_moments, adamw_state, adamw_step, grad_norm, irreps_norm_backward,
+                    irreps_norm_forward, layer_norm_backward, layer_norm_forward)
 
 __all__ = ["Plan", "neighbors_build", "conv_prepare", "edge_sh", "conv_forward", "conv_backward", "CgtpError",
-           "CGTP_PATHS_ALL", "CGTP_PATHS_PARITY", "library_path", "version"]
+           "CGTP_PATHS_ALL", "CGTP_PATHS_PARITY", "library_path", "version", "NormPlan", "ParamSet", "adamw_moments",
+           "adamw_state", "adamw_step", "grad_norm", "irreps_norm_backward", "irreps_norm_forward",
+           "layer_norm_backward", "layer_norm_forward"]
 
 
 def library_path() -> str:

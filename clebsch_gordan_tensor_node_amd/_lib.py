@@ -17,12 +17,14 @@ CGTP_OK = 0
 ERRORS = {
     -1: "CGTP_ERR_INVALID_ARG", -2: "CGTP_ERR_PARSE", -3: "CGTP_ERR_UNSUPPORTED",
     -4: "CGTP_ERR_CAPACITY", -5: "CGTP_ERR_WORKSPACE", -6: "CGTP_ERR_HIP", -7: "CGTP_ERR_NO_DEVICE",
+    -8: "CGTP_ERR_NO_MEMORY",
 }
 CGTP_ERR_CAPACITY = -4
 CGTP_PATHS_ALL = 0
 CGTP_PATHS_PARITY = 1
 CGTP_PLAN_HOST_ONLY = 1
 CGTP_PLAN_FP64 = 2
+ELEM = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # CGTP_F32, CGTP_BF16, CGTP_F16
 
 EXPORTED = [
     "cgtp_plan_create", "cgtp_plan_info", "cgtp_plan_paths", "cgtp_plan_cg", "cgtp_plan_schedule",
@@ -30,6 +32,11 @@ EXPORTED = [
     "cgtp_conv_prepare", "cgtp_edge_sh", "cgtp_conv_forward", "cgtp_conv_forward_gated", "cgtp_conv_forward_timed",
     "cgtp_conv_forward_f64", "cgtp_conv_forward_noalloc", "cgtp_backward_workspace_size", "cgtp_conv_backward", "cgtp_plan_destroy",
     "cgtp_last_error", "cgtp_version",
+    "cgtp_layer_norm_forward", "cgtp_layer_norm_backward_workspace_size", "cgtp_layer_norm_backward",
+    "cgtp_norm_create", "cgtp_norm_info", "cgtp_norm_destroy", "cgtp_irreps_norm_forward",
+    "cgtp_irreps_norm_backward_workspace_size", "cgtp_irreps_norm_backward", "cgtp_params_create",
+    "cgtp_params_info", "cgtp_params_destroy", "cgtp_adamw_step", "cgtp_adamw_step_8bit", "cgtp_adamw_read_8bit",
+    "cgtp_grad_norm_workspace_size", "cgtp_grad_norm",
 ]
 
 
@@ -44,6 +51,8 @@ _lib = None
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
 I32 = ctypes.c_int
+U32 = ctypes.c_uint32
+F64 = ctypes.c_double
 SZ = ctypes.c_size_t
 FP = ctypes.POINTER(ctypes.c_float)
 DP = ctypes.POINTER(ctypes.c_double)
@@ -80,6 +89,24 @@ def load():
         "cgtp_plan_destroy": ([P], None),
         "cgtp_last_error": ([], ctypes.c_char_p),
         "cgtp_version": ([], ctypes.c_char_p),
+        "cgtp_layer_norm_forward": ([I32, I64, I64, P, I64, I32, P, P, F64, P, I64, P, P], I32),
+        "cgtp_layer_norm_backward_workspace_size": ([I64, I64, ctypes.POINTER(SZ)], I32),
+        "cgtp_layer_norm_backward": ([I32, I64, I64, P, I64, P, I64, P, I32, P, P, I64, P, P, P, SZ, P], I32),
+        "cgtp_norm_create": ([ctypes.c_char_p, ctypes.POINTER(P)], I32),
+        "cgtp_norm_info": ([P, ctypes.POINTER(I64), ctypes.POINTER(I64), ctypes.POINTER(I64),
+                            ctypes.POINTER(I32)], I32),
+        "cgtp_norm_destroy": ([P], None),
+        "cgtp_irreps_norm_forward": ([P, I32, I64, P, I64, I32, P, P, F64, P, I64, P, P], I32),
+        "cgtp_irreps_norm_backward_workspace_size": ([P, I64, ctypes.POINTER(SZ)], I32),
+        "cgtp_irreps_norm_backward": ([P, I32, I64, P, I64, P, I64, P, I32, P, P, I64, P, P, P, SZ, P], I32),
+        "cgtp_params_create": ([ctypes.POINTER(I64), DP, I32, ctypes.c_uint, ctypes.POINTER(P)], I32),
+        "cgtp_params_info": ([P, ctypes.POINTER(I32), ctypes.POINTER(I64), ctypes.POINTER(I64)], I32),
+        "cgtp_params_destroy": ([P], None),
+        "cgtp_adamw_step": ([P, I32, P, I32, P, P, P, F64, F64, F64, F64, I64, P, P], I32),
+        "cgtp_adamw_step_8bit": ([P, I32, P, I32, P, P, P, P, P, F64, F64, F64, F64, I64, U32, P, P], I32),
+        "cgtp_adamw_read_8bit": ([P, P, P, P, P, P, P, P], I32),
+        "cgtp_grad_norm_workspace_size": ([P, ctypes.POINTER(SZ)], I32),
+        "cgtp_grad_norm": ([P, I32, P, P, F64, P, P, SZ, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)

@@ -42,7 +42,8 @@ def _hipcc() -> str:
 
 def _units():
     units = [("cgtp_api.hip", [], "cgtp_api.o"), ("kernels_graph.hip", [], "kernels_graph.o"),
-             ("kernels_bwd.hip", [], "kernels_bwd.o")]
+             ("kernels_bwd.hip", [], "kernels_bwd.o"), ("train_api.hip", [], "train_api.o"),
+             ("kernels_norm.hip", [], "kernels_norm.o"), ("kernels_optim.hip", [], "kernels_optim.o")]
     for c in range(N_CONV_CLASSES):
         units.append(("kernels_conv.hip", [f"-DCGTP_CONV_CLASS={c}"], f"kernels_conv_c{c}.o"))
     return units

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/cgtp.h"
+#include "api_common.hpp"
 #include "launch.hpp"
 #include "nbr.hpp"
 #include "variants.hpp"
@@ -43,6 +44,8 @@ void log_line(int level, const char* fmt, ...) {
   std::fprintf(stderr, "cgtp: %s\n", buf);
 }
 
+}  // namespace
+
 int fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -59,21 +62,14 @@ int ok() {
   return CGTP_OK;
 }
 
-#define CGTP_HIP(call)                                                                  \
-  do {                                                                                  \
-    hipError_t e_ = (call);                                                             \
-    if (e_ != hipSuccess) return fail(CGTP_ERR_HIP, "%s: %s", #call, hipGetErrorString(e_)); \
-  } while (0)
-
-struct Irrep {
-  int mul, l, p;
-};
+namespace {
 
 struct PathInfo {
   int l1, p1, l2, p2, l3, p3, mul, i_in, i_sh, in_off, out_off, w_off;
 };
 
-// Parse "128x0e+64x1o" (a bare "1o" means multiplicity 1).
+}  // namespace
+
 bool parse_irreps(const char* spec, std::vector<Irrep>& out, std::string& err) {
   out.clear();
   if (!spec || !*spec) {
@@ -118,6 +114,8 @@ bool parse_irreps(const char* spec, std::vector<Irrep>& out, std::string& err) {
   }
   return true;
 }
+
+namespace {
 
 std::string format_irreps(const std::vector<Irrep>& v) {
   std::string s;

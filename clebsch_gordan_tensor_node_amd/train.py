@@ -1,0 +1,360 @@
+"""Operators that train a network around the convolution: layer normalisation of rows,
+its equivariant form over irreps, and the AdamW step over many tensors with 32-bit or
+8-bit moments and a gradient norm.
+
+Argument marshalling over libcgtp.so as in the package's other calls: device tensors in,
+the HIP kernels on the caller's current torch stream, no fallback.  The formulas stand in
+include/cgtp.h beside each entry point.
+
+    y, stats = layer_norm_forward(hidden, gamma, beta)
+    grad_hidden, grad_gamma, grad_beta = layer_norm_backward(grad_y, hidden, stats, gamma)
+
+    norm = NormPlan(plan.irreps_out)
+    y, stats = irreps_norm_forward(norm, out, weight, bias)
+
+    params = ParamSet([p.numel() for p in tensors], weight_decay=0.01)
+    state = adamw_state(params, bits=8)
+    factor = grad_norm(params, grads, max_norm=1.0)[1:]
+    adamw_step(params, tensors, grads, state, lr=1e-3, step=t, grad_scale=factor, seed=t)
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import ELEM, check, load
+
+__all__ = ["layer_norm_forward", "layer_norm_backward", "NormPlan", "irreps_norm_forward", "irreps_norm_backward",
+           "ParamSet", "adamw_state", "adamw_step", "adamw_moments", "grad_norm"]
+
+
+def _rows(t, name, shape=None, dtype=None):
+    """Checks a [rows, width] device tensor whose rows are dense; its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device (cuda) tensor")
+    if (t.dtype != dtype) if dtype is not None else (t.dtype not in ELEM):
+        raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {'(rows, width)' if shape is None else tuple(shape)}")
+    n, f = t.shape
+    ld, inner = t.stride()
+    if (inner != 1 and f > 1) or (ld < f and n > 1):
+        raise ValueError(f"{name} must have dense rows that do not overlap, got strides {t.stride()}")
+    return max(ld, f)
+
+
+def _vec(t, n, name, x):
+    """Checks a weight or bias [n] of fp32 or x's type (None passes); its type."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device (cuda) tensor")
+    if t.dtype != torch.float32 and t.dtype != x.dtype:
+        raise TypeError(f"{name} must be float32 or {x.dtype}, got {t.dtype}")
+    if t.shape != (n,):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n},)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.dtype
+
+
+def _device(x, **others):
+    """The library's calls run on the current device: every tensor has to be there."""
+    here = torch.cuda.current_device()
+    for name, t in (("x", x), *others.items()):
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name} is on device {t.device.index}, the current device is {here}")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _weight_type(weight, bias, x, nw, nb):
+    tw, tb = _vec(weight, nw, "weight", x), _vec(bias, nb, "bias", x)
+    if tw is not None and tb is not None and tw != tb:
+        raise TypeError(f"weight ({tw}) and bias ({tb}) must have one type")
+    return tw or tb or torch.float32
+
+
+def _head(plan, x):
+    """The leading arguments of a norm call, and x's row stride, weights, biases and shape
+    of stats."""
+    ld = _rows(x, "x")
+    n, f = x.shape
+    if plan is None:
+        return (ELEM[x.dtype], n, f), ld, f, f, (2, n)
+    if f != plan.n_features:
+        raise ValueError(f"x has rows of {f}, the plan's have {plan.n_features}")
+    return (plan.handle, ELEM[x.dtype], n), ld, plan.n_weights, plan.n_biases, (2, n, plan.n_terms)
+
+
+def _forward(call, plan, x, weight, bias, eps, out):
+    head, ld, nw, nb, stats_shape = _head(plan, x)
+    wt = _weight_type(weight, bias, x, nw, nb)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    ld_y = _rows(out, "out", x.shape, x.dtype)
+    stats = torch.empty(stats_shape, dtype=torch.float32, device=x.device)
+    stream = _device(x, weight=weight, bias=bias, out=out)
+    check(call(*head, _at(x), ld, ELEM[wt], _at(weight), _at(bias), eps, _at(out), ld_y, _at(stats), stream))
+    return out, stats
+
+
+def _backward(call, size, plan, grad_out, x, stats, weight, need, workspace):
+    head, ld, nw, nb, stats_shape = _head(plan, x)
+    ld_g = _rows(grad_out, "grad_out", x.shape, x.dtype)
+    wt = _weight_type(weight, None, x, nw, nb)
+    if not isinstance(stats, torch.Tensor) or not stats.is_cuda or stats.dtype != torch.float32:
+        raise TypeError("stats must be a float32 device (cuda) tensor")
+    if stats.shape != stats_shape or not stats.is_contiguous():
+        raise ValueError(f"stats must be contiguous of shape {stats_shape}, got {tuple(stats.shape)}")
+    dev = x.device
+    gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if "x" in need else None
+    gw = torch.empty(nw, dtype=wt, device=dev) if "weight" in need else None
+    gb = torch.empty(nb, dtype=wt, device=dev) if "bias" in need else None
+    stream = _device(x, grad_out=grad_out, stats=stats, weight=weight, workspace=workspace)
+    if workspace is None and (gw is not None or gb is not None):
+        workspace = torch.empty(size(x.shape[0]), dtype=torch.uint8, device=dev)
+    check(call(*head, _at(grad_out), ld_g, _at(x), ld, _at(stats), ELEM[wt], _at(weight), _at(gx), x.shape[1], _at(gw),
+               _at(gb), _at(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+               stream))
+    return gx, gw, gb
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None):
+    """y [rows, width] of the layer norm of each row of x, and stats [2, rows] (mean and
+    1/sqrt(variance + eps), fp32) for the backward.
+
+    x is fp32, bf16 or fp16 with dense rows any stride apart; weight and bias [width] are
+    fp32 or x's type (None: 1, 0).  Asynchronous on the current stream."""
+    return _forward(load().cgtp_layer_norm_forward, None, x, weight, bias, eps, out)
+
+
+def layer_norm_backward(grad_out, x, stats, weight=None, need=("x", "weight", "bias"), workspace=None):
+    """Gradients of a scalar L with dL/dy = grad_out: (grad_x [rows, width], grad_weight
+    [width], grad_bias [width]); an entry not in `need` is None.  stats is the forward's.
+    grad_weight and grad_bias have weight's type (fp32 without one).  Asynchronous on the
+    current stream; bitwise reproducible."""
+    lib = load()
+
+    def size(n):
+        b = ctypes.c_size_t()
+        check(lib.cgtp_layer_norm_backward_workspace_size(n, x.shape[1], ctypes.byref(b)))
+        return b.value
+
+    return _backward(lib.cgtp_layer_norm_backward, size, None, grad_out, x, stats, weight, need, workspace)
+
+
+class NormPlan:
+    """The equivariant layer norm of irreps rows ("128x0e+64x1o"): each term by itself,
+    0e terms centred and with a bias, every channel with a weight."""
+
+    def __init__(self, irreps: str):
+        lib = load()
+        h = ctypes.c_void_p()
+        check(lib.cgtp_norm_create(irreps.encode(), ctypes.byref(h)))
+        self._h = h
+        f, w, b, t = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int()
+        check(lib.cgtp_norm_info(h, ctypes.byref(f), ctypes.byref(w), ctypes.byref(b), ctypes.byref(t)))
+        self.irreps = irreps
+        self.n_features, self.n_weights, self.n_biases, self.n_terms = f.value, w.value, b.value, t.value
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise ValueError("plan is closed")
+        return self._h
+
+    def backward_workspace_size(self, n_rows: int) -> int:
+        b = ctypes.c_size_t()
+        check(load().cgtp_irreps_norm_backward_workspace_size(self.handle, int(n_rows), ctypes.byref(b)))
+        return b.value
+
+    def close(self):
+        if getattr(self, "_h", None) is not None:
+            load().cgtp_norm_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def irreps_norm_forward(plan: NormPlan, x, weight=None, bias=None, eps: float = 1e-5, out=None):
+    """y [rows, plan.n_features] and stats [2, rows, plan.n_terms]; weight
+    [plan.n_weights] one per channel, bias [plan.n_biases] one per 0e channel.  Types and
+    strides as layer_norm_forward."""
+    return _forward(load().cgtp_irreps_norm_forward, plan, x, weight, bias, eps, out)
+
+
+def irreps_norm_backward(plan: NormPlan, grad_out, x, stats, weight=None, need=("x", "weight", "bias"),
+                         workspace=None):
+    """(grad_x, grad_weight [plan.n_weights], grad_bias [plan.n_biases]) as
+    layer_norm_backward."""
+    return _backward(load().cgtp_irreps_norm_backward, plan.backward_workspace_size, plan, grad_out, x, stats, weight,
+                     need, workspace)
+
+
+class _Pointers:
+    """Device pointers of a set's tensors, checked and laid out for the library; keeps the
+    tensors alive."""
+
+    def __init__(self, tensors, sizes):
+        tensors = list(tensors)
+        if len(tensors) != len(sizes):
+            raise ValueError(f"{len(tensors)} tensors, the set has {len(sizes)}")
+        for k, (t, n) in enumerate(zip(tensors, sizes)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"tensor {k} must be a device (cuda) tensor")
+            if t.dtype != tensors[0].dtype or t.dtype not in ELEM:
+                raise TypeError(f"tensor {k} is {t.dtype}: one type, float32, bfloat16 or float16")
+            if t.device != tensors[0].device:
+                raise ValueError("the tensors of a set are on one device")
+            if t.numel() != n:
+                raise ValueError(f"tensor {k} has {t.numel()} elements, expected {n}")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {k} must be contiguous")
+        self.tensors = tensors
+        self.type = ELEM[tensors[0].dtype] if tensors else 0
+        self.array = (ctypes.c_void_p * max(len(tensors), 1))(*[t.data_ptr() for t in tensors])
+
+
+class ParamSet:
+    """The tensors that one optimiser step covers: their sizes (ints, or tensors whose
+    numel is taken) and weight decay (one number, or one per tensor).  Device tables are on
+    the device that is current when it is made (host_only: none, sizes only)."""
+
+    def __init__(self, sizes, weight_decay=0.0, host_only: bool = False):
+        lib = load()
+        self.sizes = [int(s.numel()) if isinstance(s, torch.Tensor) else int(s) for s in sizes]
+        n = len(self.sizes)
+        decay = list(weight_decay) if hasattr(weight_decay, "__iter__") else [weight_decay] * n
+        if len(decay) != n:
+            raise ValueError(f"{len(decay)} weight decays for {n} tensors")
+        h = ctypes.c_void_p()
+        check(lib.cgtp_params_create((ctypes.c_int64 * max(n, 1))(*self.sizes), (ctypes.c_double * max(n, 1))(*decay),
+                                     n, _lib.CGTP_PLAN_HOST_ONLY if host_only else 0, ctypes.byref(h)))
+        self._h = h
+        elems, offs = ctypes.c_int64(), (ctypes.c_int64 * max(n, 1))()
+        check(lib.cgtp_params_info(h, None, ctypes.byref(elems), offs))
+        self.state_elems, self.offsets = elems.value, list(offs)[:n]
+        b = ctypes.c_size_t()
+        check(lib.cgtp_grad_norm_workspace_size(h, ctypes.byref(b)))
+        self.grad_norm_workspace_size = b.value
+        self.device = None if host_only else torch.device("cuda", torch.cuda.current_device())
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise ValueError("set is closed")
+        return self._h
+
+    def pointers(self, tensors) -> _Pointers:
+        """The set's parameters or gradients laid out once, for calls that use the same
+        tensors again; the calls also take the plain list, and lay it out each time."""
+        return tensors if isinstance(tensors, _Pointers) else _Pointers(tensors, self.sizes)
+
+    def close(self):
+        if getattr(self, "_h", None) is not None:
+            load().cgtp_params_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def adamw_state(params: ParamSet, bits: int = 32):
+    """Zeroed states of a set: (m, v) fp32, or with bits=8 (m codes, r codes, m exponents,
+    r exponents), uint8, of m and r = sqrt(v).  Tensor t's begin at params.offsets[t]."""
+    n = params.state_elems
+    if bits == 32:
+        return tuple(torch.zeros(n, dtype=torch.float32, device=params.device) for _ in range(2))
+    if bits == 8:
+        return tuple(torch.zeros(k, dtype=torch.uint8, device=params.device) for k in (n, n, n // 64, n // 64))
+    raise ValueError("states have 32 or 8 bits")
+
+
+def _state(params, state):
+    n = params.state_elems
+    want = {2: (torch.float32, (n, n)), 4: (torch.uint8, (n, n, n // 64, n // 64))}.get(len(state))
+    if want is None:
+        raise ValueError("a state is (m, v) or (m codes, r codes, m exponents, r exponents)")
+    for t, k in zip(state, want[1]):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != want[0]:
+            raise TypeError(f"states must be {want[0]} device (cuda) tensors")
+        if t.shape != (k,) or not t.is_contiguous():
+            raise ValueError(f"a state has shape {tuple(t.shape)}, expected ({k},), contiguous")
+        if t.device != params.device:
+            raise ValueError("states must be on the set's device")
+    return [t.data_ptr() for t in state]
+
+
+def _scale(params, t):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != params.device or t.dtype != torch.float32 or t.numel() != 1:
+        raise TypeError("grad_scale must be a float32 tensor of one element on the set's device")
+    return t.data_ptr()
+
+
+def _laid(params, tensors, what):
+    p = params.pointers(tensors)
+    if len(p.tensors) != len(params.sizes):
+        raise ValueError(f"{what}: {len(p.tensors)} tensors, the set has {len(params.sizes)}")
+    if p.tensors and p.tensors[0].device != params.device:
+        raise ValueError(f"{what} must be on the set's device")
+    return p
+
+
+def adamw_step(params: ParamSet, tensors, grads, state, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
+               step: int = 1, grad_scale=None, seed: int = 0):
+    """One AdamW step of the set, in place on `tensors` and `state`; step counts from 1.
+
+    tensors and grads: lists of contiguous device tensors (or params.pointers of them).
+    grad_scale: a device tensor of one fp32 (grad_norm's second value, or an inverse loss
+    scale) that multiplies the gradients; NaN skips the step.  With 8-bit states, seed
+    chooses the rounding: pass another each step.  Asynchronous on the current stream."""
+    p, g = _laid(params, tensors, "tensors"), _laid(params, grads, "grads")
+    s, scale, stream = _state(params, state), _scale(params, grad_scale), torch.cuda.current_stream().cuda_stream
+    lib = load()
+    if len(s) == 2:
+        check(lib.cgtp_adamw_step(params.handle, p.type, p.array, g.type, g.array, *s, lr, betas[0], betas[1], eps,
+                                  step, scale, stream))
+    else:
+        check(lib.cgtp_adamw_step_8bit(params.handle, p.type, p.array, g.type, g.array, *s, lr, betas[0], betas[1],
+                                       eps, step, seed & 0xffffffff, scale, stream))
+
+
+def adamw_moments(params: ParamSet, state):
+    """The values of 8-bit states: m and r = sqrt(v) [state_elems], in bf16, which holds
+    them exactly; 32-bit states are returned as they are."""
+    s = _state(params, state)
+    if len(s) == 2:
+        return state
+    m, r = (torch.empty(params.state_elems, dtype=torch.bfloat16, device=params.device) for _ in range(2))
+    check(load().cgtp_adamw_read_8bit(params.handle, *s, m.data_ptr(), r.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream))
+    return m, r
+
+
+def grad_norm(params: ParamSet, grads, max_norm: float = float("inf"), grad_scale=None, workspace=None):
+    """[2] fp32 on the device: the 2-norm of all gradients (times grad_scale) and the
+    factor grad_scale min(1, max_norm / norm) for adamw_step, NaN where the norm is not
+    finite.  Asynchronous on the current stream; bitwise reproducible."""
+    g = _laid(params, grads, "grads")
+    out = torch.empty(2, dtype=torch.float32, device=params.device)
+    if workspace is None:
+        workspace = torch.empty(params.grad_norm_workspace_size, dtype=torch.uint8, device=params.device)
+    check(load().cgtp_grad_norm(params.handle, g.type, g.array, _scale(params, grad_scale), max_norm, out.data_ptr(),
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                torch.cuda.current_stream().cuda_stream))
+    return out

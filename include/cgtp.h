@@ -1,7 +1,8 @@
 /*
  * cgtp.h -- C ABI of libcgtp.so: the Clebsch-Gordan tensor-product (CGTP)
  * convolution, forward (fp32, and fp64 for l <= 4) and gradients (fp32, l <= 4), for
- * AMD Instinct MI355X (gfx950).
+ * AMD Instinct MI355X (gfx950); and operators that train a network around it (layer and
+ * irreps normalisation, AdamW), at the end of this file.
  *
  * What is computed (the pages print no formula; this is the textbook definition that
  * LunaTP's abstract says its kernels preserve):
@@ -71,7 +72,8 @@ enum {
   CGTP_ERR_CAPACITY = -4,     /* edge list longer than the caller's capacity */
   CGTP_ERR_WORKSPACE = -5,    /* workspace smaller than the size query returned */
   CGTP_ERR_HIP = -6,          /* a HIP runtime call failed */
-  CGTP_ERR_NO_DEVICE = -7     /* no usable gfx950 device */
+  CGTP_ERR_NO_DEVICE = -7,    /* no usable gfx950 device */
+  CGTP_ERR_NO_MEMORY = -8     /* a host allocation of a create call failed */
 };
 
 enum { CGTP_PATHS_ALL = 0, CGTP_PATHS_PARITY = 1 };
@@ -259,6 +261,135 @@ int cgtp_conv_backward(cgtp_plan_t plan, const float* pos, int64_t n_nodes, cons
                        int64_t n_edges, const float* x, const float* w, const uint8_t* mask,
                        const float* gate, const float* grad_out, float* grad_x, float* grad_w,
                        float* grad_pos, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- Training operators ---------------------------------------------------------
+ *
+ * What a network around the convolution needs besides it: normalisation of rows (a
+ * radial network's hidden rows, per-edge weights) and of irreps features (what goes into
+ * and comes out of the convolution), and the optimiser step that applies the gradients.
+ * The interface is this library's own; the pages define no such calls (LunaTP, Abstract,
+ * names training of whole potentials as the use).  Ownership, asynchrony and errors as
+ * above: the library allocates nothing in them and keeps no pointer after a call returns.
+ *
+ * Element types of rows, parameters and gradients.  Everything is computed in fp32 and
+ * rounded to nearest even where it is stored; sums, statistics and 32-bit states are
+ * fp32 (the gradient norm fp64) whatever the element type.  Infinities and NaN go where
+ * the formulas take them, unless stated. */
+enum { CGTP_F32 = 0, CGTP_BF16 = 1, CGTP_F16 = 2 };
+
+/* Layer normalisation of each row x[r, 0..width):
+ *   mu = sum(x)/width, s2 = sum((x - mu)^2)/width, rstd = 1/sqrt(s2 + eps),
+ *   y = (x - mu) rstd weight + bias
+ * x and y are device arrays of type dtype whose rows lie ld_x / ld_y elements apart (>=
+ * width) and hold consecutive elements; they need the alignment of one element only and
+ * may not overlap.  weight and bias [width] (each may be NULL: 1, 0) are of type
+ * weight_dtype, CGTP_F32 or dtype.  stats [2, n_rows] fp32 (may be NULL) receives mu and
+ * rstd, which the backward reads.  n_rows may be 0; a row of one element gives y = bias.
+ * Asynchronous on `stream`; bitwise reproducible. */
+int cgtp_layer_norm_forward(int dtype, int64_t n_rows, int64_t width, const void* x, int64_t ld_x, int weight_dtype,
+                            const void* weight, const void* bias, double eps, void* y, int64_t ld_y, float* stats,
+                            void* stream);
+
+/* Workspace bytes that cgtp_layer_norm_backward needs when it writes grad_weight or
+ * grad_bias. */
+int cgtp_layer_norm_backward_workspace_size(int64_t n_rows, int64_t width, size_t* bytes);
+
+/* Gradients of a scalar L of the layer norm's output, given grad_out = dL/dy (rows ld_g
+ * elements apart) and the forward's x and stats.  With h = (x - mu) rstd, a = grad_out
+ * weight:
+ *   grad_x = rstd (a - sum(a)/width - h sum(a h)/width)        rows ld_gx elements apart
+ *   grad_weight[c] = sum over rows of grad_out h, grad_bias[c] = sum over rows of grad_out
+ * Each output may be NULL to skip it, and is overwritten; grad_weight and grad_bias are of
+ * type weight_dtype (with n_rows = 0 they are 0).  workspace: 256-byte aligned, not needed
+ * (NULL) when both are NULL.  No atomics: bitwise reproducible. */
+int cgtp_layer_norm_backward(int dtype, int64_t n_rows, int64_t width, const void* grad_out, int64_t ld_g,
+                             const void* x, int64_t ld_x, const float* stats, int weight_dtype, const void* weight,
+                             void* grad_x, int64_t ld_gx, void* grad_weight, void* grad_bias, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/* The equivariant layer norm of irreps rows: each term "mul x l p" of `irreps` is
+ * normalised by itself.  A 0e term is layer-normalised as above, with a weight and a bias
+ * per channel.  Any other term's block [mul][2l+1] has no mean taken off and no bias (both
+ * would break equivariance under rotation, or under inversion for 0o): with
+ *   s2 = sum(x^2) / (mul (2l+1)), rstd = 1/sqrt(s2 + eps),  y[u, m] = x[u, m] rstd weight[u].
+ * The plan holds host memory only and belongs to no device; it may be shared by threads
+ * and streams.  At most 64 terms, l <= 6. */
+typedef struct cgtp_norm_s* cgtp_norm_t;
+int cgtp_norm_create(const char* irreps, cgtp_norm_t* out);
+
+/* Row width, number of weights (all channels, in term order), of biases (channels of the
+ * 0e terms, in term order) and of terms.  Any output pointer may be NULL. */
+int cgtp_norm_info(cgtp_norm_t plan, int64_t* n_features, int64_t* n_weights, int64_t* n_biases, int* n_terms);
+void cgtp_norm_destroy(cgtp_norm_t plan);
+
+/* Forward and backward over rows of n_features elements; arguments as the layer norm's,
+ * with weight [n_weights], bias [n_biases] and stats [2, n_rows, n_terms]. */
+int cgtp_irreps_norm_forward(cgtp_norm_t plan, int dtype, int64_t n_rows, const void* x, int64_t ld_x,
+                             int weight_dtype, const void* weight, const void* bias, double eps, void* y, int64_t ld_y,
+                             float* stats, void* stream);
+int cgtp_irreps_norm_backward_workspace_size(cgtp_norm_t plan, int64_t n_rows, size_t* bytes);
+int cgtp_irreps_norm_backward(cgtp_norm_t plan, int dtype, int64_t n_rows, const void* grad_out, int64_t ld_g,
+                              const void* x, int64_t ld_x, const float* stats, int weight_dtype, const void* weight,
+                              void* grad_x, int64_t ld_gx, void* grad_weight, void* grad_bias, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/* A set of n_tensors tensors (numel[t] >= 0 elements each, dense) that one optimiser step
+ * covers, with a weight decay each (NULL: 0).  It holds their sizes, on the host and in a
+ * small table on the current device, and no pointer to them.  Optimiser states of the whole
+ * set are flat arrays of state_elems elements: tensor t's begin at offsets[t], a multiple
+ * of 64.  flags: 0, or CGTP_PLAN_HOST_ONLY (sizes only, no device).  May be shared by
+ * threads and streams; freed by cgtp_params_destroy (NULL is ignored). */
+typedef struct cgtp_params_s* cgtp_params_t;
+int cgtp_params_create(const int64_t* numel, const double* weight_decay, int n_tensors, unsigned flags,
+                       cgtp_params_t* out);
+int cgtp_params_info(cgtp_params_t set, int* n_tensors, int64_t* state_elems, int64_t* offsets);
+void cgtp_params_destroy(cgtp_params_t set);
+
+/* One AdamW step over the set, in place.  params and grads are host arrays of n_tensors
+ * device pointers (read before the call returns; entries of empty tensors may be NULL) of
+ * types param_dtype and grad_dtype, aligned to one element; m and v [state_elems] fp32,
+ * 16-byte aligned, zero before the first step.  step counts from 1:
+ *   g = grad grad_scale[0];  p <- p (1 - lr decay);  m <- beta1 m + (1 - beta1) g;
+ *   v <- beta2 v + (1 - beta2) g^2;
+ *   p <- p - (lr / (1 - beta1^step)) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * grad_scale (device fp32, NULL = 1): the inverse of a loss scale, or the factor that
+ * cgtp_grad_norm writes; where it is NaN the whole step is skipped, params and states
+ * untouched.  Asynchronous on `stream`; bitwise reproducible.  The scalars travel in the
+ * launch: a captured graph repeats the step number it was captured with. */
+int cgtp_adamw_step(cgtp_params_t set, int param_dtype, void* const* params, int grad_dtype, const void* const* grads,
+                    float* m, float* v, double lr, double beta1, double beta2, double eps, int64_t step,
+                    const float* grad_scale, void* stream);
+
+/* The same step with the states in 8 bits: codes of m and of r = sqrt(v) [state_elems each,
+ * 16-byte aligned] and one exponent byte per block of 64 elements [state_elems / 64 each];
+ * all zero bytes before the first step.  With E a block's exponent byte (the biased fp32
+ * exponent of its largest magnitude), a code is the top of the fp32 number |value| 2^(14 -
+ * max(E, 1)): for m a sign bit, 4 exponent and 3 mantissa bits, for r 4 exponent and 4
+ * mantissa bits.  The rest is rounded up or down at random in proportion, by 16 bits of a
+ * hash of the element's place and `seed` (give every step another one; the step number
+ * serves), so that moments keep their mean although a step moves them by less than a
+ * code's distance; equal seeds give equal results bit for bit.  A positive r is stored as
+ * code 1 at least; a moment that is not finite is stored as NaN and does not disturb its
+ * block.  p is updated from the moments before they are rounded. */
+int cgtp_adamw_step_8bit(cgtp_params_t set, int param_dtype, void* const* params, int grad_dtype,
+                         const void* const* grads, uint8_t* m_code, uint8_t* r_code, uint8_t* m_exp, uint8_t* r_exp,
+                         double lr, double beta1, double beta2, double eps, int64_t step, uint32_t seed,
+                         const float* grad_scale, void* stream);
+
+/* The values that 8-bit states stand for, m and r [state_elems] in bf16 (which holds them
+ * exactly), 16-byte aligned: for checkpoints and inspection. */
+int cgtp_adamw_read_8bit(cgtp_params_t set, const uint8_t* m_code, const uint8_t* r_code, const uint8_t* m_exp,
+                         const uint8_t* r_exp, void* m, void* r, void* stream);
+
+/* The 2-norm of all gradients of the set and the factor that clips them, on the device:
+ *   out[0] = |grad_scale[0]| sqrt(sum of grad^2);
+ *   out[1] = grad_scale[0] min(1, max_norm / out[0]), the grad_scale of an AdamW step;
+ * NaN where out[0] is not finite, so that the step is skipped.  max_norm > 0 (infinity:
+ * no clipping).  Squares and sums in fp64, in a fixed order.  workspace: 256-byte
+ * aligned, cgtp_grad_norm_workspace_size bytes. */
+int cgtp_grad_norm_workspace_size(cgtp_params_t set, size_t* bytes);
+int cgtp_grad_norm(cgtp_params_t set, int grad_dtype, const void* const* grads, const float* grad_scale,
+                   double max_norm, float* out, void* workspace, size_t ws_bytes, void* stream);
 
 /* Frees the plan's device tables, streams and events (interface bookkeeping; the pages
  * define no such call).  NULL is ignored. */

@@ -1,0 +1,518 @@
+"""GPU checks of the training operators against their fp64 references.
+
+Tolerances (u = 2^-24, the fp32 rounding unit).  Inputs are rows of spread 0.5 to 1.5
+around an offset of at most 4, |x| < 10, and weights below 2.
+  forward: x - mu carries the mean's error, some 10 u of |x| (partial sums of a thread and
+    a tree), and its own rounding; rstd (at most 1/0.4) some 30 u: 10 * 10 u * 2.5 + 30 u * 6
+    below 3e-5 for |h| < 6; times the weight.  fp32 is held to 5e-5 absolute.
+  grad_x: the same terms with two sums more: 1e-4 absolute, |grad_x| being of order 1 to 10.
+  grad_weight, grad_bias: partial sums of at most 100 terms in a chain and a tree: 100 u of
+    the sum of the terms' magnitudes, and h's error (3e-5 / 6 relative at most) of it.
+  bf16 and fp16 outputs: the nearest value of the type to a number within these bounds.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import train_oracle as T
+
+C = pytest.importorskip("clebsch_gordan_tensor_node_amd")
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+SPECS = [1, 2, 5, 16, 63, 64, 65, 128, 129, 480, 1312, 2048, 2049, 8192, 8193, 32768, 40001,
+         "16x0e+8x1e+16x1o", "1x0e", "1x0o+1x1o+1x6e", "128x0e+64x1o+32x2e+32x3o", "640x0e+1024x1o+1280x2e",
+         "5x0e+3x0o+7x4e+2x0e", "+".join(["3x0e+1x1o"] * 32)]
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a device"
+    return torch.device("cuda:0")
+
+
+def _rows(rng, n, f, dtype, dev, pad=0, first=0):
+    """[n, f] rows inside rows `pad` wider, from column `first`; and their values in fp64."""
+    v = rng.normal(size=(n, f)).clip(-4, 4) * rng.uniform(0.5, 1.5, size=(n, 1)) + rng.uniform(-3, 3, size=(n, 1))
+    wide = torch.full((n, f + pad), float("nan"), dtype=dtype, device=dev)
+    t = wide[:, first:first + f]
+    t.copy_(torch.from_numpy(v))
+    return t, t.double().cpu().numpy()
+
+
+def _weights(rng, n, dtype, dev):
+    t = torch.from_numpy(1 + 0.3 * rng.normal(size=n).clip(-3, 3)).to(dtype).to(dev)
+    return t, t.double().cpu().numpy()
+
+
+def _call(spec, x, w, b, eps=1e-5, **kw):
+    if isinstance(spec, int):
+        y, st = C.layer_norm_forward(x, w, b, eps, **kw)
+        return y, st.view(2, x.shape[0], 1)
+    return C.irreps_norm_forward(C.NormPlan(spec), x, w, b, eps, **kw)
+
+
+def _grads(spec, g, x, st, w, **kw):
+    if isinstance(spec, int):
+        return C.layer_norm_backward(g, x, st.view(2, x.shape[0]), w, **kw)
+    return C.irreps_norm_backward(C.NormPlan(spec), g, x, st, w, **kw)
+
+
+def _shape(spec):
+    t = T.row_terms(spec) if isinstance(spec, int) else T.norm_terms(spec)
+    return (t, sum(m * d for _, m, d, _, _ in t), sum(m for _, m, _, _, _ in t),
+            sum(m for _, m, _, _, b in t if b is not None))
+
+
+def _near(got, ref, tol, what):
+    """got is within tol of ref, or in 16 bits the rounding of a number that is."""
+    assert tuple(got.shape) == ref.shape, (what, got.shape, ref.shape)
+    lo, hi = (torch.from_numpy(np.asarray(v)) for v in (ref - tol, ref + tol))
+    if got.dtype != torch.float32:
+        lo, hi = lo.to(got.dtype).double(), hi.to(got.dtype).double()
+    v = got.double().cpu()
+    assert v.isfinite().all() and ((lo <= v) & (v <= hi)).all(), (what, float((v - torch.from_numpy(ref)).abs().max()))
+
+
+def _check(spec, rows, dtype, wdtype, dev, pad=0, first=0, seed=0):
+    rng = np.random.default_rng(seed)
+    terms, f, nw, nb = _shape(spec)
+    x, xr = _rows(rng, rows, f, dtype, dev, pad, first)
+    (w, wr), (b, br) = _weights(rng, nw, wdtype, dev), _weights(rng, nb, wdtype, dev)
+    y, st = _call(spec, x, w, b)
+    ry, rm, rr = T.norm_forward(xr, terms, wr, br)
+    scale = max(1.0, np.abs(rr).max(initial=0) / 2.5)   # a row of one or two values may have a large rstd
+    _near(y, ry, 5e-5 * scale, "y")
+    _near(st[0], rm, 100 * U, "mean")
+    _near(st[1], rr, (60 * U + 2e-5 * scale) * rr, "rstd")
+    g, gr = _rows(rng, rows, f, dtype, dev, pad, 0)
+    gx, gw, gb = _grads(spec, g, x, st, w)
+    rx, rw, rb = T.norm_backward(gr, xr, terms, wr)
+    _near(gx, rx, 1e-4 * scale ** 2, "grad_x")
+    aw, ab = np.zeros(nw), np.zeros(nb)
+    for k, (off, m, d, w0, b0) in enumerate(terms):
+        q = np.abs(gr[:, off:off + m * d]).reshape(rows, m, d)
+        h = np.abs((xr[:, off:off + m * d].reshape(rows, m, d) - rm[:, k, None, None]) * rr[:, k, None, None])
+        aw[w0:w0 + m] = (q * (h + 1)).sum(axis=(0, 2))
+        if b0 is not None:
+            ab[b0:b0 + m] = q.sum(axis=(0, 2))
+    _near(gw, rw, (100 * U + 2e-5) * aw * scale, "grad_weight")
+    _near(gb, rb, 100 * U * ab, "grad_bias")
+    return x, g, w, b, y, st, (gx, gw, gb)
+
+
+@pytest.mark.parametrize("spec", SPECS, ids=lambda s: str(s)[:30])
+def test_norm_widths(spec, dev):
+    _check(spec, 7, torch.float32, torch.float32, dev)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("spec", [5, 64, 129, 1312, 4097, 20000, "128x0e+64x1o+32x2e+32x3o", "5x0e+3x0o+7x4e+2x0e"],
+                         ids=str)
+def test_norm_types(spec, dtype, dev):
+    _check(spec, 9, dtype, torch.float32, dev)
+    _check(spec, 9, dtype, dtype, dev, pad=3, first=1)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 31, 257, 4000])
+@pytest.mark.parametrize("spec", [16, 77, 480, "16x0e+8x1e+16x1o"], ids=str)
+def test_norm_row_counts(spec, rows, dev):
+    _check(spec, rows, torch.float32, torch.float32, dev)
+
+
+@pytest.mark.parametrize("pad,first", [(1, 0), (1, 1), (7, 3), (64, 32)])
+@pytest.mark.parametrize("spec", [64, 65, 1312, "128x0e+64x1o+32x2e+32x3o"], ids=str)
+def test_norm_strides(spec, pad, first, dev):
+    # rows inside wider ones, starting anywhere: what lies beside them (NaN) is not read into
+    # the result and the output's neighbours are not written
+    for dtype in (torch.float32, torch.bfloat16):
+        x, g, w, b, y, st, _ = _check(spec, 33, dtype, torch.float32, dev, pad, first)
+        f = x.shape[1]
+        wide = torch.full((33, f + pad), 7.0, dtype=dtype, device=dev)
+        out, _ = _call(spec, x, w, b, out=wide[:, first:first + f])
+        assert torch.equal(out, y)
+        assert (wide[:, :first] == 7).all() and (wide[:, first + f:] == 7).all()
+
+
+def test_norm_optional_arguments(dev):
+    for spec in (65, "5x0e+3x1o"):
+        rng = np.random.default_rng(1)
+        terms, f, nw, nb = _shape(spec)
+        x, xr = _rows(rng, 12, f, torch.float32, dev)
+        g, gr = _rows(rng, 12, f, torch.float32, dev)
+        y, st = _call(spec, x, None, None)
+        _near(y, T.norm_forward(xr, terms)[0], 5e-5, "y")
+        rx, rw, rb = T.norm_backward(gr, xr, terms)
+        full = _grads(spec, g, x, st, None)
+        for got, ref in zip(full, (rx, rw, rb)):
+            _near(got, ref, 5e-4, "gradient")
+        for need in ((), ("x",), ("weight",), ("bias",), ("x", "bias"), ("weight", "bias")):
+            some = _grads(spec, g, x, st, None, need=need)
+            for name, a, c in zip(("x", "weight", "bias"), some, full):
+                assert (a is None) == (name not in need) and (a is None or torch.equal(a, c))
+
+
+def test_norm_empty(dev):
+    for spec in (8, "5x0e+3x1o"):
+        terms, f, nw, nb = _shape(spec)
+        x = torch.empty(0, f, device=dev)
+        y, st = _call(spec, x, None, None)
+        assert y.shape == (0, f) and st.shape == (2, 0, len(terms))
+        gx, gw, gb = _grads(spec, x, x, st, None)
+        assert gx.shape == (0, f) and (gw == 0).all() and (gb == 0).all() and gw.shape == (nw,) and gb.shape == (nb,)
+
+
+def test_norm_rows_that_are_constant_or_not_finite(dev):
+    # a constant row is its bias; a row that holds NaN or infinity is NaN throughout and no
+    # other row changes
+    for f in (16, 100, 1312, 5000, 40000):
+        rng = np.random.default_rng(2)
+        x, _ = _rows(rng, 40, f, torch.float32, dev)
+        b = torch.linspace(-1, 1, f, device=dev)
+        clean, _ = C.layer_norm_forward(x, None, b)
+        x[3], x[4] = 2.5, 0.0
+        x[7, f // 2], x[9, 1] = float("nan"), float("inf")
+        y, st = C.layer_norm_forward(x, None, b)
+        assert torch.equal(y[4], b) and (y[3] - b).abs().max() < 1e-3   # 2.5's mean may miss by some u of 2.5, times 1/sqrt(eps)
+        assert y[7].isnan().all() and y[9].isnan().all()
+        keep = [r for r in range(40) if r not in (3, 4, 7, 9)]
+        assert torch.equal(y[keep], clean[keep])
+        g, _ = _rows(rng, 40, f, torch.float32, dev)
+        gx, gw, gb = C.layer_norm_backward(g, x, st)
+        assert gx[7].isnan().all() and gx[keep].isfinite().all() and gb.isfinite().all()
+
+
+def test_norm_gradient_by_differences(dev):
+    for spec in (48, "16x0e+8x1e+16x1o"):
+        rng = np.random.default_rng(3)
+        terms, f, nw, nb = _shape(spec)
+        x, xr = _rows(rng, 20, f, torch.float32, dev)
+        g, gr = _rows(rng, 20, f, torch.float32, dev)
+        (w, wr), (b, br) = _weights(rng, nw, torch.float32, dev), _weights(rng, nb, torch.float32, dev)
+        _, st = _call(spec, x, w, b)
+        gx, gw, gb = (t.double().cpu().numpy() for t in _grads(spec, g, x, st, w))
+        loss = lambda x, w, b: (T.norm_forward(x, terms, w, b)[0] * gr).sum()  # noqa: E731
+        h = 1e-5
+        dx, dw, db = rng.normal(size=xr.shape), rng.normal(size=nw), rng.normal(size=nb)
+        for got, lo, hi in (((gx * dx).sum(), (xr - h * dx, wr, br), (xr + h * dx, wr, br)),
+                            ((gw * dw).sum(), (xr, wr - h * dw, br), (xr, wr + h * dw, br)),
+                            ((gb * db).sum(), (xr, wr, br - h * db), (xr, wr, br + h * db))):
+            # the sum of up to 1000 gradients each within 1e-4, and the differences' own error
+            assert abs(got - (loss(*hi) - loss(*lo)) / (2 * h)) < 1e-4 * 1000 ** 0.5 + 1e-5 * abs(got)
+
+
+def test_norm_repeats_bitwise_on_another_stream(dev):
+    rng = np.random.default_rng(4)
+    x, _ = _rows(rng, 3000, 480, torch.float32, dev)
+    g, _ = _rows(rng, 3000, 480, torch.float32, dev)
+    y, st = C.layer_norm_forward(x)
+    first = (y, *C.layer_norm_backward(g, x, st))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y2, st2 = C.layer_norm_forward(x)
+        again = (y2, *C.layer_norm_backward(g, x, st2))
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, c) for a, c in zip(first, again))
+
+
+def test_norm_offsets_past_32_bits(dev):
+    # rows 2^21 elements apart: the last row's offset is above 2^32 elements
+    rows, ld, f = 2100, 1 << 21, 100
+    rng = np.random.default_rng(5)
+    buf = torch.empty(rows * ld, dtype=torch.bfloat16, device=dev)
+    x = buf.view(rows, ld)[:, :f]
+    v = torch.from_numpy(rng.normal(size=(rows, f))).to(torch.bfloat16).to(dev)
+    x.copy_(v)
+    y, st = C.layer_norm_forward(x)
+    dense, st2 = C.layer_norm_forward(v)
+    assert torch.equal(y, dense) and torch.equal(st, st2)
+    got, ref = C.layer_norm_backward(x, x, st), C.layer_norm_backward(v, v, st)
+    assert all(torch.equal(a, c) for a, c in zip(got, ref))
+
+
+def test_norm_in_a_graph(dev):
+    rng = np.random.default_rng(6)
+    x, _ = _rows(rng, 100, 96, torch.float32, dev)
+    g, _ = _rows(rng, 100, 96, torch.float32, dev)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    C.layer_norm_backward(g, x, C.layer_norm_forward(x)[1], workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, st = C.layer_norm_forward(x)
+        grads = C.layer_norm_backward(g, x, st, workspace=ws)
+    for _ in range(4):
+        x.copy_(_rows(rng, 100, 96, torch.float32, dev)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        want, st2 = C.layer_norm_forward(x)
+        assert torch.equal(y, want)
+        assert all(torch.equal(a, c) for a, c in zip(grads, C.layer_norm_backward(g, x, st2)))
+
+
+def test_norm_argument_checks(dev):
+    x = torch.zeros(4, 8, device=dev)
+    st = torch.zeros(2, 4, device=dev)
+    bad = [lambda: C.layer_norm_forward(x.double()), lambda: C.layer_norm_forward(x, torch.zeros(8, device=dev).half()),
+           lambda: C.layer_norm_forward(x, torch.zeros(8)), lambda: C.layer_norm_forward(x, out=x.bfloat16()),
+           lambda: C.layer_norm_backward(x.bfloat16(), x, st), lambda: C.layer_norm_backward(x, x, st.double())]
+    for f in bad:
+        with pytest.raises(TypeError):
+            f()
+    bad = [lambda: C.layer_norm_forward(x, torch.zeros(7, device=dev)), lambda: C.layer_norm_forward(x.view(2, 2, 8)),
+           lambda: C.layer_norm_forward(x.t()), lambda: C.layer_norm_forward(x[:1].expand(4, 8)),
+           lambda: C.layer_norm_forward(x, out=x[:2]), lambda: C.layer_norm_backward(x[:2], x, st),
+           lambda: C.layer_norm_backward(x, x, st.t()), lambda: C.irreps_norm_forward(C.NormPlan("9x0e"), x)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(C.CgtpError) as e:
+        C.layer_norm_forward(x, eps=-1.0)
+    assert e.value.code == -1
+    with pytest.raises(C.CgtpError) as e:
+        C.layer_norm_backward(x, x, st, workspace=torch.empty(0, dtype=torch.uint8, device=dev))
+    assert e.value.code == -5
+
+
+# ---- AdamW ---------------------------------------------------------------------------
+
+SIZES = [[1], [63, 64, 65], [0, 5, 0, 128, 0], [4095, 4096, 4097, 3], [100000, 1, 17, 8191],
+         [(37 * k) % 90 for k in range(500)]]
+HYPER = dict(lr=0.02, betas=(0.9, 0.99), eps=1e-6)
+
+
+def _tensors(rng, sizes, dtype, dev, scale=1.0, skip=0):
+    """Tensors that start `skip` elements into their storage."""
+    out = []
+    for n in sizes:
+        t = torch.empty(n + skip, dtype=dtype, device=dev)[skip:]
+        out.append(t.copy_(torch.from_numpy(scale * rng.normal(size=n))))
+    return out
+
+
+def _flat(s, tensors):
+    """The tensors' values at their places among the states (0 between them), fp32."""
+    v = np.zeros(s.state_elems, dtype=np.float32)
+    for t, o in zip(tensors, s.offsets):
+        v[o:o + t.numel()] = t.float().cpu().numpy()
+    return v
+
+
+def _split(s, v):
+    return [v[o:o + n] for n, o in zip(s.sizes, s.offsets)]
+
+
+def _bits(t):
+    return np.ascontiguousarray(t.detach().cpu().numpy()).view(np.uint8)
+
+
+@pytest.mark.parametrize("pt,gt,skip", [(torch.float32, torch.float32, 0), (torch.float32, torch.bfloat16, 1),
+                                        (torch.bfloat16, torch.bfloat16, 0), (torch.float16, torch.float16, 3),
+                                        (torch.bfloat16, torch.float32, 1)])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: str(len(s)))
+def test_adamw_steps_bitwise(sizes, bits, pt, gt, skip, dev):
+    """Three steps from zero states equal the documented fp32 operations bit for bit: params,
+    moments, codes and exponents."""
+    rng = np.random.default_rng(sum(sizes))
+    decay = [0.0 if k % 2 else 0.03 for k in range(len(sizes))]
+    s = C.ParamSet(sizes, decay)
+    p = _tensors(rng, sizes, pt, dev, skip=skip)
+    state = C.adamw_state(s, bits)
+    n = s.state_elems
+    pr, dr = _flat(s, p), np.repeat(0.0, n)
+    for o, c, d in zip(s.offsets, sizes, decay):
+        dr[o:o + c] = d
+    m, v = np.zeros(n, np.float32), np.zeros(n, np.float32)
+    codes = [np.zeros(k, np.uint8) for k in (n, n, n // 64, n // 64)]
+    kept = {d: np.float32(1 - HYPER["lr"] * d) for d in (0.0, 0.03)}
+    scale = torch.tensor([0.25], device=dev)
+    inside = np.zeros(n, bool)
+    for o, c in zip(s.offsets, sizes):
+        inside[o:o + c] = True
+    for t in (1, 2, 3):
+        g = _tensors(rng, sizes, gt, dev, scale=10.0 ** rng.uniform(-4, 1), skip=skip)
+        C.adamw_step(s, p, g, state, step=t, grad_scale=scale, seed=77 * t, **HYPER)
+        if bits == 8:
+            m, v = T.decode(codes[0], codes[2], True).astype(np.float32), T.decode(codes[1], codes[3], False).astype(np.float32)
+            v = v * v
+        base = pr * np.where(dr > 0, kept[0.03], kept[0.0]).astype(np.float32)
+        q, m, v, root = T.adamw_f32(base, _flat(s, g), m, v, HYPER["lr"], *HYPER["betas"], HYPER["eps"], t, 0.0, 0.25)
+        q = np.where(inside, q, 0).astype(np.float32)
+        if bits == 8:
+            h = T.random_bits(np.arange(n), 77 * t)
+            (codes[0], codes[2]), (codes[1], codes[3]) = T.encode(m, h & 0xffff, True), T.encode(root, h >> 16, False)
+        pr = torch.from_numpy(q).to(pt).float().numpy()
+        for a, b in zip(p, _split(s, pr)):
+            assert np.array_equal(a.float().cpu().numpy(), b), (t, np.abs(a.float().cpu().numpy() - b).max())
+        if bits == 32:
+            assert np.array_equal(state[0].cpu().numpy(), m) and np.array_equal(state[1].cpu().numpy(), v)
+        else:
+            for name, a, b in zip(("m", "r", "m exponents", "r exponents"), state, codes):
+                assert np.array_equal(a.cpu().numpy(), b), (t, name, (a.cpu().numpy() != b).sum())
+            vm, vr = C.adamw_moments(s, state)
+            assert np.array_equal(vm.double().cpu().numpy(), T.decode(codes[0], codes[2], True))
+            assert np.array_equal(vr.double().cpu().numpy(), T.decode(codes[1], codes[3], False))
+
+
+def test_adamw_against_64_bits(dev):
+    rng = np.random.default_rng(8)
+    sizes = [5000, 77]
+    s = C.ParamSet(sizes, 0.1)
+    p, state = _tensors(rng, sizes, torch.float32, dev), C.adamw_state(s)
+    pr, m, v = _flat(s, p).astype(np.float64), 0.0, 0.0
+    for t in range(1, 21):
+        g = _tensors(rng, sizes, torch.float32, dev, scale=1e-3)
+        C.adamw_step(s, p, g, state, lr=1e-2, step=t)
+        pr, m, v = T.adamw(pr, _flat(s, g), m, v, 1e-2, 0.9, 0.999, 1e-8, t, 0.1)
+    # 20 steps, each a rounding of p (|p| < 5) and of an update of at most 0.1 by some 10 u
+    assert np.abs(_flat(s, p) - pr).max() < 20 * (5 * U * 2 + 0.1 * 20 * U)
+
+
+def test_adamw8_follows_adamw32(dev):
+    # the same gradients with both states: the 8-bit run's path stays near the 32-bit one's, in
+    # both directions of the second moment (the gradients shrink a hundredfold half-way)
+    rng = np.random.default_rng(9)
+    s = C.ParamSet([20000])
+    p32, p8 = [torch.zeros(20000, device=dev)], [torch.zeros(20000, device=dev)]
+    st32, st8 = C.adamw_state(s), C.adamw_state(s, 8)
+    sign = torch.from_numpy(np.where(rng.random(20000) < 0.5, -1.0, 1.0)).float().to(dev)
+    size = torch.from_numpy(10.0 ** rng.uniform(-2, 0, 20000)).float().to(dev)
+    for t in range(1, 601):
+        g = [(sign + torch.from_numpy(rng.normal(size=20000)).float().to(dev)) * size * (1.0 if t <= 300 else 0.01)]
+        C.adamw_step(s, p32, g, st32, lr=1e-3, betas=(0.9, 0.99), step=t)
+        C.adamw_step(s, p8, g, st8, lr=1e-3, betas=(0.9, 0.99), step=t, seed=t)
+    # a code's distance is 2^-3 of m and 2^-4 of r; held over 1/(1 - b) steps the roundings'
+    # deviations stay below one distance, so single updates differ by a quarter and, being
+    # unbiased, their sum over hundreds of steps by far less
+    rel = (p8[0] - p32[0]).norm() / p32[0].norm()
+    assert rel < 0.1, rel
+    _, r = C.adamw_moments(s, st8)
+    r32 = st32[1].sqrt()
+    assert abs((r.float()[:20000] / r32[:20000]).mean() - 1) < 0.05
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_skips_on_nan_scale_and_contains_bad_gradients(bits, dev):
+    rng = np.random.default_rng(10)
+    sizes = [300, 70]
+    s = C.ParamSet(sizes, 0.1)
+    p, g, state = _tensors(rng, sizes, torch.float32, dev), _tensors(rng, sizes, torch.float32, dev), C.adamw_state(s, bits)
+    C.adamw_step(s, p, g, state, lr=1e-2, step=1)
+    before = [t.clone() for t in (*p, *state)]
+    C.adamw_step(s, p, g, state, lr=1e-2, step=2, grad_scale=torch.tensor([float("nan")], device=dev))
+    assert all(torch.equal(a, b) for a, b in zip(before, (*p, *state)))
+    g[0][10], g[0][100], g[1][69] = float("nan"), float("inf"), -float("inf")
+    clean = [t.clone() for t in (*p, *state)]
+    g2 = [torch.nan_to_num(t, 0.0, 0.0, 0.0) for t in g]
+    C.adamw_step(s, clean[:2], g2, tuple(clean[2:]), lr=1e-2, step=2)
+    C.adamw_step(s, p, g, state, lr=1e-2, step=2)
+    hit = torch.zeros(300, dtype=torch.bool, device=dev)
+    hit[[10, 100]] = True
+    assert p[0][hit].isnan().all() and torch.equal(p[0][~hit], clean[0][~hit])
+    assert p[1][69].isnan() and torch.equal(p[1][:69], clean[1][:69])
+    if bits == 8:
+        m, r = C.adamw_moments(s, state)
+        assert m[10].isnan() and r[10].isnan() and m[100].isnan() and r[100].isnan()
+        assert m.isnan().sum() == 3 and r.isnan().sum() == 3
+
+
+def test_adamw_repeats_bitwise_and_in_a_graph(dev):
+    rng = np.random.default_rng(11)
+    sizes = [5000, 33, 700]
+    s = C.ParamSet(sizes)
+    g = s.pointers(_tensors(rng, sizes, torch.float32, dev))
+    start = _tensors(rng, sizes, torch.float32, dev)
+
+    def fresh():
+        return [t.clone() for t in start], C.adamw_state(s, 8)
+
+    def step(p, st):
+        f = C.grad_norm(s, g, 1.0)
+        C.adamw_step(s, p, g, st, lr=1e-2, step=3, grad_scale=f[1:], seed=5)
+        return f
+
+    p, st = fresh()
+    for _ in range(3):
+        norm = step(p, st)
+    q, su = fresh()
+    step(*fresh())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm2 = step(q, su)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((*p, *st, norm), (*q, *su, norm2)))
+
+
+def test_adamw_tensor_past_32_bits(dev):
+    # one tensor of 2^32 + 1000 elements in bf16 with 8-bit states: its last elements move as
+    # those of a small one at the same places, and the first ones too
+    n = (1 << 32) + 1000
+    s = C.ParamSet([n])
+    p, g = [torch.ones(n, dtype=torch.bfloat16, device=dev)], [torch.zeros(n, dtype=torch.bfloat16, device=dev)]
+    g[0][-500:], g[0][:500] = 1.0, -1.0
+    state = C.adamw_state(s, 8)
+    C.adamw_step(s, p, g, state, lr=0.25, step=1)
+    assert (p[0][-500:] == 0.75).all() and (p[0][:500] == 1.25).all() and (p[0][500:-500] == 1).all()
+    f = C.grad_norm(s, g)
+    assert abs(float(f[0]) - 1000 ** 0.5) < 1e-4 and float(f[1]) == 1.0
+
+
+@pytest.mark.parametrize("gt", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: str(len(s)))
+def test_grad_norm(sizes, gt, dev):
+    rng = np.random.default_rng(12)
+    s = C.ParamSet(sizes)
+    g = _tensors(rng, sizes, gt, dev, skip=1)
+    scale = torch.tensor([0.5], device=dev)
+    for most in (float("inf"), 1e-2, 1e9):
+        norm, factor = T.grad_norm([t.double().cpu().numpy() for t in g], 0.5, most)
+        got = C.grad_norm(s, g, most, grad_scale=scale).double().cpu().numpy()
+        assert abs(got[0] - norm) <= 2 * U * norm and abs(got[1] - factor) <= 4 * U * factor
+
+
+def test_grad_norm_extremes(dev):
+    s = C.ParamSet([100, 50])
+    zero = [torch.zeros(100, device=dev), torch.zeros(50, device=dev)]
+    assert C.grad_norm(s, zero, 1.0).tolist() == [0.0, 1.0]
+    huge = [torch.full((100,), 1e30, device=dev), zero[1]]
+    got = C.grad_norm(s, huge, 1.0).tolist()
+    assert abs(got[0] / 1e31 - 1) < 1e-6 and abs(got[1] / 1e-31 - 1) < 1e-6
+    tiny = [torch.full((100,), 1e-30, device=dev), zero[1]]
+    assert abs(C.grad_norm(s, tiny).tolist()[0] / 1e-29 - 1) < 1e-6
+    for bad in (float("nan"), float("inf")):
+        zero[1][49] = bad
+        assert np.isnan(C.grad_norm(s, zero, 1.0).tolist()[1])
+    assert C.grad_norm(C.ParamSet([]), [], 1.0).tolist() == [0.0, 1.0]
+
+
+def test_optimiser_argument_checks(dev):
+    s = C.ParamSet([4, 6])
+    p, g, st = [torch.zeros(4, device=dev), torch.zeros(6, device=dev)], [torch.zeros(4, device=dev), torch.zeros(6, device=dev)], C.adamw_state(s)
+    for kw in (dict(lr=-1.0), dict(lr=float("nan")), dict(lr=1.0, betas=(1.0, 0.9)), dict(lr=1.0, betas=(0.9, -0.1)),
+               dict(lr=1.0, eps=-1.0), dict(lr=1.0, step=0)):
+        with pytest.raises(C.CgtpError) as e:
+            C.adamw_step(s, p, g, st, **kw)
+        assert e.value.code == -1
+    with pytest.raises(C.CgtpError):
+        C.grad_norm(s, g, max_norm=0.0)
+    with pytest.raises(C.CgtpError) as e:
+        C.grad_norm(s, g, workspace=torch.empty(0, dtype=torch.uint8, device=dev))
+    assert e.value.code == -5
+    for f in (lambda: s.pointers(p[:1]), lambda: s.pointers([p[1], p[0]]), lambda: s.pointers([p[0], torch.zeros(6, 2, device=dev)[:, 0]]),
+              lambda: C.adamw_step(s, p, g, st[:1], lr=1.0), lambda: C.adamw_step(s, p, g, (st[0], st[1][:-1]), lr=1.0)):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: s.pointers([p[0], p[1].half()]), lambda: s.pointers([p[0], p[1].cpu()]),
+              lambda: C.adamw_step(s, p, g, (st[0], st[1].double()), lr=1.0),
+              lambda: C.adamw_step(s, p, g, st, lr=1.0, grad_scale=torch.zeros(1))):
+        with pytest.raises(TypeError):
+            f()
+    assert all((t == 0).all() for t in (*p, *st))
