@@ -21,11 +21,16 @@ struct NormTerm {
   int32_t d;       // components that share a channel's weight (2l + 1)
   int32_t w_off;   // first weight
   int32_t b_off;   // first bias; -1: not centred, no bias
-  int32_t index;   // the term's column in the statistics
 };
 constexpr int kMaxNormTerms = 64;   // terms of an irreps row (they travel in the kernel arguments)
 
-struct NormArgs {
+struct NormShape {
+  int64_t features, weights, biases;
+  const NormTerm* terms;
+  int n_terms;
+};
+
+struct NormCall {
   const void* x;
   const void* weight;      // may be null (1)
   const void* bias;        // may be null (0); forward only
@@ -39,16 +44,14 @@ struct NormArgs {
   int64_t rows;
   int64_t ld_x, ld_y, ld_g;   // elements from row to row
   float eps;
-  int n_terms;
-  int n_weights, n_biases;
   int weight_f32;          // weight, bias and their gradients are fp32 (else x's type)
-  NormTerm term[kMaxNormTerms];
 };
 
-hipError_t launch_norm_forward(const NormArgs& a, Elem type, hipStream_t s);
-// Floats of partial sums that launch_norm_backward needs in a.part.
-size_t norm_part_floats(int64_t rows, int n_weights, int n_biases);
-hipError_t launch_norm_backward(const NormArgs& a, Elem type, hipStream_t s);
+hipError_t launch_norm_forward(const NormCall& c, const NormShape& p, Elem type, hipStream_t s);
+// Floats of partial sums that launch_norm_backward needs in c.part when a weight's or
+// bias's gradient is asked for.
+size_t norm_part_floats(int64_t rows, const NormShape& p);
+hipError_t launch_norm_backward(const NormCall& c, const NormShape& p, Elem type, hipStream_t s);
 
 // ---- optimiser ---------------------------------------------------------------------
 

@@ -52,13 +52,7 @@ int guarded(F&& body) {
 
 // ---- normalisation -----------------------------------------------------------------
 
-struct NormShape {
-  int64_t features, weights, biases;
-  const NormTerm* terms;
-  int n_terms;
-};
-
-int fill_norm(NormArgs& a, const NormShape& p, int dtype, int64_t rows, const void* x, int64_t ld_x, int weight_dtype,
+int fill_norm(NormCall& a, const NormShape& p, int dtype, int64_t rows, const void* x, int64_t ld_x, int weight_dtype,
               const void* weight) {
   const int es = elem_size(dtype);
   if (!es) return fail(CGTP_ERR_INVALID_ARG, "unknown element type %d", dtype);
@@ -75,11 +69,7 @@ int fill_norm(NormArgs& a, const NormShape& p, int dtype, int64_t rows, const vo
   a.ld_x = ld_x;
   a.weight = weight;
   a.rows = rows;
-  a.n_terms = p.n_terms;
-  a.n_weights = int(p.weights);
-  a.n_biases = int(p.biases);
   a.weight_f32 = weight_dtype == CGTP_F32;
-  std::memcpy(a.term, p.terms, size_t(p.n_terms) * sizeof(NormTerm));
   return CGTP_OK;
 }
 
@@ -89,11 +79,11 @@ int check_width(int64_t width) {
   return CGTP_OK;
 }
 
-NormTerm whole_row(int64_t width) { return NormTerm{0, int32_t(width), 1, 0, 0, 0}; }
+NormTerm whole_row(int64_t width) { return NormTerm{0, int32_t(width), 1, 0, 0}; }
 
 int norm_forward(const NormShape& p, int dtype, int64_t rows, const void* x, int64_t ld_x, int weight_dtype,
                  const void* weight, const void* bias, double eps, void* y, int64_t ld_y, float* stats, void* stream) {
-  NormArgs a;
+  NormCall a;
   if (int rc = fill_norm(a, p, dtype, rows, x, ld_x, weight_dtype, weight)) return rc;
   if (!(eps >= 0) || !std::isfinite(eps)) return fail(CGTP_ERR_INVALID_ARG, "eps must be finite and not negative");
   if (rows > 0 && !y) return fail(CGTP_ERR_INVALID_ARG, "y is NULL");
@@ -106,21 +96,21 @@ int norm_forward(const NormShape& p, int dtype, int64_t rows, const void* x, int
   a.ld_y = ld_y;
   a.stats = stats;
   a.eps = float(eps);
-  CGTP_HIP(launch_norm_forward(a, Elem(dtype), static_cast<hipStream_t>(stream)));
+  CGTP_HIP(launch_norm_forward(a, p, Elem(dtype), static_cast<hipStream_t>(stream)));
   return ok();
 }
 
 int norm_backward_workspace(const NormShape& p, int64_t rows, size_t* bytes) {
   if (!bytes) return fail(CGTP_ERR_INVALID_ARG, "NULL argument");
   if (rows < 0) return fail(CGTP_ERR_INVALID_ARG, "negative size");
-  *bytes = (norm_part_floats(rows, int(p.weights), int(p.biases)) * sizeof(float) + 255) / 256 * 256;
+  *bytes = (norm_part_floats(rows, p) * sizeof(float) + 255) / 256 * 256;
   return ok();
 }
 
 int norm_backward(const NormShape& p, int dtype, int64_t rows, const void* grad_out, int64_t ld_g, const void* x,
                   int64_t ld_x, const float* stats, int weight_dtype, const void* weight, void* grad_x, int64_t ld_gx,
                   void* grad_weight, void* grad_bias, void* workspace, size_t ws_bytes, void* stream) {
-  NormArgs a;
+  NormCall a;
   if (int rc = fill_norm(a, p, dtype, rows, x, ld_x, weight_dtype, weight)) return rc;
   const size_t es = size_t(elem_size(dtype)), ws = size_t(elem_size(weight_dtype));
   if (rows > 0 && (!grad_out || !stats)) return fail(CGTP_ERR_INVALID_ARG, "NULL argument");
@@ -130,7 +120,7 @@ int norm_backward(const NormShape& p, int dtype, int64_t rows, const void* grad_
       !aligned(grad_bias, ws))
     return fail(CGTP_ERR_INVALID_ARG, "misaligned pointer");
   if (grad_weight || grad_bias) {
-    const size_t need = norm_part_floats(rows, int(p.weights), int(p.biases)) * sizeof(float);
+    const size_t need = norm_part_floats(rows, p) * sizeof(float);
     if (!workspace || ws_bytes < need)
       return fail(CGTP_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace ? ws_bytes : size_t(0), need);
     if (!aligned(workspace, 256)) return fail(CGTP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -143,7 +133,7 @@ int norm_backward(const NormShape& p, int dtype, int64_t rows, const void* grad_
   a.grad_weight = grad_weight;
   a.grad_bias = grad_bias;
   a.part = static_cast<float*>(workspace);
-  CGTP_HIP(launch_norm_backward(a, Elem(dtype), static_cast<hipStream_t>(stream)));
+  CGTP_HIP(launch_norm_backward(a, p, Elem(dtype), static_cast<hipStream_t>(stream)));
   return ok();
 }
 
@@ -166,7 +156,8 @@ int cgtp_layer_norm_forward(int dtype, int64_t n_rows, int64_t width, const void
 
 int cgtp_layer_norm_backward_workspace_size(int64_t n_rows, int64_t width, size_t* bytes) {
   if (int rc = check_width(width)) return rc;
-  return norm_backward_workspace(NormShape{width, width, width, nullptr, 1}, n_rows, bytes);
+  const NormTerm t = whole_row(width);
+  return norm_backward_workspace(NormShape{width, width, width, &t, 1}, n_rows, bytes);
 }
 
 int cgtp_layer_norm_backward(int dtype, int64_t n_rows, int64_t width, const void* grad_out, int64_t ld_g,
@@ -196,7 +187,7 @@ int cgtp_norm_create(const char* irreps, cgtp_norm_t* out) {
       const int64_t d = 2 * r.l + 1, len = r.mul * d;
       if (P.features + len > kMaxInt32 / 2) return fail(CGTP_ERR_UNSUPPORTED, "row wider than 2^30 - 1");
       P.terms.push_back(NormTerm{int32_t(P.features), int32_t(len), int32_t(d), int32_t(P.weights),
-                                 centred ? int32_t(P.biases) : -1, int32_t(P.terms.size())});
+                                 centred ? int32_t(P.biases) : -1});
       P.features += len;
       P.weights += r.mul;
       if (centred) P.biases += r.mul;
