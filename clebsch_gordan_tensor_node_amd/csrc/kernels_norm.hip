@@ -441,40 +441,55 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs<Cap> a) {
   CGTP_NORM_VARIANTS(bwd_rows)
 }
 
-// The weight's and bias's gradients from the workgroups' sums.  A workgroup takes whole
-// channels, at most 64 elements; its 16 waves each add every 16th partial sum of theirs,
-// LDS joins the waves and a channel's components, all in a fixed order.
+// The weight's and bias's gradients from the workgroups' sums, in a fixed order.  A
+// workgroup takes whole channels, at most 16 elements; 64 slices of its threads each add
+// every 64th partial sum (all their loads in flight at once: the kernel is a chain of
+// memory latencies, not of bytes), DPP and LDS join the slices, then a channel's components.
 constexpr int kSumThreads = 1024;
+constexpr int kTile = 16;
 constexpr int kSumWaves = kSumThreads / kWave;
 
 template <typename T, int Cap>
 __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) {
-  __shared__ float lds[kSumWaves][kWave];
+  __shared__ float lds[2][kSumWaves][kTile];
+  __shared__ float col[2][kTile];
   const int k = term_of(a);
   const TermArgs& t = a.term[k];
-  const bool centred = t.b_off >= 0;
-  const int tile = kWave / t.d * t.d, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const int e = (int(blockIdx.x) - a.first_block[k]) * tile + lane;
-  const bool has = lane < tile && e < t.len;
-  for (int q = 0; q < (centred ? 2 : 1); ++q) {
-    void* out = q ? a.c.grad_bias : a.c.grad_weight;
-    if (!out) continue;
-    const float* part = a.c.part + t.part + int64_t(q) * t.n_blocks * t.len + e;
-    float s = 0;
-    if (has)
-      for (int b = wave; b < t.n_blocks; b += kSumWaves) s += part[int64_t(b) * t.len];
-    __syncthreads();
-    lds[wave][lane] = s;
-    __syncthreads();
-    if (threadIdx.x < unsigned(tile / t.d)) {
-      const int first = int(threadIdx.x) * t.d, ch = (e - lane) / t.d + int(threadIdx.x);
-      if (ch < t.len / t.d) {
-        float sum = 0;
-        for (int m = 0; m < t.d; ++m)
-          for (int v = 0; v < kSumWaves; ++v) sum += lds[v][first + m];
-        store_either<T>(out, a.c.weight_f32, (q ? t.b_off : t.w_off) + ch, sum);
-      }
+  const bool want_b = t.b_off >= 0 && a.c.grad_bias;
+  const int tile = kTile / t.d * t.d, lane = threadIdx.x % kTile;
+  const int first = (int(blockIdx.x) - a.first_block[k]) * tile;
+  float sw = 0, sb = 0;
+  if (lane < tile && first + lane < t.len) {
+    const float* part = a.c.part + t.part + first + lane;
+    const int64_t other = int64_t(t.n_blocks) * t.len;
+#pragma unroll 8
+    for (int b = threadIdx.x / kTile; b < t.n_blocks; b += kSumThreads / kTile) sw += part[int64_t(b) * t.len];
+    if (want_b) {
+#pragma unroll 8
+      for (int b = threadIdx.x / kTile; b < t.n_blocks; b += kSumThreads / kTile) sb += part[other + int64_t(b) * t.len];
     }
+  }
+  sw += __shfl_xor(sw, 16);
+  sb += __shfl_xor(sb, 16);
+  sw += __shfl_xor(sw, 32);
+  sb += __shfl_xor(sb, 32);
+  if (threadIdx.x % kWave < kTile) {
+    lds[0][threadIdx.x / kWave][lane] = sw;
+    lds[1][threadIdx.x / kWave][lane] = sb;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2 * kSumWaves * kTile) {   // one lane per wave's sum, 16 of a column beside one another
+    const int q = threadIdx.x / (kSumWaves * kTile), c = threadIdx.x / kSumWaves % kTile;
+    const float v = lanes_sum<kSumWaves>(lds[q][threadIdx.x % kSumWaves][c]);
+    if (threadIdx.x % kSumWaves == 0) col[q][c] = v;
+  }
+  __syncthreads();
+  const int q = threadIdx.x / kTile, ch = first / t.d + lane;
+  if (q < 2 && lane < tile / t.d && ch < t.len / t.d) {
+    float v = 0;
+    for (int m = 0; m < t.d; ++m) v += col[q][lane * t.d + m];
+    if (q == 0 && a.c.grad_weight) store_either<T>(a.c.grad_weight, a.c.weight_f32, t.w_off + ch, v);
+    if (q == 1 && want_b) store_either<T>(a.c.grad_bias, a.c.weight_f32, t.b_off + ch, v);
   }
 }
 
@@ -547,7 +562,7 @@ hipError_t backward(const NormCall& c, const NormShape& p, hipStream_t s) {
   if (c.grad_weight || c.grad_bias) {
     int at = 0;
     for (int k = 0; k < p.n_terms; ++k) {
-      const int tile = kWave / p.terms[k].d * p.terms[k].d;
+      const int tile = kTile / p.terms[k].d * p.terms[k].d;
       a.first_block[k] = at;
       at += (p.terms[k].len + tile - 1) / tile;
     }
