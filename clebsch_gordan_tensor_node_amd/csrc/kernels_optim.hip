@@ -76,6 +76,50 @@ __device__ inline Moments adamw(const AdamwArgs& a, float p, float g, float m, f
   return o;
 }
 
+// A lane's elements: kPasses vectors of 4, the workgroup's lanes after one another.
+constexpr int kVec = 4;
+constexpr int kPasses = kChunk / (kThreads * kVec);
+
+// Four elements at any element's address; past n they read as 0 and are not written.
+template <typename T>
+__device__ inline void load4(const T* p, int i, int n, float (&v)[kVec]) {
+  T r[kVec];
+  if (i + kVec <= n) {
+    __builtin_memcpy(r, p + i, sizeof(r));
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = to_f32(r[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = i + j < n ? to_f32(p[i + j]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ inline void store4(T* p, int i, int n, const float (&v)[kVec]) {
+  T r[kVec];
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) r[j] = from_f32<T>(v[j]);
+  if (i + kVec <= n) {
+    __builtin_memcpy(p + i, r, sizeof(r));
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (i + j < n) p[i + j] = r[j];
+  }
+}
+
+template <int Ctrl>
+__device__ inline int dpp(int v) {
+  return __builtin_amdgcn_mov_dpp(v, Ctrl, 0xf, 0xf, true);
+}
+// Largest of 16 neighbouring lanes: of one block of 64 elements.
+__device__ inline int block_max(int v) {
+  v = max(v, dpp<0xB1>(v));    // quad_perm 1 0 3 2
+  v = max(v, dpp<0x4E>(v));    // quad_perm 2 3 0 1
+  v = max(v, dpp<0x141>(v));   // row_half_mirror
+  return max(v, dpp<0x140>(v));   // row_mirror
+}
+static_assert(kStateBlock == 16 * kVec, "a block of states is 16 lanes");
+
 template <typename P, typename G, bool Bits8>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   const Chunk c = a.chunks[blockIdx.x];
@@ -84,34 +128,71 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   P* p = static_cast<P*>(a.param[c.tensor - a.first_tensor]) + c.start;
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
   const float kept = float(1.0 - a.lr * c.decay);
-  const int n = Bits8 ? (c.n + kStateBlock - 1) / kStateBlock * kStateBlock : c.n;   // whole blocks
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int64_t s = c.state + i;
-    const bool in = i < c.n;
-    const float pi = in ? to_f32(p[i]) : 0.0f, gi = in ? to_f32(g[i]) * scale : 0.0f;
-    Moments o;
-    if constexpr (Bits8) {
-      const int me = a.m_exp[s / kStateBlock], re = a.r_exp[s / kStateBlock];
-      const float r = decode_r(a.r_code[s], re);
-      o = adamw(a, pi, gi, decode_m(a.m_code[s], me), r * r, kept);
-      int em = exponent_of(fabsf(o.m)), er = exponent_of(o.root);
-      for (int k = 32; k > 0; k >>= 1) {
-        em = max(em, __shfl_xor(em, k));
-        er = max(er, __shfl_xor(er, k));
+  const int n = (c.n + kStateBlock - 1) / kStateBlock * kStateBlock;   // states are held in whole blocks
+  float pv[kPasses][kVec], gv[kPasses][kVec], mv[kPasses][kVec], vv[kPasses][kVec];
+  uint32_t mc[kPasses], rc[kPasses];
+  int me[kPasses], re[kPasses];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int i = (k * kThreads + int(threadIdx.x)) * kVec;
+    if (i < n) {
+      const int64_t s = c.state + i;
+      load4(p, i, c.n, pv[k]);
+      load4(g, i, c.n, gv[k]);
+      if constexpr (Bits8) {
+        __builtin_memcpy(&mc[k], __builtin_assume_aligned(a.m_code + s, 4), 4);
+        __builtin_memcpy(&rc[k], __builtin_assume_aligned(a.r_code + s, 4), 4);
+        me[k] = a.m_exp[s / kStateBlock];
+        re[k] = a.r_exp[s / kStateBlock];
+      } else {
+        __builtin_memcpy(mv[k], __builtin_assume_aligned(a.m + s, 16), 16);
+        __builtin_memcpy(vv[k], __builtin_assume_aligned(a.v + s, 16), 16);
       }
-      const uint32_t u = random_bits(s, a.seed);
-      a.m_code[s] = uint8_t(encode_m(o.m, em, u & 0xffff));
-      a.r_code[s] = uint8_t(encode_r(o.root, er, u >> 16));
-      if (threadIdx.x % kStateBlock == 0) {
-        a.m_exp[s / kStateBlock] = uint8_t(em);
-        a.r_exp[s / kStateBlock] = uint8_t(er);
-      }
-    } else {
-      o = adamw(a, pi, gi, a.m[s], a.v[s], kept);
-      a.m[s] = o.m;
-      a.v[s] = o.v;
     }
-    if (in) p[i] = from_f32<P>(o.p);
+  }
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int i = (k * kThreads + int(threadIdx.x)) * kVec;
+    if (i < n) {   // the same in the 16 lanes of a block
+      const int64_t s = c.state + i;
+      Moments o[kVec];
+      int em = 0, er = 0;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if constexpr (Bits8) {
+          const float r = decode_r(rc[k] >> (8 * j) & 0xff, re[k]);
+          o[j] = adamw(a, pv[k][j], gv[k][j] * scale, decode_m(mc[k] >> (8 * j) & 0xff, me[k]), r * r, kept);
+          em = max(em, exponent_of(fabsf(o[j].m)));
+          er = max(er, exponent_of(o[j].root));
+        } else {
+          o[j] = adamw(a, pv[k][j], gv[k][j] * scale, mv[k][j], vv[k][j], kept);
+          mv[k][j] = o[j].m;
+          vv[k][j] = o[j].v;
+        }
+        pv[k][j] = o[j].p;
+      }
+      if constexpr (Bits8) {
+        em = block_max(em);
+        er = block_max(er);
+        uint32_t cm = 0, cr = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const uint32_t u = random_bits(s + j, a.seed);
+          cm |= encode_m(o[j].m, em, u & 0xffff) << (8 * j);
+          cr |= encode_r(o[j].root, er, u >> 16) << (8 * j);
+        }
+        __builtin_memcpy(__builtin_assume_aligned(a.m_code + s, 4), &cm, 4);
+        __builtin_memcpy(__builtin_assume_aligned(a.r_code + s, 4), &cr, 4);
+        if (threadIdx.x % 16 == 0) {
+          a.m_exp[s / kStateBlock] = uint8_t(em);
+          a.r_exp[s / kStateBlock] = uint8_t(er);
+        }
+      } else {
+        __builtin_memcpy(__builtin_assume_aligned(a.m + s, 16), mv[k], 16);
+        __builtin_memcpy(__builtin_assume_aligned(a.v + s, 16), vv[k], 16);
+      }
+      store4(p, i, c.n, pv[k]);
+    }
   }
 }
 
@@ -130,11 +211,14 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) 
   __shared__ double lds[kThreads / 64];
   const Chunk c = a.chunks[blockIdx.x];
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
+  float v[kPasses][kVec];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) load4(g, (k * kThreads + int(threadIdx.x)) * kVec, c.n, v[k]);
   double s = 0;
-  for (int i = threadIdx.x; i < c.n; i += kThreads) {
-    const double v = to_f32(g[i]);
-    s += v * v;
-  }
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) s += double(v[k][j]) * double(v[k][j]);
   s = block_sum(s, lds);
   if (threadIdx.x == 0) a.part[blockIdx.x] = s;
 }
@@ -143,6 +227,7 @@ __global__ __launch_bounds__(kFinish) void grad_norm_kernel(const double* part, 
                                                             float max_norm, float* out) {
   __shared__ double lds[kFinish / 64];
   double s = 0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < n; i += kFinish) s += part[i];
   s = block_sum(s, lds);
   if (threadIdx.x == 0) {
@@ -153,13 +238,24 @@ __global__ __launch_bounds__(kFinish) void grad_norm_kernel(const double* part, 
   }
 }
 
+// n is a multiple of kStateBlock; 8 elements a lane.
 __global__ __launch_bounds__(kThreads) void decode_states_kernel(const uint8_t* m_code, const uint8_t* r_code,
                                                                  const uint8_t* m_exp, const uint8_t* r_exp, int64_t n,
                                                                  Bf16* m, Bf16* r) {
-  const int64_t step = int64_t(gridDim.x) * kThreads;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += step) {
-    m[i] = from_f32<Bf16>(decode_m(m_code[i], m_exp[i / kStateBlock]));
-    r[i] = from_f32<Bf16>(decode_r(r_code[i], r_exp[i / kStateBlock]));
+  const int64_t step = int64_t(gridDim.x) * kThreads * 8;
+  for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < n; i += step) {
+    uint8_t mc[8], rc[8];
+    __builtin_memcpy(mc, __builtin_assume_aligned(m_code + i, 8), 8);
+    __builtin_memcpy(rc, __builtin_assume_aligned(r_code + i, 8), 8);
+    const int me = m_exp[i / kStateBlock], re = r_exp[i / kStateBlock];
+    Bf16 mv[8], rv[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      mv[j] = from_f32<Bf16>(decode_m(mc[j], me));
+      rv[j] = from_f32<Bf16>(decode_r(rc[j], re));
+    }
+    __builtin_memcpy(__builtin_assume_aligned(m + i, 16), mv, 16);
+    __builtin_memcpy(__builtin_assume_aligned(r + i, 16), rv, 16);
   }
 }
 
@@ -204,7 +300,7 @@ hipError_t launch_grad_norm_finish(const double* part, int n, const float* grad_
 hipError_t launch_decode_states(const uint8_t* m_code, const uint8_t* r_code, const uint8_t* m_exp,
                                 const uint8_t* r_exp, int64_t n, void* m, void* r, hipStream_t s) {
   if (n > 0) {
-    const int64_t blocks = (n + kThreads - 1) / kThreads;
+    const int64_t blocks = (n + kThreads * 8 - 1) / (kThreads * 8);
     hipLaunchKernelGGL(decode_states_kernel, dim3(unsigned(blocks < 8192 ? blocks : 8192)), dim3(kThreads), 0, s,
                        m_code, r_code, m_exp, r_exp, n, static_cast<Bf16*>(m), static_cast<Bf16*>(r));
   }

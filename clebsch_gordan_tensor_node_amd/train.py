@@ -30,6 +30,17 @@ __all__ = ["layer_norm_forward", "layer_norm_backward", "NormPlan", "irreps_norm
            "ParamSet", "adamw_state", "adamw_step", "adamw_moments", "grad_norm"]
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() makes an object: 3 us a call
+
+
+def _on(t, name, dev):
+    """Checks that t is a tensor on device number `dev`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device (cuda) tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, expected {dev}")
+
+
 def _rows(t, name, shape=None, dtype=None):
     """Checks a [rows, width] device tensor whose rows are dense; its row stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -45,84 +56,78 @@ def _rows(t, name, shape=None, dtype=None):
     return max(ld, f)
 
 
-def _vec(t, n, name, x):
-    """Checks a weight or bias [n] of fp32 or x's type (None passes); its type."""
+def _vec(t, n, name, x, dev):
+    """Checks a weight or bias [n] of fp32 or x's type (None passes); its address and type."""
     if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a device (cuda) tensor")
+        return None, None
+    _on(t, name, dev)
     if t.dtype != torch.float32 and t.dtype != x.dtype:
         raise TypeError(f"{name} must be float32 or {x.dtype}, got {t.dtype}")
     if t.shape != (n,):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n},)")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.dtype
-
-
-def _device(x, **others):
-    """The library's calls run on the current device: every tensor has to be there."""
-    here = torch.cuda.current_device()
-    for name, t in (("x", x), *others.items()):
-        if t is not None and t.device.index != here:
-            raise ValueError(f"{name} is on device {t.device.index}, the current device is {here}")
-    return torch.cuda.current_stream().cuda_stream
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _weight_type(weight, bias, x, nw, nb):
-    tw, tb = _vec(weight, nw, "weight", x), _vec(bias, nb, "bias", x)
-    if tw is not None and tb is not None and tw != tb:
-        raise TypeError(f"weight ({tw}) and bias ({tb}) must have one type")
-    return tw or tb or torch.float32
+    return t.data_ptr(), t.dtype
 
 
 def _head(plan, x):
-    """The leading arguments of a norm call, and x's row stride, weights, biases and shape
-    of stats."""
+    """The leading arguments of a norm call, and x's row stride, weights, biases, shape of
+    stats and device.  The library's calls run on the current device: x has to be there."""
     ld = _rows(x, "x")
     n, f = x.shape
+    dev = x.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"x is on device {dev}, the current device is {torch.cuda.current_device()}")
     if plan is None:
-        return (ELEM[x.dtype], n, f), ld, f, f, (2, n)
+        return (ELEM[x.dtype], n, f), ld, f, f, (2, n), dev
     if f != plan.n_features:
         raise ValueError(f"x has rows of {f}, the plan's have {plan.n_features}")
-    return (plan.handle, ELEM[x.dtype], n), ld, plan.n_weights, plan.n_biases, (2, n, plan.n_terms)
+    return (plan.handle, ELEM[x.dtype], n), ld, plan.n_weights, plan.n_biases, (2, n, plan.n_terms), dev
 
 
 def _forward(call, plan, x, weight, bias, eps, out):
-    head, ld, nw, nb, stats_shape = _head(plan, x)
-    wt = _weight_type(weight, bias, x, nw, nb)
+    head, ld, nw, nb, stats_shape, dev = _head(plan, x)
+    (w, tw), (b, tb) = _vec(weight, nw, "weight", x, dev), _vec(bias, nb, "bias", x, dev)
+    if tw is not None and tb is not None and tw != tb:
+        raise TypeError(f"weight ({tw}) and bias ({tb}) must have one type")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    ld_y = _rows(out, "out", x.shape, x.dtype)
-    stats = torch.empty(stats_shape, dtype=torch.float32, device=x.device)
-    stream = _device(x, weight=weight, bias=bias, out=out)
-    check(call(*head, _at(x), ld, ELEM[wt], _at(weight), _at(bias), eps, _at(out), ld_y, _at(stats), stream))
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ld_y = x.shape[1]
+    else:
+        _on(out, "out", dev)
+        ld_y = _rows(out, "out", x.shape, x.dtype)
+    stats = x.new_empty(stats_shape, dtype=torch.float32)
+    check(call(*head, x.data_ptr(), ld, ELEM[tw or tb or torch.float32], w, b, eps, out.data_ptr(), ld_y,
+               stats.data_ptr(), _raw_stream(dev)))
     return out, stats
 
 
 def _backward(call, size, plan, grad_out, x, stats, weight, need, workspace):
-    head, ld, nw, nb, stats_shape = _head(plan, x)
+    head, ld, nw, nb, stats_shape, dev = _head(plan, x)
+    _on(grad_out, "grad_out", dev)
     ld_g = _rows(grad_out, "grad_out", x.shape, x.dtype)
-    wt = _weight_type(weight, None, x, nw, nb)
-    if not isinstance(stats, torch.Tensor) or not stats.is_cuda or stats.dtype != torch.float32:
-        raise TypeError("stats must be a float32 device (cuda) tensor")
+    w, wt = _vec(weight, nw, "weight", x, dev)
+    wt = wt or torch.float32
+    _on(stats, "stats", dev)
+    if stats.dtype != torch.float32:
+        raise TypeError(f"stats must be float32, got {stats.dtype}")
     if stats.shape != stats_shape or not stats.is_contiguous():
         raise ValueError(f"stats must be contiguous of shape {stats_shape}, got {tuple(stats.shape)}")
-    dev = x.device
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if "x" in need else None
-    gw = torch.empty(nw, dtype=wt, device=dev) if "weight" in need else None
-    gb = torch.empty(nb, dtype=wt, device=dev) if "bias" in need else None
-    stream = _device(x, grad_out=grad_out, stats=stats, weight=weight, workspace=workspace)
-    if workspace is None and (gw is not None or gb is not None):
-        workspace = torch.empty(size(x.shape[0]), dtype=torch.uint8, device=dev)
-    check(call(*head, _at(grad_out), ld_g, _at(x), ld, _at(stats), ELEM[wt], _at(weight), _at(gx), x.shape[1], _at(gw),
-               _at(gb), _at(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-               stream))
+    gx = torch.empty_like(x, memory_format=torch.contiguous_format) if "x" in need else None
+    gw = x.new_empty(nw, dtype=wt) if "weight" in need else None
+    gb = x.new_empty(nb, dtype=wt) if "bias" in need else None
+    if workspace is not None:
+        _on(workspace, "workspace", dev)
+    elif gw is not None or gb is not None:
+        workspace = x.new_empty(size(x.shape[0]), dtype=torch.uint8)
+    check(call(*head, grad_out.data_ptr(), ld_g, x.data_ptr(), ld, stats.data_ptr(), ELEM[wt], w, _at(gx), x.shape[1],
+               _at(gw), _at(gb), _at(workspace),
+               0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev)))
     return gx, gw, gb
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None):
@@ -220,7 +225,8 @@ class _Pointers:
                 raise ValueError(f"tensor {k} has {t.numel()} elements, expected {n}")
             if not t.is_contiguous():
                 raise ValueError(f"tensor {k} must be contiguous")
-        self.tensors = tensors
+        self.tensors, self.sizes = tensors, sizes
+        self.device = tensors[0].device if tensors else None
         self.type = ELEM[tensors[0].dtype] if tensors else 0
         self.array = (ctypes.c_void_p * max(len(tensors), 1))(*[t.data_ptr() for t in tensors])
 
@@ -284,33 +290,35 @@ def adamw_state(params: ParamSet, bits: int = 32):
 
 
 def _state(params, state):
-    n = params.state_elems
-    want = {2: (torch.float32, (n, n)), 4: (torch.uint8, (n, n, n // 64, n // 64))}.get(len(state))
-    if want is None:
+    """Checks a set's states; their addresses."""
+    if len(state) not in (2, 4):
         raise ValueError("a state is (m, v) or (m codes, r codes, m exponents, r exponents)")
-    for t, k in zip(state, want[1]):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != want[0]:
-            raise TypeError(f"states must be {want[0]} device (cuda) tensors")
-        if t.shape != (k,) or not t.is_contiguous():
-            raise ValueError(f"a state has shape {tuple(t.shape)}, expected ({k},), contiguous")
-        if t.device != params.device:
-            raise ValueError("states must be on the set's device")
-    return [t.data_ptr() for t in state]
+    dtype = torch.float32 if len(state) == 2 else torch.uint8
+    at = []
+    for k, t in enumerate(state):
+        _on(t, "a state", params.device.index)
+        if t.dtype != dtype:
+            raise TypeError(f"a state is {t.dtype}, expected {dtype}")
+        n = params.state_elems // (64 if k > 1 else 1)
+        if t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"a state has shape {tuple(t.shape)}, expected ({n},), contiguous")
+        at.append(t.data_ptr())
+    return at
 
 
 def _scale(params, t):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != params.device or t.dtype != torch.float32 or t.numel() != 1:
+    if not isinstance(t, torch.Tensor) or t.get_device() != params.device.index or t.dtype != torch.float32 or t.numel() != 1:
         raise TypeError("grad_scale must be a float32 tensor of one element on the set's device")
     return t.data_ptr()
 
 
 def _laid(params, tensors, what):
     p = params.pointers(tensors)
-    if len(p.tensors) != len(params.sizes):
-        raise ValueError(f"{what}: {len(p.tensors)} tensors, the set has {len(params.sizes)}")
-    if p.tensors and p.tensors[0].device != params.device:
+    if len(p.tensors) != len(params.sizes) or p.sizes != params.sizes:
+        raise ValueError(f"{what} were laid out for another set")
+    if p.device is not None and p.device != params.device:
         raise ValueError(f"{what} must be on the set's device")
     return p
 
@@ -324,7 +332,7 @@ def adamw_step(params: ParamSet, tensors, grads, state, lr: float, betas=(0.9, 0
     scale) that multiplies the gradients; NaN skips the step.  With 8-bit states, seed
     chooses the rounding: pass another each step.  Asynchronous on the current stream."""
     p, g = _laid(params, tensors, "tensors"), _laid(params, grads, "grads")
-    s, scale, stream = _state(params, state), _scale(params, grad_scale), torch.cuda.current_stream().cuda_stream
+    s, scale, stream = _state(params, state), _scale(params, grad_scale), _raw_stream(params.device.index)
     lib = load()
     if len(s) == 2:
         check(lib.cgtp_adamw_step(params.handle, p.type, p.array, g.type, g.array, *s, lr, betas[0], betas[1], eps,
@@ -342,7 +350,7 @@ def adamw_moments(params: ParamSet, state):
         return state
     m, r = (torch.empty(params.state_elems, dtype=torch.bfloat16, device=params.device) for _ in range(2))
     check(load().cgtp_adamw_read_8bit(params.handle, *s, m.data_ptr(), r.data_ptr(),
-                                      torch.cuda.current_stream().cuda_stream))
+                                      _raw_stream(params.device.index)))
     return m, r
 
 
@@ -356,5 +364,5 @@ def grad_norm(params: ParamSet, grads, max_norm: float = float("inf"), grad_scal
         workspace = torch.empty(params.grad_norm_workspace_size, dtype=torch.uint8, device=params.device)
     check(load().cgtp_grad_norm(params.handle, g.type, g.array, _scale(params, grad_scale), max_norm, out.data_ptr(),
                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                torch.cuda.current_stream().cuda_stream))
+                                _raw_stream(params.device.index)))
     return out
