@@ -28,39 +28,36 @@ constexpr int kFinish = 1024;
 __device__ inline uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
 __device__ inline float float_of(uint32_t v) { return __builtin_bit_cast(float, v); }
 
-// 32 random bits of state element i.  The odd constants are the fractions of the golden
-// ratio and of the square roots of 2 and 3.
-__device__ inline uint32_t random_bits(int64_t i, uint32_t seed) {
-  uint32_t h = uint32_t(i) * 0x9E3779B9u + uint32_t(uint64_t(i) >> 32) * 0x6A09E667u + seed;
+// 32 random bits of state element i: mix(place(i, seed)), with place(i + 1) = place(i) +
+// kGolden inside 2^32 elements.  The odd constants are the fractions of the golden ratio
+// and of the square roots of 2 and 3.
+constexpr uint32_t kGolden = 0x9E3779B9u;
+__device__ inline uint32_t place(int64_t i, uint32_t seed) {
+  return uint32_t(i) * kGolden + uint32_t(uint64_t(i) >> 32) * 0x6A09E667u + seed;
+}
+__device__ inline uint32_t mix(uint32_t h) {
   h ^= h >> 15;
   h *= 0xBB67AE85u;
   return h ^ (h >> 16);
 }
 
 constexpr uint32_t kMNan = 0x7f, kRNan = 0xff;   // codes of values that are not finite
+constexpr uint32_t kInf = 0x7f800000u;
 
-__device__ inline float decode_m(uint32_t code, int e) {
-  if ((code & 0x7f) == kMNan) return __builtin_nanf("");
-  const float a = ldexpf(float_of((code & 0x7f) << 20), max(e, 1) - 14);
-  return code & 0x80 ? -a : a;
+// Values and codes of finite moments (sh = max(E, 1) - 14).
+__device__ inline float decode_m(uint32_t code, int sh) {
+  return ldexpf(float_of((code & 0x7f) << 20 | (code & 0x80) << 24), sh);
 }
-__device__ inline float decode_r(uint32_t code, int e) {
-  if (code == kRNan) return __builtin_nanf("");
-  return ldexpf(float_of(code << 19), max(e, 1) - 14);
+__device__ inline float decode_r(uint32_t code, int sh) { return ldexpf(float_of(code << 19), sh); }
+__device__ inline uint32_t encode_m(float m, int sh, uint32_t u) {
+  return (bits_of(ldexpf(fabsf(m), -sh)) + (u << 4)) >> 20 | bits_of(m) >> 31 << 7;
 }
-__device__ inline uint32_t encode_m(float m, int e, uint32_t u) {
-  const float a = fabsf(m);
-  const uint32_t c = a < __builtin_inff() ? (bits_of(ldexpf(a, 14 - max(e, 1))) + (u << 4)) >> 20 : kMNan;
-  return c | (m < 0 ? 0x80u : 0u);
+__device__ inline uint32_t encode_r(float r, int sh, uint32_t u) {
+  return max((bits_of(ldexpf(r, -sh)) + (u << 3)) >> 19, min(bits_of(r), 1u));
 }
-__device__ inline uint32_t encode_r(float r, int e, uint32_t u) {
-  if (!(r < __builtin_inff())) return kRNan;
-  const uint32_t c = (bits_of(ldexpf(r, 14 - max(e, 1))) + (u << 3)) >> 19;
-  return r > 0 && c == 0 ? 1u : c;
-}
-// A magnitude's biased exponent, 0 where it is not finite (such a value is coded as NaN
-// and does not set the block's scale).
-__device__ inline int exponent_of(float a) { return a < __builtin_inff() ? int(bits_of(a) >> 23) : 0; }
+// Whether one of four codes is a NaN's: a byte of all ones (m: but for its sign).
+__device__ inline bool any_ones(uint32_t v) { return ((~v - 0x01010101u) & v & 0x80808080u) != 0; }
+__device__ inline float nan() { return __builtin_nanf(""); }
 
 struct Moments {
   float p, m, v, root;
@@ -80,11 +77,12 @@ __device__ inline Moments adamw(const AdamwArgs& a, float p, float g, float m, f
 constexpr int kVec = 4;
 constexpr int kPasses = kChunk / (kThreads * kVec);
 
-// Four elements at any element's address; past n they read as 0 and are not written.
-template <typename T>
-__device__ inline void load4(const T* p, int i, int n, float (&v)[kVec]) {
+// Four elements at any element's address; past n (unless Full) they read as 0 and are not
+// written.
+template <bool Full, typename T>
+__device__ inline void load4(const T* p, unsigned i, unsigned n, float (&v)[kVec]) {
   T r[kVec];
-  if (i + kVec <= n) {
+  if (Full || i + kVec <= n) {
     __builtin_memcpy(r, p + i, sizeof(r));
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[j] = to_f32(r[j]);
@@ -93,12 +91,12 @@ __device__ inline void load4(const T* p, int i, int n, float (&v)[kVec]) {
     for (int j = 0; j < kVec; ++j) v[j] = i + j < n ? to_f32(p[i + j]) : 0.0f;
   }
 }
-template <typename T>
-__device__ inline void store4(T* p, int i, int n, const float (&v)[kVec]) {
+template <bool Full, typename T>
+__device__ inline void store4(T* p, unsigned i, unsigned n, const float (&v)[kVec]) {
   T r[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) r[j] = from_f32<T>(v[j]);
-  if (i + kVec <= n) {
+  if (Full || i + kVec <= n) {
     __builtin_memcpy(p + i, r, sizeof(r));
   } else {
 #pragma unroll
@@ -108,11 +106,11 @@ __device__ inline void store4(T* p, int i, int n, const float (&v)[kVec]) {
 }
 
 template <int Ctrl>
-__device__ inline int dpp(int v) {
-  return __builtin_amdgcn_mov_dpp(v, Ctrl, 0xf, 0xf, true);
+__device__ inline uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_mov_dpp(int(v), Ctrl, 0xf, 0xf, true));
 }
 // Largest of 16 neighbouring lanes: of one block of 64 elements.
-__device__ inline int block_max(int v) {
+__device__ inline uint32_t block_max(uint32_t v) {
   v = max(v, dpp<0xB1>(v));    // quad_perm 1 0 3 2
   v = max(v, dpp<0x4E>(v));    // quad_perm 2 3 0 1
   v = max(v, dpp<0x141>(v));   // row_half_mirror
@@ -120,80 +118,127 @@ __device__ inline int block_max(int v) {
 }
 static_assert(kStateBlock == 16 * kVec, "a block of states is 16 lanes");
 
-template <typename P, typename G, bool Bits8>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
-  const Chunk c = a.chunks[blockIdx.x];
-  const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
-  if (scale != scale) return;   // the gradients are not finite: the step is skipped
+// One chunk.  Full: all kChunk elements are there, nothing is guarded.
+template <typename P, typename G, bool Bits8, bool Full>
+__device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float scale) {
   P* p = static_cast<P*>(a.param[c.tensor - a.first_tensor]) + c.start;
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
+  float *m = a.m + c.state, *v = a.v + c.state;
+  uint8_t *m_code = a.m_code + c.state, *r_code = a.r_code + c.state;
+  uint8_t *m_exp = a.m_exp + c.state / kStateBlock, *r_exp = a.r_exp + c.state / kStateBlock;
   const float kept = float(1.0 - a.lr * c.decay);
-  const int n = (c.n + kStateBlock - 1) / kStateBlock * kStateBlock;   // states are held in whole blocks
+  const unsigned n = Full ? kChunk : unsigned(c.n), whole = (n + kStateBlock - 1) / kStateBlock * kStateBlock;
   float pv[kPasses][kVec], gv[kPasses][kVec], mv[kPasses][kVec], vv[kPasses][kVec];
   uint32_t mc[kPasses], rc[kPasses];
   int me[kPasses], re[kPasses];
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const int i = (k * kThreads + int(threadIdx.x)) * kVec;
-    if (i < n) {
-      const int64_t s = c.state + i;
-      load4(p, i, c.n, pv[k]);
-      load4(g, i, c.n, gv[k]);
-      if constexpr (Bits8) {
-        __builtin_memcpy(&mc[k], __builtin_assume_aligned(a.m_code + s, 4), 4);
-        __builtin_memcpy(&rc[k], __builtin_assume_aligned(a.r_code + s, 4), 4);
-        me[k] = a.m_exp[s / kStateBlock];
-        re[k] = a.r_exp[s / kStateBlock];
-      } else {
-        __builtin_memcpy(mv[k], __builtin_assume_aligned(a.m + s, 16), 16);
-        __builtin_memcpy(vv[k], __builtin_assume_aligned(a.v + s, 16), 16);
-      }
+    const unsigned i = (k * kThreads + threadIdx.x) * kVec;
+    if (!Full && i >= whole) break;   // states are held in whole blocks
+    load4<Full>(p, i, n, pv[k]);
+    load4<Full>(g, i, n, gv[k]);
+    if constexpr (Bits8) {
+      __builtin_memcpy(&mc[k], __builtin_assume_aligned(m_code + i, 4), 4);
+      __builtin_memcpy(&rc[k], __builtin_assume_aligned(r_code + i, 4), 4);
+      me[k] = m_exp[i / kStateBlock];
+      re[k] = r_exp[i / kStateBlock];
+    } else {
+      __builtin_memcpy(mv[k], __builtin_assume_aligned(m + i, 16), 16);
+      __builtin_memcpy(vv[k], __builtin_assume_aligned(v + i, 16), 16);
     }
   }
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const int i = (k * kThreads + int(threadIdx.x)) * kVec;
-    if (i < n) {   // the same in the 16 lanes of a block
-      const int64_t s = c.state + i;
-      Moments o[kVec];
-      int em = 0, er = 0;
+    const unsigned i = (k * kThreads + threadIdx.x) * kVec;
+    if (!Full && i >= whole) break;   // the same in the 16 lanes of a block
+    if constexpr (Bits8) {
+      const int sm = max(me[k], 1) - 14, sr = max(re[k], 1) - 14;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        if constexpr (Bits8) {
-          const float r = decode_r(rc[k] >> (8 * j) & 0xff, re[k]);
-          o[j] = adamw(a, pv[k][j], gv[k][j] * scale, decode_m(mc[k] >> (8 * j) & 0xff, me[k]), r * r, kept);
-          em = max(em, exponent_of(fabsf(o[j].m)));
-          er = max(er, exponent_of(o[j].root));
-        } else {
-          o[j] = adamw(a, pv[k][j], gv[k][j] * scale, mv[k][j], vv[k][j], kept);
-          mv[k][j] = o[j].m;
-          vv[k][j] = o[j].v;
-        }
-        pv[k][j] = o[j].p;
+        mv[k][j] = decode_m(mc[k] >> (8 * j) & 0xff, sm);
+        const float r = decode_r(rc[k] >> (8 * j) & 0xff, sr);
+        vv[k][j] = r * r;
       }
-      if constexpr (Bits8) {
-        em = block_max(em);
-        er = block_max(er);
-        uint32_t cm = 0, cr = 0;
+      if (any_ones(mc[k] | 0x80808080u) || any_ones(rc[k])) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-          const uint32_t u = random_bits(s + j, a.seed);
-          cm |= encode_m(o[j].m, em, u & 0xffff) << (8 * j);
-          cr |= encode_r(o[j].root, er, u >> 16) << (8 * j);
+          if ((mc[k] >> (8 * j) & kMNan) == kMNan) mv[k][j] = nan();
+          if ((rc[k] >> (8 * j) & kRNan) == kRNan) vv[k][j] = nan();
         }
-        __builtin_memcpy(__builtin_assume_aligned(a.m_code + s, 4), &cm, 4);
-        __builtin_memcpy(__builtin_assume_aligned(a.r_code + s, 4), &cr, 4);
-        if (threadIdx.x % 16 == 0) {
-          a.m_exp[s / kStateBlock] = uint8_t(em);
-          a.r_exp[s / kStateBlock] = uint8_t(er);
-        }
-      } else {
-        __builtin_memcpy(__builtin_assume_aligned(a.m + s, 16), mv[k], 16);
-        __builtin_memcpy(__builtin_assume_aligned(a.v + s, 16), vv[k], 16);
       }
-      store4(p, i, c.n, pv[k]);
     }
+    float root[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const Moments o = adamw(a, pv[k][j], gv[k][j] * scale, mv[k][j], vv[k][j], kept);
+      pv[k][j] = o.p;
+      mv[k][j] = o.m;
+      vv[k][j] = o.v;
+      root[j] = o.root;
+    }
+    if constexpr (Bits8) {
+      // the block's largest magnitudes; where one is not finite, the largest finite ones
+      uint32_t tm = 0, tr = 0;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        tm = max(tm, bits_of(mv[k][j]) & 0x7fffffffu);
+        tr = max(tr, bits_of(root[j]) & 0x7fffffffu);
+      }
+      tm = block_max(tm);
+      tr = block_max(tr);
+      const bool bad = tm >= kInf || tr >= kInf;
+      if (bad) {
+        tm = tr = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const uint32_t bm = bits_of(mv[k][j]) & 0x7fffffffu, br = bits_of(root[j]) & 0x7fffffffu;
+          tm = max(tm, bm < kInf ? bm : 0u);
+          tr = max(tr, br < kInf ? br : 0u);
+        }
+        tm = block_max(tm);
+        tr = block_max(tr);
+      }
+      const int em = int(tm >> 23), er = int(tr >> 23), sm = max(em, 1) - 14, sr = max(er, 1) - 14;
+      const uint32_t h0 = place(c.state + i, a.seed);
+      uint32_t cm = 0, cr = 0;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const uint32_t u = mix(h0 + j * kGolden);
+        cm |= encode_m(mv[k][j], sm, u & 0xffff) << (8 * j);
+        cr |= encode_r(root[j], sr, u >> 16) << (8 * j);
+      }
+      if (bad) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const uint32_t sign = bits_of(mv[k][j]) >> 31 << 7;
+          if (!(fabsf(mv[k][j]) < float_of(kInf)))
+            cm = (cm & ~(0xffu << (8 * j))) | (kMNan | (mv[k][j] < 0 ? sign : 0u)) << (8 * j);
+          if (!(root[j] < float_of(kInf))) cr |= kRNan << (8 * j);
+        }
+      }
+      __builtin_memcpy(__builtin_assume_aligned(m_code + i, 4), &cm, 4);
+      __builtin_memcpy(__builtin_assume_aligned(r_code + i, 4), &cr, 4);
+      if (threadIdx.x % 16 == 0) {
+        m_exp[i / kStateBlock] = uint8_t(em);
+        r_exp[i / kStateBlock] = uint8_t(er);
+      }
+    } else {
+      __builtin_memcpy(__builtin_assume_aligned(m + i, 16), mv[k], 16);
+      __builtin_memcpy(__builtin_assume_aligned(v + i, 16), vv[k], 16);
+    }
+    store4<Full>(p, i, n, pv[k]);
   }
+}
+
+template <typename P, typename G, bool Bits8>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
+  const Chunk c = a.chunks[blockIdx.x];
+  const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
+  if (scale != scale) return;   // the gradients are not finite: the step is skipped
+  if (c.n == kChunk)
+    adamw_chunk<P, G, Bits8, true>(a, c, scale);
+  else
+    adamw_chunk<P, G, Bits8, false>(a, c, scale);
 }
 
 __device__ inline double block_sum(double v, double* lds) {
@@ -213,7 +258,8 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) 
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
   float v[kPasses][kVec];
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) load4(g, (k * kThreads + int(threadIdx.x)) * kVec, c.n, v[k]);
+  for (int k = 0; k < kPasses; ++k)
+    load4<false>(g, (k * kThreads + threadIdx.x) * kVec, unsigned(c.n), v[k]);
   double s = 0;
 #pragma unroll
   for (int k = 0; k < kPasses; ++k)
@@ -247,12 +293,12 @@ __global__ __launch_bounds__(kThreads) void decode_states_kernel(const uint8_t* 
     uint8_t mc[8], rc[8];
     __builtin_memcpy(mc, __builtin_assume_aligned(m_code + i, 8), 8);
     __builtin_memcpy(rc, __builtin_assume_aligned(r_code + i, 8), 8);
-    const int me = m_exp[i / kStateBlock], re = r_exp[i / kStateBlock];
+    const int sm = max(int(m_exp[i / kStateBlock]), 1) - 14, sr = max(int(r_exp[i / kStateBlock]), 1) - 14;
     Bf16 mv[8], rv[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      mv[j] = from_f32<Bf16>(decode_m(mc[j], me));
-      rv[j] = from_f32<Bf16>(decode_r(rc[j], re));
+      mv[j] = from_f32<Bf16>((mc[j] & kMNan) == kMNan ? nan() : decode_m(mc[j], sm));
+      rv[j] = from_f32<Bf16>(rc[j] == kRNan ? nan() : decode_r(rc[j], sr));
     }
     __builtin_memcpy(__builtin_assume_aligned(m + i, 16), mv, 16);
     __builtin_memcpy(__builtin_assume_aligned(r + i, 16), rv, 16);
