@@ -93,18 +93,35 @@ int elems_of(int variant, int elem_bytes) {
 
 template <typename T, int V>
 struct Vec {
+  typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T) * V / 4), aligned(sizeof(T))));
   T v[V];
 };
-// 16 bytes (or one element) at any element's address.
-template <typename T, int V>
+template <>
+struct Vec<Bf16, 1> {
+  typedef uint16_t Bits;
+  Bf16 v[1];
+};
+template <>
+struct Vec<F16, 1> {
+  typedef uint16_t Bits;
+  F16 v[1];
+};
+// 16 bytes (or one element) at any element's address.  Stream: the access does not keep
+// the line in the caches.
+template <bool Stream, typename T, int V>
 __device__ inline Vec<T, V> load_vec(const T* p) {
-  Vec<T, V> r;
-  __builtin_memcpy(&r, p, sizeof(r));
-  return r;
+  typedef typename Vec<T, V>::Bits Bits;
+  const Bits* b = reinterpret_cast<const Bits*>(p);
+  return __builtin_bit_cast(Vec<T, V>, Stream ? __builtin_nontemporal_load(b) : *b);
 }
-template <typename T, int V>
+template <bool Stream, typename T, int V>
 __device__ inline void store_vec(T* p, const Vec<T, V>& r) {
-  __builtin_memcpy(p, &r, sizeof(r));
+  typedef typename Vec<T, V>::Bits Bits;
+  Bits* b = reinterpret_cast<Bits*>(p);
+  if constexpr (Stream)
+    __builtin_nontemporal_store(__builtin_bit_cast(Bits, r), b);
+  else
+    *b = __builtin_bit_cast(Bits, r);
 }
 
 template <int Ctrl>
@@ -170,28 +187,43 @@ struct Place {
   __device__ int skip(int c) const { return start(c) - at(c); }       // of which these belong to the one before
 };
 
+template <typename T, int V, int C>
+struct Row {
+  Vec<T, V> c[C];
+};
 template <typename T, int V, int G, int C>
-__device__ inline void load_row(const Place<V, G, C>& p, const T* row, float (&x)[C][V]) {
+__device__ inline Row<T, V, C> read_row(const Place<V, G, C>& p, const T* row, bool stream) {
+  Row<T, V, C> r = {};
+  if (stream) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (p.has(c)) r.c[c] = load_vec<true, T, V>(row + p.at(c));
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (p.has(c)) r.c[c] = load_vec<false, T, V>(row + p.at(c));
+  }
+  return r;
+}
+template <typename T, int V, int C>
+__device__ inline void widen(const Row<T, V, C>& r, float (&x)[C][V]) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
-    if (p.has(c)) {
-      const Vec<T, V> r = load_vec<T, V>(row + p.at(c));
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[c][j] = to_f32(r.v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[c][j] = 0;
-    }
+    for (int j = 0; j < V; ++j) x[c][j] = to_f32(r.c[c].v[j]);
 }
 template <typename T, int V, int G, int C>
-__device__ inline void store_row(const Place<V, G, C>& p, T* row, const float (&y)[C][V]) {
+__device__ inline void store_row(const Place<V, G, C>& p, T* row, const float (&y)[C][V], bool stream) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
     if (p.has(c)) {
       Vec<T, V> r;
 #pragma unroll
       for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(y[c][j]);
-      store_vec<T, V>(row + p.at(c), r);
+      if (stream)
+        store_vec<true, T, V>(row + p.at(c), r);
+      else
+        store_vec<false, T, V>(row + p.at(c), r);
     }
 }
 // Sum of f(c, j) over the lane's own elements.
@@ -239,7 +271,7 @@ __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_term
   load_weights<T>(p, centred ? a.bias : nullptr, a.weight_f32, t.b_off, t, 0.0f, b);
   int turn = 0;
   for (int64_t r = int64_t(block) * kGroups + threadIdx.x / G; r < a.rows; r += int64_t(t.n_blocks) * kGroups) {
-    load_row(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off, x);
+    widen(read_row(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off, a.stream), x);
     float mu = 0;
     if (centred) mu = group_sum<G>(own_sum(p, [&](int c, int j) { return x[c][j]; }), lds, turn) * inv;
     const float s2 = group_sum<G>(own_sum(p, [&](int c, int j) { return (x[c][j] - mu) * (x[c][j] - mu); }), lds, turn);
@@ -248,7 +280,7 @@ __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_term
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) x[c][j] = (x[c][j] - mu) * rstd * w[c][j] + b[c][j];
-    store_row(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, x);
+    store_row(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, x, a.stream);
     if (a.stats && p.lane == 0) {
       a.stats[r * n_terms + index] = mu;
       a.stats[(a.rows + r) * n_terms + index] = rstd;
@@ -270,8 +302,8 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
     for (int j = 0; j < V; ++j) gw[c][j] = gb[c][j] = 0;
   int turn = 0;
   for (int64_t r = int64_t(block) * kGroups + threadIdx.x / G; r < a.rows; r += int64_t(t.n_blocks) * kGroups) {
-    load_row(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off, x);
-    load_row(p, static_cast<const T*>(a.grad_out) + r * a.ld_g + t.off, g);
+    widen(read_row(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off, a.stream), x);
+    widen(read_row(p, static_cast<const T*>(a.grad_out) + r * a.ld_g + t.off, a.stream), g);
     const float mu = a.stats[r * n_terms + index], rstd = a.stats[(a.rows + r) * n_terms + index];
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -292,7 +324,7 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) g[c][j] = (g[c][j] - sa - x[c][j] * sh) * rstd;
-    store_row(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, g);
+    store_row(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, g, a.stream);
   }
   if (!a.grad_weight && !a.grad_bias) return;
   // the workgroup's sums: its groups' added in LDS, one row of `part`
@@ -513,6 +545,7 @@ int64_t most_backward_blocks(int64_t rows, const NormShape& p, int k) {
 template <int Cap>
 int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, int elem_bytes, bool backward, int* max_e) {
   a.c = c;
+  a.c.stream = c.rows * p.features * elem_bytes * (backward ? 3 : 2) > kCacheBytes;
   a.n_terms = p.n_terms;
   int64_t part = 0;
   int at = 0;

@@ -78,30 +78,54 @@ constexpr int kVec = 4;
 constexpr int kPasses = kChunk / (kThreads * kVec);
 
 // Four elements at any element's address; past n (unless Full) they read as 0 and are not
-// written.
-template <bool Full, typename T>
+// written.  Stream: the access does not keep the line in the caches.
+template <typename T>
+struct Four {
+  typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T)), aligned(sizeof(T))));
+  T v[kVec];
+};
+template <>
+struct Four<uint8_t> {
+  typedef uint32_t Bits;
+  uint8_t v[kVec];
+};
+template <bool Stream, typename T>
+__device__ inline Four<T> read4(const T* p) {
+  typedef typename Four<T>::Bits Bits;
+  const Bits* b = reinterpret_cast<const Bits*>(p);
+  return __builtin_bit_cast(Four<T>, Stream ? __builtin_nontemporal_load(b) : *b);
+}
+template <bool Stream, typename T>
+__device__ inline void write4(T* p, const Four<T>& v) {
+  typedef typename Four<T>::Bits Bits;
+  Bits* b = reinterpret_cast<Bits*>(p);
+  if constexpr (Stream)
+    __builtin_nontemporal_store(__builtin_bit_cast(Bits, v), b);
+  else
+    *b = __builtin_bit_cast(Bits, v);
+}
+template <bool Full, bool Stream, typename T>
 __device__ inline void load4(const T* p, unsigned i, unsigned n, float (&v)[kVec]) {
-  T r[kVec];
   if (Full || i + kVec <= n) {
-    __builtin_memcpy(r, p + i, sizeof(r));
+    const Four<T> r = read4<Stream>(p + i);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) v[j] = to_f32(r[j]);
+    for (int j = 0; j < kVec; ++j) v[j] = to_f32(r.v[j]);
   } else {
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[j] = i + j < n ? to_f32(p[i + j]) : 0.0f;
   }
 }
-template <bool Full, typename T>
+template <bool Full, bool Stream, typename T>
 __device__ inline void store4(T* p, unsigned i, unsigned n, const float (&v)[kVec]) {
-  T r[kVec];
+  Four<T> r;
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) r[j] = from_f32<T>(v[j]);
+  for (int j = 0; j < kVec; ++j) r.v[j] = from_f32<T>(v[j]);
   if (Full || i + kVec <= n) {
-    __builtin_memcpy(p + i, r, sizeof(r));
+    write4<Stream>(p + i, r);
   } else {
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
-      if (i + j < n) p[i + j] = r[j];
+      if (i + j < n) p[i + j] = r.v[j];
   }
 }
 
@@ -119,7 +143,7 @@ __device__ inline uint32_t block_max(uint32_t v) {
 static_assert(kStateBlock == 16 * kVec, "a block of states is 16 lanes");
 
 // One chunk.  Full: all kChunk elements are there, nothing is guarded.
-template <typename P, typename G, bool Bits8, bool Full>
+template <typename P, typename G, bool Bits8, bool Stream, bool Full>
 __device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float scale) {
   P* p = static_cast<P*>(a.param[c.tensor - a.first_tensor]) + c.start;
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
@@ -135,16 +159,16 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float sca
   for (int k = 0; k < kPasses; ++k) {
     const unsigned i = (k * kThreads + threadIdx.x) * kVec;
     if (!Full && i >= whole) break;   // states are held in whole blocks
-    load4<Full>(p, i, n, pv[k]);
-    load4<Full>(g, i, n, gv[k]);
+    load4<Full, Stream>(p, i, n, pv[k]);
+    load4<Full, Stream>(g, i, n, gv[k]);
     if constexpr (Bits8) {
-      __builtin_memcpy(&mc[k], __builtin_assume_aligned(m_code + i, 4), 4);
-      __builtin_memcpy(&rc[k], __builtin_assume_aligned(r_code + i, 4), 4);
+      mc[k] = __builtin_bit_cast(uint32_t, read4<Stream>(m_code + i));
+      rc[k] = __builtin_bit_cast(uint32_t, read4<Stream>(r_code + i));
       me[k] = m_exp[i / kStateBlock];
       re[k] = r_exp[i / kStateBlock];
     } else {
-      __builtin_memcpy(mv[k], __builtin_assume_aligned(m + i, 16), 16);
-      __builtin_memcpy(vv[k], __builtin_assume_aligned(v + i, 16), 16);
+      load4<true, Stream>(m, i, n, mv[k]);
+      load4<true, Stream>(v, i, n, vv[k]);
     }
   }
 #pragma unroll
@@ -216,29 +240,29 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float sca
           if (!(root[j] < float_of(kInf))) cr |= kRNan << (8 * j);
         }
       }
-      __builtin_memcpy(__builtin_assume_aligned(m_code + i, 4), &cm, 4);
-      __builtin_memcpy(__builtin_assume_aligned(r_code + i, 4), &cr, 4);
+      write4<Stream>(m_code + i, __builtin_bit_cast(Four<uint8_t>, cm));
+      write4<Stream>(r_code + i, __builtin_bit_cast(Four<uint8_t>, cr));
       if (threadIdx.x % 16 == 0) {
         m_exp[i / kStateBlock] = uint8_t(em);
         r_exp[i / kStateBlock] = uint8_t(er);
       }
     } else {
-      __builtin_memcpy(__builtin_assume_aligned(m + i, 16), mv[k], 16);
-      __builtin_memcpy(__builtin_assume_aligned(v + i, 16), vv[k], 16);
+      store4<true, Stream>(m, i, n, mv[k]);
+      store4<true, Stream>(v, i, n, vv[k]);
     }
-    store4<Full>(p, i, n, pv[k]);
+    store4<Full, Stream>(p, i, n, pv[k]);
   }
 }
 
-template <typename P, typename G, bool Bits8>
+template <typename P, typename G, bool Bits8, bool Stream>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
-  const Chunk c = a.chunks[blockIdx.x];
+  const Chunk c = a.chunks[gridDim.x - 1 - blockIdx.x];
   const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
   if (scale != scale) return;   // the gradients are not finite: the step is skipped
   if (c.n == kChunk)
-    adamw_chunk<P, G, Bits8, true>(a, c, scale);
+    adamw_chunk<P, G, Bits8, Stream, true>(a, c, scale);
   else
-    adamw_chunk<P, G, Bits8, false>(a, c, scale);
+    adamw_chunk<P, G, Bits8, Stream, false>(a, c, scale);
 }
 
 __device__ inline double block_sum(double v, double* lds) {
@@ -257,9 +281,13 @@ __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) 
   const Chunk c = a.chunks[blockIdx.x];
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
   float v[kPasses][kVec];
+  if (c.n == kChunk) {
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k)
-    load4<false>(g, (k * kThreads + threadIdx.x) * kVec, unsigned(c.n), v[k]);
+    for (int k = 0; k < kPasses; ++k) load4<true, false>(g, (k * kThreads + threadIdx.x) * kVec, kChunk, v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) load4<false, false>(g, (k * kThreads + threadIdx.x) * kVec, unsigned(c.n), v[k]);
+  }
   double s = 0;
 #pragma unroll
   for (int k = 0; k < kPasses; ++k)
@@ -305,25 +333,34 @@ __global__ __launch_bounds__(kThreads) void decode_states_kernel(const uint8_t* 
   }
 }
 
-template <typename P, typename G>
-hipError_t adamw_pg(const AdamwArgs& a, int n, bool bits8, hipStream_t s) {
-  if (bits8)
-    hipLaunchKernelGGL((adamw_kernel<P, G, true>), dim3(unsigned(n)), dim3(kThreads), 0, s, a);
+template <typename P, typename G, bool Bits8>
+void adamw_launch(const AdamwArgs& a, int n, bool stream, hipStream_t s) {
+  const dim3 grid{unsigned(n)}, block(kThreads);
+  if (stream)
+    hipLaunchKernelGGL((adamw_kernel<P, G, Bits8, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((adamw_kernel<P, G, false>), dim3(unsigned(n)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((adamw_kernel<P, G, Bits8, false>), grid, block, 0, s, a);
+}
+template <typename P, typename G>
+hipError_t adamw_pg(const AdamwArgs& a, int n, bool bits8, bool stream, hipStream_t s) {
+  if (bits8)
+    adamw_launch<P, G, true>(a, n, stream, s);
+  else
+    adamw_launch<P, G, false>(a, n, stream, s);
   return hipGetLastError();
 }
 template <typename P>
-hipError_t adamw_p(const AdamwArgs& a, int n, Elem grad, bool bits8, hipStream_t s) {
-  return grad == Elem::f32 ? adamw_pg<P, float>(a, n, bits8, s)
-         : grad == Elem::bf16 ? adamw_pg<P, Bf16>(a, n, bits8, s) : adamw_pg<P, F16>(a, n, bits8, s);
+hipError_t adamw_p(const AdamwArgs& a, int n, Elem grad, bool bits8, bool stream, hipStream_t s) {
+  return grad == Elem::f32 ? adamw_pg<P, float>(a, n, bits8, stream, s)
+         : grad == Elem::bf16 ? adamw_pg<P, Bf16>(a, n, bits8, stream, s) : adamw_pg<P, F16>(a, n, bits8, stream, s);
 }
 
 }  // namespace
 
-hipError_t launch_adamw(const AdamwArgs& a, int n_chunks, Elem param, Elem grad, bool bits8, hipStream_t s) {
-  return param == Elem::f32 ? adamw_p<float>(a, n_chunks, grad, bits8, s)
-         : param == Elem::bf16 ? adamw_p<Bf16>(a, n_chunks, grad, bits8, s) : adamw_p<F16>(a, n_chunks, grad, bits8, s);
+hipError_t launch_adamw(const AdamwArgs& a, int n_chunks, Elem param, Elem grad, bool bits8, bool stream,
+                        hipStream_t s) {
+  return param == Elem::f32 ? adamw_p<float>(a, n_chunks, grad, bits8, stream, s)
+         : param == Elem::bf16 ? adamw_p<Bf16>(a, n_chunks, grad, bits8, stream, s) : adamw_p<F16>(a, n_chunks, grad, bits8, stream, s);
 }
 
 hipError_t launch_grad_squares(const GradNormArgs& a, Elem grad, hipStream_t s) {

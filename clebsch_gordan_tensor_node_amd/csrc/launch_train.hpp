@@ -11,6 +11,11 @@ namespace cgtp {
 // Element types of the training operators (CGTP_F32, CGTP_BF16, CGTP_F16).
 enum class Elem : int { f32 = 0, bf16 = 1, f16 = 2 };
 
+// What the last-level cache holds.  A call that moves more has nothing of it left in the
+// caches when it ends: its accesses pass them by (non-temporal), which keeps the lines that
+// it writes from being written back during the next kernel.
+constexpr int64_t kCacheBytes = int64_t(256) << 20;
+
 // ---- normalisation -----------------------------------------------------------------
 
 // One normalised stretch of a row: a term "mul x l p" of an irreps row, or the whole row
@@ -45,6 +50,7 @@ struct NormCall {
   int64_t ld_x, ld_y, ld_g;   // elements from row to row
   float eps;
   int weight_f32;          // weight, bias and their gradients are fp32 (else x's type)
+  int stream;              // rows pass by the caches (set by the launchers)
 };
 
 hipError_t launch_norm_forward(const NormCall& c, const NormShape& p, Elem type, hipStream_t s);
@@ -56,7 +62,10 @@ hipError_t launch_norm_backward(const NormCall& c, const NormShape& p, Elem type
 // ---- optimiser ---------------------------------------------------------------------
 
 constexpr int kStateBlock = 64;          // elements that share an exponent in 8-bit states
-constexpr int kChunk = 4096;             // most elements of one chunk
+// Most elements of one chunk.  A step of 50 M elements with 32-bit states took 207, 204 and
+// 210 us with 4096, 2048 and 1024, one of 37 M with 8-bit states 112, 106 and 103 us, the
+// gradient norm's first pass over 50 M 34, 34 and 52 us.
+constexpr int kChunk = 2048;
 constexpr int kTensorsPerLaunch = 232;   // tensors whose pointers fit the kernel arguments
 
 // A stretch of one tensor that one workgroup handles.
@@ -94,7 +103,10 @@ struct GradNormArgs {
   const void* grad[kTensorsPerLaunch];
 };
 
-hipError_t launch_adamw(const AdamwArgs& a, int n_chunks, Elem param, Elem grad, bool bits8, hipStream_t s);
+// stream: params, gradients and states pass by the caches (a step that moves more than
+// they hold).
+hipError_t launch_adamw(const AdamwArgs& a, int n_chunks, Elem param, Elem grad, bool bits8, bool stream,
+                        hipStream_t s);
 hipError_t launch_grad_squares(const GradNormArgs& a, Elem grad, hipStream_t s);
 // out[0] = scale * sqrt(sum of part), out[1] = scale * min(1, max_norm / out[0]), NaN
 // where out[0] is not finite; scale = *grad_scale (1 if null).

@@ -331,12 +331,13 @@ int check_tensors(cgtp_params_t P, int dtype, const void* const* t, const char* 
 }
 
 // Calls launch(first tensor, tensors, first chunk, chunks) for ranges of tensors whose
-// pointers fit one launch's kernel arguments.
+// pointers fit one launch's kernel arguments, from the last range to the first if `back`.
 template <typename F>
-int for_launches(cgtp_params_t P, F&& launch) {
-  const int n = int(P->numel.size());
-  for (int t = 0; t < n; t += kTensorsPerLaunch) {
-    const int to = std::min(n, t + kTensorsPerLaunch), c0 = P->first_chunk[t], c1 = P->first_chunk[to];
+int for_launches(cgtp_params_t P, bool back, F&& launch) {
+  const int n = int(P->numel.size()), ranges = (n + kTensorsPerLaunch - 1) / kTensorsPerLaunch;
+  for (int r = 0; r < ranges; ++r) {
+    const int t = (back ? ranges - 1 - r : r) * kTensorsPerLaunch, to = std::min(n, t + kTensorsPerLaunch);
+    const int c0 = P->first_chunk[t], c1 = P->first_chunk[to];
     if (c1 > c0) CGTP_HIP(launch(t, to - t, c0, c1 - c0));
   }
   return ok();
@@ -362,12 +363,15 @@ int adamw_step(cgtp_params_t P, int param_dtype, void* const* params, int grad_d
   a.step_size = float(lr / (1 - std::pow(beta1, double(step))));
   a.inv_root = float(1 / std::sqrt(1 - std::pow(beta2, double(step))));
   a.eps = float(eps);
-  return for_launches(P, [&](int t, int n, int c0, int chunks) {
+  const int64_t each = 2 * elem_size(param_dtype) + elem_size(grad_dtype) + (bits8 ? 4 : 16);
+  const bool stream_by = P->state_elems * each > kCacheBytes;
+  return for_launches(P, true, [&](int t, int n, int c0, int chunks) {
     a.chunks = P->d_chunks + c0;
     a.first_tensor = t;
     std::memcpy(a.param, params + t, size_t(n) * sizeof(void*));
     std::memcpy(a.grad, grads + t, size_t(n) * sizeof(void*));
-    return launch_adamw(a, chunks, Elem(param_dtype), Elem(grad_dtype), bits8, static_cast<hipStream_t>(stream));
+    return launch_adamw(a, chunks, Elem(param_dtype), Elem(grad_dtype), bits8, stream_by,
+                        static_cast<hipStream_t>(stream));
   });
 }
 
@@ -435,7 +439,7 @@ int cgtp_grad_norm(cgtp_params_t P, int grad_dtype, const void* const* grads, co
   if (!aligned(workspace, 256)) return fail(CGTP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   double* part = static_cast<double*>(workspace);
   GradNormArgs a{};
-  int rc = for_launches(P, [&](int t, int n, int c0, int count) {
+  int rc = for_launches(P, false, [&](int t, int n, int c0, int count) {
     a.chunks = P->d_chunks + c0;
     a.part = part + c0;
     a.first_tensor = t;
