@@ -17,6 +17,8 @@
 // stretch that V does not divide is moved back to end with the stretch; the elements that
 // it repeats are left out of the sums, and written twice with the same value.
 // A workgroup keeps its weights in registers over all its rows (workgroup, then stride).
+#include <algorithm>
+
 #include "elem.hpp"
 #include "launch_train.hpp"
 
@@ -39,6 +41,7 @@ template <int Cap>
 struct NormArgs {
   NormCall c;
   int32_t n_terms;
+  int32_t direct;             // backward: one workgroup per term, which writes the gradients itself
   int32_t first_block[Cap];   // of each term (INT32_MAX past the last)
   TermArgs term[Cap];
 };
@@ -191,18 +194,12 @@ template <typename T, int V, int C>
 struct Row {
   Vec<T, V> c[C];
 };
-template <typename T, int V, int G, int C>
-__device__ inline Row<T, V, C> read_row(const Place<V, G, C>& p, const T* row, bool stream) {
+template <bool Stream, typename T, int V, int G, int C>
+__device__ inline Row<T, V, C> read_row(const Place<V, G, C>& p, const T* row) {
   Row<T, V, C> r = {};
-  if (stream) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (p.has(c)) r.c[c] = load_vec<true, T, V>(row + p.at(c));
-  } else {
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (p.has(c)) r.c[c] = load_vec<false, T, V>(row + p.at(c));
-  }
+  for (int c = 0; c < C; ++c)
+    if (p.has(c)) r.c[c] = load_vec<Stream, T, V>(row + p.at(c));
   return r;
 }
 template <typename T, int V, int C>
@@ -212,18 +209,15 @@ __device__ inline void widen(const Row<T, V, C>& r, float (&x)[C][V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) x[c][j] = to_f32(r.c[c].v[j]);
 }
-template <typename T, int V, int G, int C>
-__device__ inline void store_row(const Place<V, G, C>& p, T* row, const float (&y)[C][V], bool stream) {
+template <bool Stream, typename T, int V, int G, int C>
+__device__ inline void store_row(const Place<V, G, C>& p, T* row, const float (&y)[C][V]) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
     if (p.has(c)) {
       Vec<T, V> r;
 #pragma unroll
       for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(y[c][j]);
-      if (stream)
-        store_vec<true, T, V>(row + p.at(c), r);
-      else
-        store_vec<false, T, V>(row + p.at(c), r);
+      store_vec<Stream, T, V>(row + p.at(c), r);
     }
 }
 // Sum of f(c, j) over the lane's own elements.
@@ -260,7 +254,7 @@ __device__ inline void load_weights(const Place<V, G, C>& p, const void* w, int 
     }
 }
 
-template <typename T, int V, int G, int C>
+template <bool Stream, typename T, int V, int G, int C>
 __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
   constexpr int kGroups = kThreads / G;
   const Place<V, G, C> p(t.len);
@@ -271,7 +265,7 @@ __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_term
   load_weights<T>(p, centred ? a.bias : nullptr, a.weight_f32, t.b_off, t, 0.0f, b);
   int turn = 0;
   for (int64_t r = int64_t(block) * kGroups + threadIdx.x / G; r < a.rows; r += int64_t(t.n_blocks) * kGroups) {
-    widen(read_row(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off, a.stream), x);
+    widen(read_row<Stream>(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off), x);
     float mu = 0;
     if (centred) mu = group_sum<G>(own_sum(p, [&](int c, int j) { return x[c][j]; }), lds, turn) * inv;
     const float s2 = group_sum<G>(own_sum(p, [&](int c, int j) { return (x[c][j] - mu) * (x[c][j] - mu); }), lds, turn);
@@ -280,7 +274,7 @@ __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_term
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) x[c][j] = (x[c][j] - mu) * rstd * w[c][j] + b[c][j];
-    store_row(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, x, a.stream);
+    store_row<Stream>(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, x);
     if (a.stats && p.lane == 0) {
       a.stats[r * n_terms + index] = mu;
       a.stats[(a.rows + r) * n_terms + index] = rstd;
@@ -288,8 +282,9 @@ __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_term
   }
 }
 
-template <typename T, int V, int G, int C>
-__device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
+template <bool Stream, typename T, int V, int G, int C>
+__device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds,
+                                bool direct) {
   constexpr int kGroups = kThreads / G;
   const Place<V, G, C> p(t.len);
   const bool centred = t.b_off >= 0;
@@ -302,8 +297,8 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
     for (int j = 0; j < V; ++j) gw[c][j] = gb[c][j] = 0;
   int turn = 0;
   for (int64_t r = int64_t(block) * kGroups + threadIdx.x / G; r < a.rows; r += int64_t(t.n_blocks) * kGroups) {
-    widen(read_row(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off, a.stream), x);
-    widen(read_row(p, static_cast<const T*>(a.grad_out) + r * a.ld_g + t.off, a.stream), g);
+    widen(read_row<Stream>(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off), x);
+    widen(read_row<Stream>(p, static_cast<const T*>(a.grad_out) + r * a.ld_g + t.off), g);
     const float mu = a.stats[r * n_terms + index], rstd = a.stats[(a.rows + r) * n_terms + index];
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -324,10 +319,10 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < V; ++j) g[c][j] = (g[c][j] - sa - x[c][j] * sh) * rstd;
-    store_row(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, g, a.stream);
+    store_row<Stream>(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, g);
   }
   if (!a.grad_weight && !a.grad_bias) return;
-  // the workgroup's sums: its groups' added in LDS, one row of `part`
+  // the workgroup's sums: its groups' added in LDS, one row of `part`, or the gradients
   float* part = a.part + t.part + int64_t(block) * t.len;
   for (int k = 0; k < (centred ? 2 : 1); ++k, part += int64_t(t.n_blocks) * t.len) {
     __syncthreads();
@@ -338,10 +333,17 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
       for (int j = 0; j < V; ++j)
         if (p.has(c) && j >= p.skip(c)) mine[p.at(c) + j] = k ? gb[c][j] : gw[c][j];
     __syncthreads();
-    for (int e = threadIdx.x; e < t.len; e += kThreads) {
+    void* out = k ? a.grad_bias : a.grad_weight;
+    if (direct && !out) continue;
+    const int d = direct ? t.d : 1;
+    for (int e = threadIdx.x; e < t.len / d; e += kThreads) {
       float s = 0;
-      for (int q = 0; q < kGroups; ++q) s += lds[q * t.len + e];
-      part[e] = s;
+      for (int m = 0; m < d; ++m)
+        for (int q = 0; q < kGroups; ++q) s += lds[q * t.len + e * d + m];
+      if (direct)
+        store_either<T>(out, a.weight_f32, (k ? t.b_off : t.w_off) + e, s);
+      else
+        part[e] = s;
     }
   }
 }
@@ -431,29 +433,29 @@ __device__ inline int term_of(const NormArgs<Cap>& a) {
 
 // One launch for all terms; a kernel holds the variants of up to MaxE elements per lane,
 // so that short rows do not pay for long ones' registers.
-#define CGTP_NORM_VARIANTS(FN)                                                            \
-  constexpr int V = 16 / int(sizeof(T));                                                  \
-  switch (t.variant) {                                                                    \
-    case kElem16: FN<T, 1, 16, 1>(a.c, t, a.n_terms, k, block, lds); break;               \
-    case kG16C1: FN<T, V, 16, 1>(a.c, t, a.n_terms, k, block, lds); break;                \
-    case kG64C1: FN<T, V, 64, 1>(a.c, t, a.n_terms, k, block, lds); break;                \
-    default:                                                                              \
-      if constexpr (MaxE >= 2 * V) {                                                      \
-        if (t.variant == kG16C2) FN<T, V, 16, 2>(a.c, t, a.n_terms, k, block, lds);       \
-        if (t.variant == kG64C2) FN<T, V, 64, 2>(a.c, t, a.n_terms, k, block, lds);       \
-        if (t.variant == kG256C2) FN<T, V, 256, 2>(a.c, t, a.n_terms, k, block, lds);     \
-      }                                                                                   \
-      if constexpr (MaxE >= 4 * V) {                                                      \
-        if (t.variant == kG64C4) FN<T, V, 64, 4>(a.c, t, a.n_terms, k, block, lds);       \
-        if (t.variant == kG256C4) FN<T, V, 256, 4>(a.c, t, a.n_terms, k, block, lds);     \
-      }                                                                                   \
-      if constexpr (MaxE >= 8 * V) {                                                      \
-        if (t.variant == kG64C8) FN<T, V, 64, 8>(a.c, t, a.n_terms, k, block, lds);       \
-        if (t.variant == kG256C8) FN<T, V, 256, 8>(a.c, t, a.n_terms, k, block, lds);     \
-      }                                                                                   \
+#define CGTP_NORM_VARIANTS(FN, ...)                                                                          \
+  constexpr int V = 16 / int(sizeof(T));                                                                     \
+  switch (t.variant) {                                                                                       \
+    case kElem16: FN<Stream, T, 1, 16, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;           \
+    case kG16C1: FN<Stream, T, V, 16, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;            \
+    case kG64C1: FN<Stream, T, V, 64, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;            \
+    default:                                                                                                 \
+      if constexpr (MaxE >= 2 * V) {                                                                         \
+        if (t.variant == kG16C2) FN<Stream, T, V, 16, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
+        if (t.variant == kG64C2) FN<Stream, T, V, 64, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
+        if (t.variant == kG256C2) FN<Stream, T, V, 256, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
+      }                                                                                                      \
+      if constexpr (MaxE >= 4 * V) {                                                                         \
+        if (t.variant == kG64C4) FN<Stream, T, V, 64, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
+        if (t.variant == kG256C4) FN<Stream, T, V, 256, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
+      }                                                                                                      \
+      if constexpr (MaxE >= 8 * V) {                                                                         \
+        if (t.variant == kG64C8) FN<Stream, T, V, 64, 8>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
+        if (t.variant == kG256C8) FN<Stream, T, V, 256, 8>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
+      }                                                                                                      \
   }
 
-template <typename T, int MaxE, int Cap>
+template <typename T, int MaxE, int Cap, bool Stream>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs<Cap> a) {
   __shared__ float lds[16];
   const int k = term_of(a);
@@ -463,60 +465,71 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs<Cap> a) {
   CGTP_NORM_VARIANTS(fwd_rows)
 }
 
-template <typename T, int MaxE, int Cap>
+template <typename T, int MaxE, int Cap, bool Stream>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs<Cap> a) {
   __shared__ float lds[kThreads * MaxE];
   const int k = term_of(a);
   const TermArgs& t = a.term[k];
   const int block = int(blockIdx.x) - a.first_block[k];
   if (t.variant == kWide) return bwd_wide<T>(a.c, t, a.n_terms, k, block, lds);
-  CGTP_NORM_VARIANTS(bwd_rows)
+  CGTP_NORM_VARIANTS(bwd_rows, a.direct)
 }
 
 // The weight's and bias's gradients from the workgroups' sums, in a fixed order.  A
-// workgroup takes whole channels, at most 16 elements; 64 slices of its threads each add
-// every 64th partial sum (all their loads in flight at once: the kernel is a chain of
-// memory latencies, not of bytes), DPP and LDS join the slices, then a channel's components.
+// workgroup takes whole channels, at most Tile elements; each slice of Tile of its threads
+// adds every n-th partial sum, 16 loads of each kind in flight at once (the kernel is a
+// chain of memory latencies, not of bytes), then LDS joins the slices and a channel's
+// components.
 constexpr int kSumThreads = 1024;
-constexpr int kTile = 16;
-constexpr int kSumWaves = kSumThreads / kWave;
+constexpr int kInFlight = 16;
 
-template <typename T, int Cap>
+template <typename T, int Cap, int Tile>
 __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) {
-  __shared__ float lds[2][kSumWaves][kTile];
-  __shared__ float col[2][kTile];
+  __shared__ float lds[2][kSumThreads / kWave][Tile];
+  __shared__ float col[2][Tile];
   const int k = term_of(a);
   const TermArgs& t = a.term[k];
   const bool want_b = t.b_off >= 0 && a.c.grad_bias;
-  const int tile = kTile / t.d * t.d, lane = threadIdx.x % kTile;
-  const int first = (int(blockIdx.x) - a.first_block[k]) * tile;
+  const int tile = Tile / t.d * t.d, lane = threadIdx.x % Tile;
+  const int first = (int(blockIdx.x) - a.first_block[k]) * tile, slices = int(blockDim.x) / Tile;
   float sw = 0, sb = 0;
   if (lane < tile && first + lane < t.len) {
     const float* part = a.c.part + t.part + first + lane;
-    const int64_t other = int64_t(t.n_blocks) * t.len;
-#pragma unroll 8
-    for (int b = threadIdx.x / kTile; b < t.n_blocks; b += kSumThreads / kTile) sw += part[int64_t(b) * t.len];
-    if (want_b) {
-#pragma unroll 8
-      for (int b = threadIdx.x / kTile; b < t.n_blocks; b += kSumThreads / kTile) sb += part[other + int64_t(b) * t.len];
+    const float* part_b = part + int64_t(t.n_blocks) * t.len;
+    for (int b0 = threadIdx.x / Tile; b0 < t.n_blocks; b0 += slices * kInFlight) {
+      // past the end the last one is read again and left out: loads under a condition wait
+      // for one another
+      float vw[kInFlight], vb[kInFlight];
+#pragma unroll
+      for (int q = 0; q < kInFlight; ++q) vw[q] = part[int64_t(min(b0 + q * slices, t.n_blocks - 1)) * t.len];
+      if (want_b) {
+#pragma unroll
+        for (int q = 0; q < kInFlight; ++q) vb[q] = part_b[int64_t(min(b0 + q * slices, t.n_blocks - 1)) * t.len];
+#pragma unroll
+        for (int q = 0; q < kInFlight; ++q) sb += b0 + q * slices < t.n_blocks ? vb[q] : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < kInFlight; ++q) sw += b0 + q * slices < t.n_blocks ? vw[q] : 0.0f;
     }
   }
-  sw += __shfl_xor(sw, 16);
-  sb += __shfl_xor(sb, 16);
-  sw += __shfl_xor(sw, 32);
-  sb += __shfl_xor(sb, 32);
-  if (threadIdx.x % kWave < kTile) {
+#pragma unroll
+  for (int x = Tile; x < kWave; x *= 2) {
+    sw += __shfl_xor(sw, x);
+    sb += __shfl_xor(sb, x);
+  }
+  if (threadIdx.x % kWave < Tile) {
     lds[0][threadIdx.x / kWave][lane] = sw;
     lds[1][threadIdx.x / kWave][lane] = sb;
   }
   __syncthreads();
-  if (threadIdx.x < 2 * kSumWaves * kTile) {   // one lane per wave's sum, 16 of a column beside one another
-    const int q = threadIdx.x / (kSumWaves * kTile), c = threadIdx.x / kSumWaves % kTile;
-    const float v = lanes_sum<kSumWaves>(lds[q][threadIdx.x % kSumWaves][c]);
-    if (threadIdx.x % kSumWaves == 0) col[q][c] = v;
+  const int q = threadIdx.x / Tile;
+  if (q < 2) {
+    float v = 0;
+    for (unsigned w = 0; w < blockDim.x / kWave; ++w) v += lds[q][w][lane];
+    col[q][lane] = v;
   }
   __syncthreads();
-  const int q = threadIdx.x / kTile, ch = first / t.d + lane;
+  const int ch = first / t.d + lane;
   if (q < 2 && lane < tile / t.d && ch < t.len / t.d) {
     float v = 0;
     for (int m = 0; m < t.d; ++m) v += col[q][lane * t.d + m];
@@ -525,27 +538,43 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) 
   }
 }
 
-// Workgroups that fill the card, shared among the terms by their length.
-constexpr int kForwardBlocks = 2048;
-constexpr int kBackwardBlocks = 1024;
+// Workgroups of a launch, shared among the terms by their length: enough to keep the
+// memory busy, which takes more of them where every access goes to HBM, and in the
+// backward no more, since each leaves a row of partial sums.  Measured: forward of 114688 x
+// 1312 fp32 232, 222 and 219 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 38, 36
+// and 41; backward and sums of 768 x 9088 (cached) 23.3, 23.3, 25.0 and 27.8 us with 512,
+// 768, 1024 and 1536, of 32768 x 704 82, 67, 60 and 56.
+constexpr int kForwardBlocks = 2048, kForwardBlocksStream = 4096;
+constexpr int kBackwardBlocks = 768, kBackwardBlocksStream = 1536;
 
 int64_t share(int64_t total, const NormShape& p, int k) {
   const int64_t s = total * p.terms[k].len / p.features;
   return s > 0 ? s : 1;
 }
 
-// The most workgroups of a term in the backward, whatever the element type.
-int64_t most_backward_blocks(int64_t rows, const NormShape& p, int k) {
-  const int64_t s = share(kBackwardBlocks, p, k);
-  return rows < s ? (rows > 0 ? rows : 1) : s;
+// Rows that outgrow the last-level cache pass it by, in plans of up to kCapSmall terms.
+template <int Cap>
+bool streams(const NormCall& c, const NormShape& p, int elem_bytes, int tensors) {
+  return Cap == kCapSmall && c.rows * p.features * elem_bytes * tensors > kCacheBytes;
 }
 
-// Fills a launch's terms with `total` workgroups at most; returns their number and the
+// Rows so few that one workgroup per term takes them all, in at most four turns: it then
+// writes the weight's and bias's gradients itself.
+bool few_rows(int64_t rows, const NormShape& p, int elem_bytes) {
+  for (int k = 0; k < p.n_terms; ++k) {
+    const int v = variant_of(p.terms[k].len, elem_bytes, true);
+    if (v == kWide || rows > 4 * groups_of(v)) return false;
+  }
+  return true;
+}
+
+// Fills a launch's terms with about `total` workgroups; returns their number and the
 // largest number of elements per lane.
 template <int Cap>
-int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, int elem_bytes, bool backward, int* max_e) {
+int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, int elem_bytes, bool backward, int64_t total,
+         int* max_e) {
   a.c = c;
-  a.c.stream = c.rows * p.features * elem_bytes * (backward ? 3 : 2) > kCacheBytes;
+  a.direct = backward && few_rows(c.rows, p, elem_bytes);
   a.n_terms = p.n_terms;
   int64_t part = 0;
   int at = 0;
@@ -555,7 +584,7 @@ int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, int elem_bytes
     const NormTerm& t = p.terms[k];
     const int v = variant_of(t.len, elem_bytes, backward), g = groups_of(v);
     const int64_t want = (c.rows + g - 1) / g > 0 ? (c.rows + g - 1) / g : 1;
-    const int64_t most = backward ? most_backward_blocks(c.rows, p, k) : share(kForwardBlocks, p, k);
+    const int64_t most = a.direct ? 1 : share(total, p, k);
     const int n = int(want < most ? want : most);
     a.term[k] = TermArgs{t.off, t.len, t.d, t.w_off, t.b_off, v, n,
                          t.d > 1 ? uint32_t(((uint64_t(1) << 32) + uint64_t(t.d) - 1) / uint64_t(t.d)) : 0u, part};
@@ -567,17 +596,37 @@ int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, int elem_bytes
   return at;
 }
 
+template <typename T, int Cap, bool Stream>
+void forward(const NormArgs<Cap>& a, int blocks, int max_e, hipStream_t s) {
+  const dim3 grid{unsigned(blocks)}, block(kThreads);
+  if (max_e <= 8)
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 8, Cap, Stream>), grid, block, 0, s, a);
+  else if (max_e <= 16)
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 16, Cap, Stream>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 32, Cap, Stream>), grid, block, 0, s, a);
+}
+template <typename T, int Cap, bool Stream>
+void backward(const NormArgs<Cap>& a, int blocks, int max_e, hipStream_t s) {
+  const dim3 grid{unsigned(blocks)}, block(kThreads);
+  if (max_e <= 8)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 8, Cap, Stream>), grid, block, 0, s, a);
+  else if (max_e <= 16)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 16, Cap, Stream>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 32, Cap, Stream>), grid, block, 0, s, a);
+}
+
 template <typename T, int Cap>
 hipError_t forward(const NormCall& c, const NormShape& p, hipStream_t s) {
   NormArgs<Cap> a;
   int max_e;
-  const dim3 grid(unsigned(fill(a, c, p, int(sizeof(T)), false, &max_e))), block(kThreads);
-  if (max_e <= 8)
-    hipLaunchKernelGGL((norm_fwd_kernel<T, 8, Cap>), grid, block, 0, s, a);
-  else if (max_e <= 16)
-    hipLaunchKernelGGL((norm_fwd_kernel<T, 16, Cap>), grid, block, 0, s, a);
+  const bool stream = streams<Cap>(c, p, int(sizeof(T)), 2);
+  const int blocks = fill(a, c, p, int(sizeof(T)), false, stream ? kForwardBlocksStream : kForwardBlocks, &max_e);
+  if (stream)
+    forward<T, Cap, Cap == kCapSmall>(a, blocks, max_e, s);
   else
-    hipLaunchKernelGGL((norm_fwd_kernel<T, 32, Cap>), grid, block, 0, s, a);
+    forward<T, Cap, false>(a, blocks, max_e, s);
   return hipGetLastError();
 }
 
@@ -585,21 +634,35 @@ template <typename T, int Cap>
 hipError_t backward(const NormCall& c, const NormShape& p, hipStream_t s) {
   NormArgs<Cap> a;
   int max_e;
-  const dim3 grid(unsigned(fill(a, c, p, int(sizeof(T)), true, &max_e))), block(kThreads);
-  if (max_e <= 8)
-    hipLaunchKernelGGL((norm_bwd_kernel<T, 8, Cap>), grid, block, 0, s, a);
-  else if (max_e <= 16)
-    hipLaunchKernelGGL((norm_bwd_kernel<T, 16, Cap>), grid, block, 0, s, a);
+  const bool stream = streams<Cap>(c, p, int(sizeof(T)), 3);
+  const int blocks = fill(a, c, p, int(sizeof(T)), true, stream ? kBackwardBlocksStream : kBackwardBlocks, &max_e);
+  if (stream)
+    backward<T, Cap, Cap == kCapSmall>(a, blocks, max_e, s);
   else
-    hipLaunchKernelGGL((norm_bwd_kernel<T, 32, Cap>), grid, block, 0, s, a);
-  if (c.grad_weight || c.grad_bias) {
+    backward<T, Cap, false>(a, blocks, max_e, s);
+  if ((c.grad_weight || c.grad_bias) && !a.direct) {
+    // Wide tiles read whole lines (a tile that ends inside one has it fetched again by
+    // another die's L2), narrow ones spread short stretches over more workgroups: 9088
+    // columns took 10.1 us in tiles of 16 and 5.4 in tiles of 64, 481 columns 6.6 and 10.2.
+    int tiles = 0, most = 0;
+    for (int k = 0; k < p.n_terms; ++k) {
+      tiles += p.terms[k].len / 64;
+      most = max(most, a.term[k].n_blocks);
+    }
+    const int wide = tiles >= 16 ? 64 : 16;
     int at = 0;
     for (int k = 0; k < p.n_terms; ++k) {
-      const int tile = kTile / p.terms[k].d * p.terms[k].d;
+      const int tile = wide / p.terms[k].d * p.terms[k].d;
       a.first_block[k] = at;
       at += (p.terms[k].len + tile - 1) / tile;
     }
-    hipLaunchKernelGGL((norm_sum_kernel<T, Cap>), dim3(unsigned(at)), dim3(kSumThreads), 0, s, a);
+    // as many slices as keep every load in flight, two at least
+    const int want = (most + kInFlight - 1) / kInFlight * wide;
+    const int threads = want <= 128 ? 128 : want <= 256 ? 256 : want <= 512 ? 512 : kSumThreads;
+    if (wide == 64)
+      hipLaunchKernelGGL((norm_sum_kernel<T, Cap, 64>), dim3(unsigned(at)), dim3(unsigned(threads)), 0, s, a);
+    else
+      hipLaunchKernelGGL((norm_sum_kernel<T, Cap, 16>), dim3(unsigned(at)), dim3(unsigned(threads)), 0, s, a);
   }
   return hipGetLastError();
 }
@@ -621,9 +684,11 @@ hipError_t launch_norm_forward(const NormCall& c, const NormShape& p, Elem type,
 }
 
 size_t norm_part_floats(int64_t rows, const NormShape& p) {
+  if (few_rows(rows, p, 2) && few_rows(rows, p, 4)) return 0;
   size_t n = 0;
   for (int k = 0; k < p.n_terms; ++k)
-    n += size_t(most_backward_blocks(rows, p, k)) * size_t(p.terms[k].len) * (p.terms[k].b_off >= 0 ? 2 : 1);
+    n += size_t(std::min(std::max<int64_t>(rows, 1), share(kBackwardBlocksStream, p, k))) * size_t(p.terms[k].len) *
+         (p.terms[k].b_off >= 0 ? 2 : 1);
   return n;
 }
 

@@ -274,27 +274,44 @@ __device__ inline double block_sum(double v, double* lds) {
   return s;
 }
 
-// Squares in fp64: no gradient's square overflows or underflows.
-template <typename G>
-__global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) {
-  __shared__ double lds[kThreads / 64];
-  const Chunk c = a.chunks[blockIdx.x];
+// The sum of a chunk's squares over the lanes of one wave (Lanes = 64) or of a workgroup.
+// In fp64: no gradient's square overflows or underflows.
+template <int Lanes, typename G>
+__device__ inline double chunk_squares(const GradNormArgs& a, int index) {
+  constexpr int kReads = kChunk / (Lanes * kVec);
+  const Chunk c = a.chunks[index];
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
-  float v[kPasses][kVec];
+  const unsigned lane = threadIdx.x % Lanes;
+  float v[kReads][kVec];
   if (c.n == kChunk) {
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) load4<true, false>(g, (k * kThreads + threadIdx.x) * kVec, kChunk, v[k]);
+    for (int k = 0; k < kReads; ++k) load4<true, false>(g, (k * Lanes + lane) * kVec, kChunk, v[k]);
   } else {
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) load4<false, false>(g, (k * kThreads + threadIdx.x) * kVec, unsigned(c.n), v[k]);
+    for (int k = 0; k < kReads; ++k) load4<false, false>(g, (k * Lanes + lane) * kVec, unsigned(c.n), v[k]);
   }
   double s = 0;
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k)
+  for (int k = 0; k < kReads; ++k)
 #pragma unroll
     for (int j = 0; j < kVec; ++j) s += double(v[k][j]) * double(v[k][j]);
+  return s;
+}
+
+template <typename G>
+__global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) {
+  __shared__ double lds[kThreads / 64];
+  double s = 0;
+  for (int c = blockIdx.x; c < a.n_chunks; c += int(gridDim.x)) s += chunk_squares<kThreads, G>(a, c);
   s = block_sum(s, lds);
   if (threadIdx.x == 0) a.part[blockIdx.x] = s;
+}
+
+__device__ inline void write_norm(double sum, const float* grad_scale, float max_norm, float* out) {
+  const float scale = grad_scale ? *grad_scale : 1.0f;
+  const float norm = float(sqrt(sum) * fabs(double(scale)));
+  out[0] = norm;
+  out[1] = norm < __builtin_inff() ? (norm > max_norm ? scale * (max_norm / norm) : scale) : nan();
 }
 
 __global__ __launch_bounds__(kFinish) void grad_norm_kernel(const double* part, int n, const float* grad_scale,
@@ -304,12 +321,18 @@ __global__ __launch_bounds__(kFinish) void grad_norm_kernel(const double* part, 
 #pragma unroll 8
   for (int i = threadIdx.x; i < n; i += kFinish) s += part[i];
   s = block_sum(s, lds);
-  if (threadIdx.x == 0) {
-    const float scale = grad_scale ? *grad_scale : 1.0f;
-    const float norm = float(sqrt(s) * fabs(double(scale)));
-    out[0] = norm;
-    out[1] = norm < __builtin_inff() ? (norm > max_norm ? scale * (max_norm / norm) : scale) : __builtin_nanf("");
-  }
+  if (threadIdx.x == 0) write_norm(s, grad_scale, max_norm, out);
+}
+
+// Small sets: a chunk to each wave of one workgroup, and the norm in the same launch.
+template <typename G>
+__global__ __launch_bounds__(kFinish) void grad_norm_small_kernel(GradNormArgs a, const float* grad_scale,
+                                                                  float max_norm, float* out) {
+  __shared__ double lds[kFinish / 64];
+  double s = 0;
+  for (int c = threadIdx.x / 64; c < a.n_chunks; c += kFinish / 64) s += chunk_squares<64, G>(a, c);
+  s = block_sum(s, lds);
+  if (threadIdx.x == 0) write_norm(s, grad_scale, max_norm, out);
 }
 
 // n is a multiple of kStateBlock; 8 elements a lane.
@@ -364,7 +387,7 @@ hipError_t launch_adamw(const AdamwArgs& a, int n_chunks, Elem param, Elem grad,
 }
 
 hipError_t launch_grad_squares(const GradNormArgs& a, Elem grad, hipStream_t s) {
-  const dim3 grid{unsigned(a.n_chunks)}, block(kThreads);
+  const dim3 grid{unsigned(square_blocks(a.n_chunks))}, block(kThreads);
   if (grad == Elem::f32)
     hipLaunchKernelGGL(grad_squares_kernel<float>, grid, block, 0, s, a);
   else if (grad == Elem::bf16)
@@ -377,6 +400,18 @@ hipError_t launch_grad_squares(const GradNormArgs& a, Elem grad, hipStream_t s) 
 hipError_t launch_grad_norm_finish(const double* part, int n, const float* grad_scale, float max_norm, float* out,
                                    hipStream_t s) {
   hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kFinish), 0, s, part, n, grad_scale, max_norm, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_norm_small(const GradNormArgs& a, Elem grad, const float* grad_scale, float max_norm, float* out,
+                                  hipStream_t s) {
+  const dim3 grid(1), block(kFinish);
+  if (grad == Elem::f32)
+    hipLaunchKernelGGL(grad_norm_small_kernel<float>, grid, block, 0, s, a, grad_scale, max_norm, out);
+  else if (grad == Elem::bf16)
+    hipLaunchKernelGGL(grad_norm_small_kernel<Bf16>, grid, block, 0, s, a, grad_scale, max_norm, out);
+  else
+    hipLaunchKernelGGL(grad_norm_small_kernel<F16>, grid, block, 0, s, a, grad_scale, max_norm, out);
   return hipGetLastError();
 }
 

@@ -50,7 +50,6 @@ struct NormCall {
   int64_t ld_x, ld_y, ld_g;   // elements from row to row
   float eps;
   int weight_f32;          // weight, bias and their gradients are fp32 (else x's type)
-  int stream;              // rows pass by the caches (set by the launchers)
 };
 
 hipError_t launch_norm_forward(const NormCall& c, const NormShape& p, Elem type, hipStream_t s);
@@ -97,7 +96,7 @@ static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments are limited to 4 KiB"
 
 struct GradNormArgs {
   const Chunk* chunks;
-  double* part;                  // [chunks of the launch]
+  double* part;                  // one for each workgroup of the launch
   int32_t first_tensor;
   int32_t n_chunks;
   const void* grad[kTensorsPerLaunch];
@@ -107,11 +106,18 @@ struct GradNormArgs {
 // they hold).
 hipError_t launch_adamw(const AdamwArgs& a, int n_chunks, Elem param, Elem grad, bool bits8, bool stream,
                         hipStream_t s);
+// Workgroups (and partial sums) of launch_grad_squares over n chunks.
+constexpr int kSquareBlocks = 4096;
+constexpr int square_blocks(int n) { return n < kSquareBlocks ? n : kSquareBlocks; }
 hipError_t launch_grad_squares(const GradNormArgs& a, Elem grad, hipStream_t s);
 // out[0] = scale * sqrt(sum of part), out[1] = scale * min(1, max_norm / out[0]), NaN
 // where out[0] is not finite; scale = *grad_scale (1 if null).
 hipError_t launch_grad_norm_finish(const double* part, int n, const float* grad_scale, float max_norm, float* out,
                                    hipStream_t s);
+// Both in one launch of one workgroup, for at most kSmallChunks chunks.
+constexpr int kSmallChunks = 32;
+hipError_t launch_grad_norm_small(const GradNormArgs& a, Elem grad, const float* grad_scale, float max_norm, float* out,
+                                  hipStream_t s);
 // Values of n coded states in bf16: m and r = sqrt(v).
 hipError_t launch_decode_states(const uint8_t* m_code, const uint8_t* r_code, const uint8_t* m_exp,
                                 const uint8_t* r_exp, int64_t n, void* m, void* r, hipStream_t s);

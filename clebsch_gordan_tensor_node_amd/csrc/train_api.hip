@@ -121,7 +121,7 @@ int norm_backward(const NormShape& p, int dtype, int64_t rows, const void* grad_
     return fail(CGTP_ERR_INVALID_ARG, "misaligned pointer");
   if (grad_weight || grad_bias) {
     const size_t need = norm_part_floats(rows, p) * sizeof(float);
-    if (!workspace || ws_bytes < need)
+    if (need > 0 && (!workspace || ws_bytes < need))
       return fail(CGTP_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace ? ws_bytes : size_t(0), need);
     if (!aligned(workspace, 256)) return fail(CGTP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   }
@@ -343,6 +343,19 @@ int for_launches(cgtp_params_t P, bool back, F&& launch) {
   return ok();
 }
 
+// Whether one workgroup takes the whole gradient norm.
+bool small_norm(cgtp_params_t P) {
+  return P->first_chunk.back() <= kSmallChunks && P->numel.size() <= size_t(kTensorsPerLaunch);
+}
+// Partial sums of the gradient norm's first pass.
+int norm_parts(cgtp_params_t P) {
+  if (small_norm(P)) return 0;
+  int parts = 0;
+  for (size_t t = 0; t < P->numel.size(); t += kTensorsPerLaunch)
+    parts += square_blocks(P->first_chunk[std::min(P->numel.size(), t + kTensorsPerLaunch)] - P->first_chunk[t]);
+  return parts;
+}
+
 int adamw_step(cgtp_params_t P, int param_dtype, void* const* params, int grad_dtype, const void* const* grads,
                AdamwArgs& a, bool bits8, double lr, double beta1, double beta2, double eps, int64_t step,
                const float* grad_scale, void* stream) {
@@ -422,7 +435,7 @@ int cgtp_adamw_read_8bit(cgtp_params_t P, const uint8_t* m_code, const uint8_t* 
 
 int cgtp_grad_norm_workspace_size(cgtp_params_t P, size_t* bytes) {
   if (!P || !bytes) return fail(CGTP_ERR_INVALID_ARG, "NULL argument");
-  *bytes = (size_t(P->first_chunk.back()) * sizeof(double) + 255) / 256 * 256;
+  *bytes = (size_t(norm_parts(P)) * sizeof(double) + 255) / 256 * 256;
   return ok();
 }
 
@@ -432,23 +445,32 @@ int cgtp_grad_norm(cgtp_params_t P, int grad_dtype, const void* const* grads, co
   if (int rc = check_tensors(P, grad_dtype, grads, "grads")) return rc;
   if (!(max_norm > 0)) return fail(CGTP_ERR_INVALID_ARG, "max_norm must be positive");
   if (!out || !aligned(out, 4) || !aligned(grad_scale, 4)) return fail(CGTP_ERR_INVALID_ARG, "NULL or misaligned pointer");
-  const int chunks = P->first_chunk.back();
-  const size_t need = size_t(chunks) * sizeof(double);
-  if (chunks > 0 && (!workspace || ws_bytes < need))
+  const int chunks = P->first_chunk.back(), parts = norm_parts(P);
+  const size_t need = size_t(parts) * sizeof(double);
+  if (parts > 0 && (!workspace || ws_bytes < need))
     return fail(CGTP_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace ? ws_bytes : size_t(0), need);
   if (!aligned(workspace, 256)) return fail(CGTP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   double* part = static_cast<double*>(workspace);
   GradNormArgs a{};
+  if (small_norm(P)) {
+    a.chunks = P->d_chunks;
+    a.n_chunks = chunks;
+    if (!P->numel.empty()) std::memcpy(a.grad, grads, P->numel.size() * sizeof(void*));
+    CGTP_HIP(launch_grad_norm_small(a, Elem(grad_dtype), grad_scale, float(max_norm), out,
+                                    static_cast<hipStream_t>(stream)));
+    return ok();
+  }
   int rc = for_launches(P, false, [&](int t, int n, int c0, int count) {
     a.chunks = P->d_chunks + c0;
-    a.part = part + c0;
+    a.part = part;
+    part += square_blocks(count);
     a.first_tensor = t;
     a.n_chunks = count;
     std::memcpy(a.grad, grads + t, size_t(n) * sizeof(void*));
     return launch_grad_squares(a, Elem(grad_dtype), static_cast<hipStream_t>(stream));
   });
   if (rc) return rc;
-  CGTP_HIP(launch_grad_norm_finish(part, chunks, grad_scale, float(max_norm), out, static_cast<hipStream_t>(stream)));
+  CGTP_HIP(launch_grad_norm_finish(static_cast<double*>(workspace), parts, grad_scale, float(max_norm), out, static_cast<hipStream_t>(stream)));
   return ok();
 }
 

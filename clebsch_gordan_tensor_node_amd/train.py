@@ -119,7 +119,8 @@ def _backward(call, size, plan, grad_out, x, stats, weight, need, workspace):
     if workspace is not None:
         _on(workspace, "workspace", dev)
     elif gw is not None or gb is not None:
-        workspace = x.new_empty(size(x.shape[0]), dtype=torch.uint8)
+        need_bytes = size(x.shape[0])
+        workspace = x.new_empty(need_bytes, dtype=torch.uint8) if need_bytes else None
     check(call(*head, grad_out.data_ptr(), ld_g, x.data_ptr(), ld, stats.data_ptr(), ELEM[wt], w, _at(gx), x.shape[1],
                _at(gw), _at(gb), _at(workspace),
                0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev)))
@@ -360,9 +361,11 @@ def grad_norm(params: ParamSet, grads, max_norm: float = float("inf"), grad_scal
     finite.  Asynchronous on the current stream; bitwise reproducible."""
     g = _laid(params, grads, "grads")
     out = torch.empty(2, dtype=torch.float32, device=params.device)
-    if workspace is None:
+    if workspace is not None:
+        _on(workspace, "workspace", params.device.index)
+    elif params.grad_norm_workspace_size:
         workspace = torch.empty(params.grad_norm_workspace_size, dtype=torch.uint8, device=params.device)
     check(load().cgtp_grad_norm(params.handle, g.type, g.array, _scale(params, grad_scale), max_norm, out.data_ptr(),
-                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                _at(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
                                 _raw_stream(params.device.index)))
     return out

@@ -274,7 +274,8 @@ def test_norm_argument_checks(dev):
         C.layer_norm_forward(x, eps=-1.0)
     assert e.value.code == -1
     with pytest.raises(C.CgtpError) as e:
-        C.layer_norm_backward(x, x, st, workspace=torch.empty(0, dtype=torch.uint8, device=dev))
+        many, st = torch.zeros(1000, 8, device=dev), torch.zeros(2, 1000, device=dev)
+        C.layer_norm_backward(many, many, st, workspace=torch.empty(0, dtype=torch.uint8, device=dev))
     assert e.value.code == -5
 
 
@@ -504,7 +505,8 @@ def test_optimiser_argument_checks(dev):
     with pytest.raises(C.CgtpError):
         C.grad_norm(s, g, max_norm=0.0)
     with pytest.raises(C.CgtpError) as e:
-        C.grad_norm(s, g, workspace=torch.empty(0, dtype=torch.uint8, device=dev))
+        C.grad_norm(C.ParamSet([100000]), [torch.zeros(100000, device=dev)],
+                    workspace=torch.empty(0, dtype=torch.uint8, device=dev))
     assert e.value.code == -5
     for f in (lambda: s.pointers(p[:1]), lambda: s.pointers([p[1], p[0]]), lambda: s.pointers([p[0], torch.zeros(6, 2, device=dev)[:, 0]]),
               lambda: C.adamw_step(s, p, g, st[:1], lr=1.0), lambda: C.adamw_step(s, p, g, (st[0], st[1][:-1]), lr=1.0)):

@@ -82,7 +82,10 @@ def test_layer_norm_refusals():
     for bad in (dict(g=None), dict(stats=None), dict(ldg=7), dict(ldgx=7), dict(gw=odd, wsp=p, wsb=1 << 20),
                 dict(gw=p, wsp=ctypes.c_void_p((a.ctypes.data + 511) // 256 * 256 + 4), wsb=1 << 20)):
         assert bwd(**bad) == INVALID, bad
-    assert bwd(gw=p) == WORKSPACE and bwd(gb=p, wsp=p, wsb=4) == WORKSPACE
+    assert bwd(rows=1000, gw=p) == WORKSPACE
+    assert bwd(rows=1000, gb=p, wsp=ctypes.c_void_p((a.ctypes.data + 255) // 256 * 256), wsb=4) == WORKSPACE
+    # a few rows need none
+    assert lib.cgtp_layer_norm_backward_workspace_size(2, 8, ctypes.byref(ws)) == 0 and ws.value == 0
 
 
 def test_irreps_norm_and_set_refusals():
