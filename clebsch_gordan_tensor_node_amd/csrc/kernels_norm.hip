@@ -25,7 +25,6 @@
 namespace cgtp {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kWave = 64;
 
 // A term as a launch carries it.
@@ -47,51 +46,58 @@ struct NormArgs {
 };
 constexpr int kCapSmall = 8;
 
-// The variants: a stretch of len elements takes the first whose room it fits.
-//   id  V G C             room, 4-byte elements   2-byte elements
+// How many lanes G hold a stretch, and in how many vectors C each: the first that has room
+// for its nv = ceil(len / V) vectors.  B is the workgroup's size.
 enum Variant : int {
-  kElem16,    // V = 1, G = 16, C = 1       16                     16   (shorter than a vector)
-  kG16C1,     //        G = 16              64                    128
-  kG16C2,     //                           128                    256
-  kG64C1,     //        G = 64             256                    512
-  kG64C2,     //                           512                   1024
-  kG64C4,     //                          1024                   2048
-  kG64C8,     //                          2048                      -     (forward)
-  kG256C2,    //        G = 256           2048                   4096     (backward)
-  kG256C4,    //                          4096                   8192
-  kG256C8,    //                          8192                      -
-  kWide       // any: the row is read again for each sum
+  kElem8,   // V = 1, G = 8: shorter than a vector
+  kG4C1,    // nv <= 4
+  kG8C1,    // nv <= 8
+  kG16C1,   // nv <= 16
+  kG32C1,   // nv <= 32
+  kG64C1,   // nv <= 64
+  kG64C2,   // nv <= 128, if a lane holds that many elements
+  kG64C4,   // nv <= 256, likewise
+  kGBC1,    // nv <= B
+  kGBC2,    // nv <= 2 B, likewise
+  kGBC4,    // nv <= 4 B, likewise
+  kWide     // any: the row is read again for each sum
 };
-constexpr int kWideOver = 8192;
 
-// The backward holds five values per element where the forward holds three, and takes at
-// most 16 elements per lane as long as a workgroup's lanes reach.
-int variant_of(int len, int elem_bytes, bool backward) {
-  const int v = 16 / elem_bytes;
-  if (len > kWideOver) return kWide;
-  if (len < v) return kElem16;
-  const int nv = (len + v - 1) / v;
-  if (nv <= 16) return kG16C1;
-  if (nv <= 32) return kG16C2;
-  if (nv <= 64) return kG64C1;
-  if (nv <= 128) return kG64C2;
-  if (nv <= 256 && !(backward && elem_bytes == 2)) return kG64C4;
-  if (nv <= 512 && backward) return kG256C2;
-  if (nv <= 512 && elem_bytes == 4) return kG64C8;
-  return nv <= 1024 ? kG256C4 : kG256C8;
+// Elements per lane, as long as a workgroup's lanes reach.  The more, the fewer waves fit a
+// SIMD's registers; the fewer, the more waves share a stretch and wait for one another.
+// Measured with 8 and with 16: forward of 2048 bf16 columns 91 and 186 us, of 1024 fp32
+// columns TBD; backward of 1024 fp32 columns TBD, of 512 bf16 columns TBD.
+int elems_of(int elem_bytes, bool backward) { return backward || elem_bytes == 2 ? 8 : 16; }
+constexpr int kMaxE = 16;
+constexpr int kWideOver = 1024 * kMaxE;
+
+// The workgroup that the longest stretch of a plan needs, with e elements per lane.
+int block_of(int longest, int e) {
+  return longest <= 64 * e ? 256 : longest <= 128 * e ? 128 : longest <= 256 * e ? 256 : longest <= 512 * e ? 512 : 1024;
 }
-// Stretches that a workgroup of a variant handles at once, and elements per lane.
-int groups_of(int variant) { return variant <= kG16C2 ? 16 : variant <= kG64C8 ? 4 : 1; }
-int elems_of(int variant, int elem_bytes) {
+
+int variant_of(int len, int elem_bytes, int block, int e) {
   const int v = 16 / elem_bytes;
-  switch (variant) {
-    case kElem16: return 1;
-    case kG16C1: case kG64C1: return v;
-    case kG16C2: case kG64C2: case kG256C2: return 2 * v;
-    case kG64C4: case kG256C4: return 4 * v;
-    case kG64C8: case kG256C8: return 8 * v;
-    default: return 1;
-  }
+  if (len > block * kMaxE) return kWide;
+  if (len < v) return kElem8;
+  const int nv = (len + v - 1) / v;
+  if (nv <= 4) return kG4C1;
+  if (nv <= 8) return kG8C1;
+  if (nv <= 16) return kG16C1;
+  if (nv <= 32) return kG32C1;
+  if (nv <= 64) return kG64C1;
+  if (nv <= 128 && e >= 2 * v) return kG64C2;
+  if (nv <= 256 && e >= 4 * v) return kG64C4;
+  if (nv <= block) return kGBC1;
+  return nv <= 2 * block ? kGBC2 : kGBC4;
+}
+// Lanes per stretch and vectors per lane.
+int lanes_of(int variant, int block) {
+  constexpr int g[] = {8, 4, 8, 16, 32, 64, 64, 64};
+  return variant <= kG64C4 ? g[variant] : block;
+}
+int vectors_of(int variant) {
+  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : 1;
 }
 
 template <typename T, int V>
@@ -131,52 +137,49 @@ template <int Ctrl>
 __device__ inline float dpp(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), Ctrl, 0xf, 0xf, true));
 }
-// Sum over G neighbouring lanes (16 or 64), to each of them.
+// Sum over G neighbouring lanes (4 to 64), to each of them.
 template <int G>
 __device__ inline float lanes_sum(float v) {
-  v += dpp<0xB1>(v);    // quad_perm 1 0 3 2
-  v += dpp<0x4E>(v);    // quad_perm 2 3 0 1
-  v += dpp<0x141>(v);   // row_half_mirror
-  v += dpp<0x140>(v);   // row_mirror
-  if constexpr (G >= 64) {
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-  }
+  v += dpp<0xB1>(v);                          // quad_perm 1 0 3 2
+  v += dpp<0x4E>(v);                          // quad_perm 2 3 0 1
+  if constexpr (G >= 8) v += dpp<0x141>(v);   // row_half_mirror
+  if constexpr (G >= 16) v += dpp<0x140>(v);  // row_mirror
+  if constexpr (G >= 32) v += __shfl_xor(v, 16);
+  if constexpr (G >= 64) v += __shfl_xor(v, 32);
   return v;
 }
-// The same over a group of G lanes, a whole workgroup for G = 256.  lds: 2 * 8 floats that
-// alternate (`turn`), so that one barrier per sum is enough.
-template <int G>
-__device__ inline float group_sum(float v, float* lds, int& turn) {
-  if constexpr (G <= kWave) {
-    return lanes_sum<G>(v);
-  } else {
-    v = lanes_sum<kWave>(v);
-    float* l = lds + (turn & 1) * 8;
-    turn ^= 1;
-    if (threadIdx.x % kWave == 0) l[threadIdx.x / kWave] = v;
-    __syncthreads();
-    return (l[0] + l[1]) + (l[2] + l[3]);
-  }
-}
+// The same over a group of G lanes, the whole workgroup for G > 64.  lds: two halves of
+// 2 * 16 floats that alternate (`turn`), so that one barrier per sum is enough.
+constexpr int kSumLds = 64;
 template <int G>
 __device__ inline void group_sum2(float& u, float& v, float* lds, int& turn) {
   if constexpr (G <= kWave) {
     u = lanes_sum<G>(u);
     v = lanes_sum<G>(v);
   } else {
+    constexpr int kWaves = G / kWave;
     u = lanes_sum<kWave>(u);
     v = lanes_sum<kWave>(v);
-    float* l = lds + (turn & 1) * 8;
+    float* l = lds + (turn & 1) * 32;
     turn ^= 1;
     if (threadIdx.x % kWave == 0) {
       l[threadIdx.x / kWave] = u;
-      l[4 + threadIdx.x / kWave] = v;
+      l[kWaves + threadIdx.x / kWave] = v;
     }
     __syncthreads();
-    u = (l[0] + l[1]) + (l[2] + l[3]);
-    v = (l[4] + l[5]) + (l[6] + l[7]);
+    u = v = 0;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) {
+      u += l[k];
+      v += l[kWaves + k];
+    }
   }
+}
+template <int G>
+__device__ inline float group_sum(float v, float* lds, int& turn) {
+  float none = 0;
+  group_sum2<G>(v, none, lds, turn);
+  return v;
 }
 
 // Where a lane's vectors of a stretch lie.
@@ -254,9 +257,9 @@ __device__ inline void load_weights(const Place<V, G, C>& p, const void* w, int 
     }
 }
 
-template <bool Stream, typename T, int V, int G, int C>
+template <int B, bool Stream, typename T, int V, int G, int C>
 __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
-  constexpr int kGroups = kThreads / G;
+  constexpr int kGroups = B / G;
   const Place<V, G, C> p(t.len);
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
@@ -282,15 +285,24 @@ __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_term
   }
 }
 
-template <bool Stream, typename T, int V, int G, int C>
+// The weights wait in LDS, a vector to each lane's place: they are used once per row, and in
+// registers they would leave fewer waves.
+template <int B, bool Stream, typename T, int V, int G, int C>
 __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds,
-                                bool direct) {
-  constexpr int kGroups = kThreads / G;
+                                float* sums, bool direct) {
+  constexpr int kGroups = B / G;
   const Place<V, G, C> p(t.len);
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
-  float w[C][V], x[C][V], g[C][V], gw[C][V], gb[C][V];
-  load_weights<T>(p, a.weight, a.weight_f32, t.w_off, t, 1.0f, w);
+  float x[C][V], g[C][V], gw[C][V], gb[C][V];
+  if (threadIdx.x < G) {
+    load_weights<T>(p, a.weight, a.weight_f32, t.w_off, t, 1.0f, x);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) lds[p.start(c) + j] = x[c][j];
+  }
+  __syncthreads();
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -307,12 +319,12 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
         x[c][j] = (x[c][j] - mu) * rstd;
         gw[c][j] += g[c][j] * x[c][j];
         gb[c][j] += g[c][j];
-        g[c][j] *= w[c][j];
+        g[c][j] *= lds[p.start(c) + j];
       }
     if (!a.y) continue;
     float sa = own_sum(p, [&](int c, int j) { return g[c][j]; });
     float sh = own_sum(p, [&](int c, int j) { return g[c][j] * x[c][j]; });
-    group_sum2<G>(sa, sh, lds, turn);
+    group_sum2<G>(sa, sh, sums, turn);
     sa = centred ? sa * inv : 0.0f;
     sh *= inv;
 #pragma unroll
@@ -336,7 +348,7 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
     void* out = k ? a.grad_bias : a.grad_weight;
     if (direct && !out) continue;
     const int d = direct ? t.d : 1;
-    for (int e = threadIdx.x; e < t.len / d; e += kThreads) {
+    for (int e = threadIdx.x; e < t.len / d; e += B) {
       float s = 0;
       for (int m = 0; m < d; ++m)
         for (int q = 0; q < kGroups; ++q) s += lds[q * t.len + e * d + m];
@@ -349,7 +361,7 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
 }
 
 // Stretches of any length: one workgroup per row, which is read again for each sum.
-template <typename T>
+template <int B, typename T>
 __device__ inline void fwd_wide(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
@@ -360,15 +372,15 @@ __device__ inline void fwd_wide(const NormCall& a, const TermArgs& t, int n_term
     float mu = 0, q = 0;
     if (centred) {
       float s = 0;
-      for (int e = threadIdx.x; e < t.len; e += kThreads) s += to_f32(x[e]);
-      mu = group_sum<kThreads>(s, lds, turn) * inv;
+      for (int e = threadIdx.x; e < t.len; e += B) s += to_f32(x[e]);
+      mu = group_sum<B>(s, lds, turn) * inv;
     }
-    for (int e = threadIdx.x; e < t.len; e += kThreads) {
+    for (int e = threadIdx.x; e < t.len; e += B) {
       const float v = to_f32(x[e]) - mu;
       q += v * v;
     }
-    const float rstd = 1.0f / sqrtf(group_sum<kThreads>(q, lds, turn) * inv + a.eps);
-    for (int e = threadIdx.x; e < t.len; e += kThreads) {
+    const float rstd = 1.0f / sqrtf(group_sum<B>(q, lds, turn) * inv + a.eps);
+    for (int e = threadIdx.x; e < t.len; e += B) {
       const int c = t.d == 1 ? e : int(__umulhi(uint32_t(e), t.inv_d));
       const float w = a.weight ? load_either<T>(a.weight, a.weight_f32, t.w_off + c) : 1.0f;
       const float b = a.bias && centred ? load_either<T>(a.bias, a.weight_f32, t.b_off + c) : 0.0f;
@@ -380,7 +392,7 @@ __device__ inline void fwd_wide(const NormCall& a, const TermArgs& t, int n_term
     }
   }
 }
-template <typename T>
+template <int B, typename T>
 __device__ inline void bwd_wide(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
@@ -395,21 +407,21 @@ __device__ inline void bwd_wide(const NormCall& a, const TermArgs& t, int n_term
       return a.weight ? load_either<T>(a.weight, a.weight_f32, t.w_off + c) : 1.0f;
     };
     float sa = 0, sh = 0;
-    for (int e = threadIdx.x; e < t.len; e += kThreads) {
+    for (int e = threadIdx.x; e < t.len; e += B) {
       const float v = to_f32(g[e]) * weight(e);
       sa += v;
       sh += v * ((to_f32(x[e]) - mu) * rstd);
     }
-    group_sum2<kThreads>(sa, sh, lds, turn);
+    group_sum2<B>(sa, sh, lds, turn);
     sa = centred ? sa * inv : 0.0f;
     sh *= inv;
-    for (int e = threadIdx.x; e < t.len; e += kThreads)
+    for (int e = threadIdx.x; e < t.len; e += B)
       y[e] = from_f32<T>((to_f32(g[e]) * weight(e) - sa - (to_f32(x[e]) - mu) * rstd * sh) * rstd);
   }
   if (!a.grad_weight && !a.grad_bias) return;
   // the sums of the workgroup's rows, column by column
   float* part = a.part + t.part + int64_t(block) * t.len;
-  for (int e = threadIdx.x; e < t.len; e += kThreads) {
+  for (int e = threadIdx.x; e < t.len; e += B) {
     float sw = 0, sb = 0;
     for (int64_t r = block; r < a.rows; r += t.n_blocks) {
       const float v = to_f32((static_cast<const T*>(a.grad_out) + r * a.ld_g + t.off)[e]);
@@ -431,48 +443,48 @@ __device__ inline int term_of(const NormArgs<Cap>& a) {
   return __builtin_amdgcn_readfirstlane(k);
 }
 
-// One launch for all terms; a kernel holds the variants of up to MaxE elements per lane,
-// so that short rows do not pay for long ones' registers.
-#define CGTP_NORM_VARIANTS(FN, ...)                                                                          \
-  constexpr int V = 16 / int(sizeof(T));                                                                     \
-  switch (t.variant) {                                                                                       \
-    case kElem16: FN<Stream, T, 1, 16, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;           \
-    case kG16C1: FN<Stream, T, V, 16, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;            \
-    case kG64C1: FN<Stream, T, V, 64, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;            \
-    default:                                                                                                 \
-      if constexpr (MaxE >= 2 * V) {                                                                         \
-        if (t.variant == kG16C2) FN<Stream, T, V, 16, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
-        if (t.variant == kG64C2) FN<Stream, T, V, 64, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
-        if (t.variant == kG256C2) FN<Stream, T, V, 256, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
-      }                                                                                                      \
-      if constexpr (MaxE >= 4 * V) {                                                                         \
-        if (t.variant == kG64C4) FN<Stream, T, V, 64, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
-        if (t.variant == kG256C4) FN<Stream, T, V, 256, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
-      }                                                                                                      \
-      if constexpr (MaxE >= 8 * V) {                                                                         \
-        if (t.variant == kG64C8) FN<Stream, T, V, 64, 8>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
-        if (t.variant == kG256C8) FN<Stream, T, V, 256, 8>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
-      }                                                                                                      \
+// One launch for all terms; a kernel holds the variants of up to E elements per lane, so
+// that short rows do not pay for long ones' registers.
+#define CGTP_NORM_VARIANTS(FN, ...)                                                                     \
+  constexpr int V = 16 / int(sizeof(T));                                                                \
+  switch (t.variant) {                                                                                  \
+    case kElem8: FN<B, Stream, T, 1, 8, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;     \
+    case kG4C1: FN<B, Stream, T, V, 4, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;      \
+    case kG8C1: FN<B, Stream, T, V, 8, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;      \
+    case kG16C1: FN<B, Stream, T, V, 16, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;    \
+    case kG32C1: FN<B, Stream, T, V, 32, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;    \
+    case kG64C1: FN<B, Stream, T, V, 64, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;    \
+    case kGBC1: FN<B, Stream, T, V, B, 1>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); break;      \
+    default:                                                                                            \
+      if constexpr (E >= 2 * V) {                                                                       \
+        if (t.variant == kG64C2) FN<B, Stream, T, V, 64, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
+        if (t.variant == kGBC2) FN<B, Stream, T, V, B, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
+      }                                                                                                 \
+      if constexpr (E >= 4 * V) {                                                                       \
+        if (t.variant == kG64C4) FN<B, Stream, T, V, 64, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
+        if (t.variant == kGBC4) FN<B, Stream, T, V, B, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
+      }                                                                                                 \
   }
 
-template <typename T, int MaxE, int Cap, bool Stream>
-__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs<Cap> a) {
-  __shared__ float lds[16];
+template <typename T, int B, int E, int Cap, bool Stream>
+__global__ __launch_bounds__(B) void norm_fwd_kernel(NormArgs<Cap> a) {
+  __shared__ float lds[kSumLds];
   const int k = term_of(a);
   const TermArgs& t = a.term[k];
   const int block = int(blockIdx.x) - a.first_block[k];
-  if (t.variant == kWide) return fwd_wide<T>(a.c, t, a.n_terms, k, block, lds);
+  if (t.variant == kWide) return fwd_wide<B, T>(a.c, t, a.n_terms, k, block, lds);
   CGTP_NORM_VARIANTS(fwd_rows)
 }
 
-template <typename T, int MaxE, int Cap, bool Stream>
-__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs<Cap> a) {
-  __shared__ float lds[kThreads * MaxE];
+template <typename T, int B, int E, int Cap, bool Stream>
+__global__ __launch_bounds__(B) void norm_bwd_kernel(NormArgs<Cap> a) {
+  __shared__ __align__(16) float lds[B * E];
+  __shared__ float sums[kSumLds];
   const int k = term_of(a);
   const TermArgs& t = a.term[k];
   const int block = int(blockIdx.x) - a.first_block[k];
-  if (t.variant == kWide) return bwd_wide<T>(a.c, t, a.n_terms, k, block, lds);
-  CGTP_NORM_VARIANTS(bwd_rows, a.direct)
+  if (t.variant == kWide) return bwd_wide<B, T>(a.c, t, a.n_terms, k, block, sums);
+  CGTP_NORM_VARIANTS(bwd_rows, sums, a.direct)
 }
 
 // The weight's and bias's gradients from the workgroups' sums, in a fixed order.  A
@@ -547,107 +559,143 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) 
 constexpr int kForwardBlocks = 2048, kForwardBlocksStream = 4096;
 constexpr int kBackwardBlocks = 768, kBackwardBlocksStream = 1536;
 
-int64_t share(int64_t total, const NormShape& p, int k) {
-  const int64_t s = total * p.terms[k].len / p.features;
-  return s > 0 ? s : 1;
+int longest(const NormShape& p) {
+  int n = 0;
+  for (int k = 0; k < p.n_terms; ++k) n = std::max(n, p.terms[k].len);
+  return n;
 }
 
-// Rows that outgrow the last-level cache pass it by, in plans of up to kCapSmall terms.
-template <int Cap>
-bool streams(const NormCall& c, const NormShape& p, int elem_bytes, int tensors) {
-  return Cap == kCapSmall && c.rows * p.features * elem_bytes * tensors > kCacheBytes;
-}
+// How the rows are laid over workgroups.
+struct Layout {
+  int block;                      // threads of a workgroup
+  bool stream;                    // rows pass by the last-level cache
+  bool direct;                    // backward: one workgroup per term
+  int max_e;                      // most elements per lane
+  int64_t part;                   // backward: floats of partial sums
+  int variant[kMaxNormTerms], n_blocks[kMaxNormTerms];
+};
 
-// Rows so few that one workgroup per term takes them all, in at most four turns: it then
-// writes the weight's and bias's gradients itself.
-bool few_rows(int64_t rows, const NormShape& p, int elem_bytes) {
+Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) {
+  Layout y;
+  const int e = elems_of(elem_bytes, backward);
+  y.block = block_of(longest(p), e);
+  // rows that outgrow the last-level cache, in plans of up to kCapSmall terms
+  y.stream = p.n_terms <= kCapSmall && rows * p.features * elem_bytes * (backward ? 3 : 2) > kCacheBytes;
+  // rows so few that one workgroup per term takes them all, in at most four turns: it then
+  // writes the weight's and bias's gradients itself
+  y.direct = backward;
+  y.max_e = 1;
+  int64_t cost = 0, part = 0, each[kMaxNormTerms];
   for (int k = 0; k < p.n_terms; ++k) {
-    const int v = variant_of(p.terms[k].len, elem_bytes, true);
-    if (v == kWide || rows > 4 * groups_of(v)) return false;
+    const int v = variant_of(p.terms[k].len, elem_bytes, y.block, e), g = lanes_of(v, y.block), c = vectors_of(v);
+    y.variant[k] = v;
+    if (v == kWide || rows > 4 * (y.block / g)) y.direct = false;
+    y.max_e = std::max(y.max_e, v == kElem8 || v == kWide ? 1 : c * 16 / elem_bytes);
+    // what a stretch costs: its lanes, for its vectors and a part that every stretch has
+    each[k] = v == kWide ? 2 * int64_t(p.terms[k].len) : int64_t(g) * (c + 1);
+    cost += each[k];
   }
-  return true;
+  const int64_t total = (backward ? (y.stream ? kBackwardBlocksStream : kBackwardBlocks)
+                                  : (y.stream ? kForwardBlocksStream : kForwardBlocks)) * 256 / y.block;
+  for (int k = 0; k < p.n_terms; ++k) {
+    const int64_t groups = y.block / lanes_of(y.variant[k], y.block);
+    const int64_t want = std::max<int64_t>((rows + groups - 1) / groups, 1);
+    y.n_blocks[k] = y.direct ? 1 : int(std::min(want, std::max<int64_t>(total * each[k] / cost, 1)));
+    part += int64_t(y.n_blocks[k]) * p.terms[k].len * (p.terms[k].b_off >= 0 ? 2 : 1);
+  }
+  y.part = y.direct ? 0 : part;
+  return y;
 }
 
-// Fills a launch's terms with about `total` workgroups; returns their number and the
-// largest number of elements per lane.
+// A launch's arguments; returns its workgroups.
 template <int Cap>
-int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, int elem_bytes, bool backward, int64_t total,
-         int* max_e) {
+int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, const Layout& y) {
   a.c = c;
-  a.direct = backward && few_rows(c.rows, p, elem_bytes);
   a.n_terms = p.n_terms;
+  a.direct = y.direct;
   int64_t part = 0;
   int at = 0;
-  *max_e = 1;
   for (int k = 0; k < Cap; ++k) a.first_block[k] = 0x7fffffff;
   for (int k = 0; k < p.n_terms; ++k) {
     const NormTerm& t = p.terms[k];
-    const int v = variant_of(t.len, elem_bytes, backward), g = groups_of(v);
-    const int64_t want = (c.rows + g - 1) / g > 0 ? (c.rows + g - 1) / g : 1;
-    const int64_t most = a.direct ? 1 : share(total, p, k);
-    const int n = int(want < most ? want : most);
-    a.term[k] = TermArgs{t.off, t.len, t.d, t.w_off, t.b_off, v, n,
+    a.term[k] = TermArgs{t.off, t.len, t.d, t.w_off, t.b_off, y.variant[k], y.n_blocks[k],
                          t.d > 1 ? uint32_t(((uint64_t(1) << 32) + uint64_t(t.d) - 1) / uint64_t(t.d)) : 0u, part};
     a.first_block[k] = at;
-    at += n;
-    part += int64_t(n) * t.len * (t.b_off >= 0 ? 2 : 1);
-    *max_e = max(*max_e, elems_of(v, elem_bytes));
+    at += y.n_blocks[k];
+    part += int64_t(y.n_blocks[k]) * t.len * (t.b_off >= 0 ? 2 : 1);
   }
   return at;
 }
 
 template <typename T, int Cap, bool Stream>
-void forward(const NormArgs<Cap>& a, int blocks, int max_e, hipStream_t s) {
-  const dim3 grid{unsigned(blocks)}, block(kThreads);
-  if (max_e <= 8)
-    hipLaunchKernelGGL((norm_fwd_kernel<T, 8, Cap, Stream>), grid, block, 0, s, a);
-  else if (max_e <= 16)
-    hipLaunchKernelGGL((norm_fwd_kernel<T, 16, Cap, Stream>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((norm_fwd_kernel<T, 32, Cap, Stream>), grid, block, 0, s, a);
+void forward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s) {
+  const dim3 grid{unsigned(blocks)}, block{unsigned(y.block)};
+  if (y.max_e <= 8) {
+    if (y.block == 256)
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 256, 8, Cap, Stream>), grid, block, 0, s, a);
+    else if (y.block == 512)
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 512, 8, Cap, Stream>), grid, block, 0, s, a);
+    else if (y.block == 1024)
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, 8, Cap, Stream>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 128, 8, Cap, Stream>), grid, block, 0, s, a);
+  } else if constexpr (sizeof(T) == 4) {
+    if (y.block == 256)
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 256, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+    else if (y.block == 512)
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 512, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+    else if (y.block == 1024)
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((norm_fwd_kernel<T, 128, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+  }
 }
 template <typename T, int Cap, bool Stream>
-void backward(const NormArgs<Cap>& a, int blocks, int max_e, hipStream_t s) {
-  const dim3 grid{unsigned(blocks)}, block(kThreads);
-  if (max_e <= 8)
-    hipLaunchKernelGGL((norm_bwd_kernel<T, 8, Cap, Stream>), grid, block, 0, s, a);
-  else if (max_e <= 16)
-    hipLaunchKernelGGL((norm_bwd_kernel<T, 16, Cap, Stream>), grid, block, 0, s, a);
+void backward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s) {
+  const dim3 grid{unsigned(blocks)}, block{unsigned(y.block)};
+  if (y.max_e > 8)   // 8 elements a lane reach 8192: the workgroup is the largest
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+  else if (y.block == 256)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 256, 8, Cap, Stream>), grid, block, 0, s, a);
+  else if (y.block == 512)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 512, 8, Cap, Stream>), grid, block, 0, s, a);
+  else if (y.block == 1024)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 1024, 8, Cap, Stream>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((norm_bwd_kernel<T, 32, Cap, Stream>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, 128, 8, Cap, Stream>), grid, block, 0, s, a);
 }
 
 template <typename T, int Cap>
 hipError_t forward(const NormCall& c, const NormShape& p, hipStream_t s) {
   NormArgs<Cap> a;
-  int max_e;
-  const bool stream = streams<Cap>(c, p, int(sizeof(T)), 2);
-  const int blocks = fill(a, c, p, int(sizeof(T)), false, stream ? kForwardBlocksStream : kForwardBlocks, &max_e);
-  if (stream)
-    forward<T, Cap, Cap == kCapSmall>(a, blocks, max_e, s);
+  const Layout y = lay_out(c.rows, p, int(sizeof(T)), false);
+  const int blocks = fill(a, c, p, y);
+  if (y.stream)
+    forward<T, Cap, Cap == kCapSmall>(a, blocks, y, s);
   else
-    forward<T, Cap, false>(a, blocks, max_e, s);
+    forward<T, Cap, false>(a, blocks, y, s);
   return hipGetLastError();
 }
 
 template <typename T, int Cap>
 hipError_t backward(const NormCall& c, const NormShape& p, hipStream_t s) {
   NormArgs<Cap> a;
-  int max_e;
-  const bool stream = streams<Cap>(c, p, int(sizeof(T)), 3);
-  const int blocks = fill(a, c, p, int(sizeof(T)), true, stream ? kBackwardBlocksStream : kBackwardBlocks, &max_e);
-  if (stream)
-    backward<T, Cap, Cap == kCapSmall>(a, blocks, max_e, s);
+  const Layout y = lay_out(c.rows, p, int(sizeof(T)), true);
+  const int blocks = fill(a, c, p, y);
+  if (y.stream)
+    backward<T, Cap, Cap == kCapSmall>(a, blocks, y, s);
   else
-    backward<T, Cap, false>(a, blocks, max_e, s);
-  if ((c.grad_weight || c.grad_bias) && !a.direct) {
+    backward<T, Cap, false>(a, blocks, y, s);
+  if ((c.grad_weight || c.grad_bias) && !y.direct) {
     // Wide tiles read whole lines (a tile that ends inside one has it fetched again by
     // another die's L2), narrow ones spread short stretches over more workgroups: 9088
     // columns took 10.1 us in tiles of 16 and 5.4 in tiles of 64, 481 columns 6.6 and 10.2.
     int tiles = 0, most = 0;
     for (int k = 0; k < p.n_terms; ++k) {
       tiles += p.terms[k].len / 64;
-      most = max(most, a.term[k].n_blocks);
+      most = std::max(most, y.n_blocks[k]);
     }
     const int wide = tiles >= 16 ? 64 : 16;
     int at = 0;
@@ -684,12 +732,8 @@ hipError_t launch_norm_forward(const NormCall& c, const NormShape& p, Elem type,
 }
 
 size_t norm_part_floats(int64_t rows, const NormShape& p) {
-  if (few_rows(rows, p, 2) && few_rows(rows, p, 4)) return 0;
-  size_t n = 0;
-  for (int k = 0; k < p.n_terms; ++k)
-    n += size_t(std::min(std::max<int64_t>(rows, 1), share(kBackwardBlocksStream, p, k))) * size_t(p.terms[k].len) *
-         (p.terms[k].b_off >= 0 ? 2 : 1);
-  return n;
+  // whatever the element type
+  return size_t(std::max(lay_out(rows, p, 2, true).part, lay_out(rows, p, 4, true).part));
 }
 
 hipError_t launch_norm_backward(const NormCall& c, const NormShape& p, Elem type, hipStream_t s) {
