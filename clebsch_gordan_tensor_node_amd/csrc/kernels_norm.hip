@@ -32,8 +32,9 @@ struct TermArgs {
   int32_t off, len, d, w_off, b_off;
   int32_t variant;        // which (V, G, C) handles it
   int32_t n_blocks;       // its workgroups
+  int32_t n_parts;        // backward: its partial sums
   uint32_t inv_d;         // ceil(2^32 / d) for d > 1: e / d = (e * inv_d) >> 32 for e < 2^32 / d
-  int64_t part;           // backward: its partial sums in `part`: [n_blocks][len] of the weight's
+  int64_t part;           // backward: its partial sums in `part`: [n_parts][len] of the weight's
                           // gradient, then (centred terms) as much of the bias's
 };
 template <int Cap>
@@ -336,7 +337,7 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
   if (!a.grad_weight && !a.grad_bias) return;
   // the workgroup's sums: its groups' added in LDS, one row of `part`, or the gradients
   float* part = a.part + t.part + int64_t(block) * t.len;
-  for (int k = 0; k < (centred ? 2 : 1); ++k, part += int64_t(t.n_blocks) * t.len) {
+  for (int k = 0; k < (centred ? 2 : 1); ++k, part += int64_t(t.n_parts) * t.len) {
     __syncthreads();
     float* mine = lds + threadIdx.x / G * t.len;
 #pragma unroll
@@ -360,77 +361,145 @@ __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_term
   }
 }
 
-// Stretches of any length: one workgroup per row, which is read again for each sum.
-template <int B, typename T>
-__device__ inline void fwd_wide(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
+// Stretches of any length, in launches of their own: one workgroup per row, which is read
+// again (from the caches, mostly) for each sum.
+constexpr int kWideBlock = 1024;
+// Calls f(first element, elements) for the thread's vectors.
+template <int B, int V, typename F>
+__device__ inline void wide_loop(int len, F&& f) {
+  for (int e = int(threadIdx.x) * V; e < len; e += B * V) f(e, min(V, len - e));
+}
+template <int V, typename T>
+__device__ inline void read_some(const T* p, int n, float (&v)[V]) {
+  if (n == V) {
+    const Vec<T, V> r = load_vec<false, T, V>(p);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = to_f32(r.v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = j < n ? to_f32(p[j]) : 0.0f;
+  }
+}
+template <int V, typename T>
+__device__ inline void write_some(T* p, int n, const float (&v)[V]) {
+  Vec<T, V> r;
+#pragma unroll
+  for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(v[j]);
+  if (n == V) {
+    store_vec<false, T, V>(p, r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) p[j] = r.v[j];
+  }
+}
+// The weights (biases) of the n elements from e on, `none` where there are none.
+template <int V, typename T>
+__device__ inline void some_weights(const void* w, int f32, int off, const TermArgs& t, int e, int n, float none,
+                                    float (&out)[V]) {
+  if (w && f32 && t.d == 1 && n == V) {
+#pragma unroll
+    for (int q = 0; q < V; q += 4) {
+      const Vec<float, 4> r = load_vec<false, float, 4>(static_cast<const float*>(w) + off + e + q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[q + j] = r.v[j];
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    out[j] = none;
+    if (w && j < n) out[j] = load_either<T>(w, f32, off + (t.d == 1 ? e + j : int(__umulhi(uint32_t(e + j), t.inv_d))));
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(NormCall a, TermArgs t, int n_terms, int index) {
+  __shared__ float sums[kSumLds];
+  constexpr int B = kWideBlock;
+  constexpr int V = 16 / int(sizeof(T));
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
   int turn = 0;
-  for (int64_t r = block; r < a.rows; r += t.n_blocks) {
+  float v[V];
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ld_x + t.off;
     T* y = static_cast<T*>(a.y) + r * a.ld_y + t.off;
     float mu = 0, q = 0;
     if (centred) {
       float s = 0;
-      for (int e = threadIdx.x; e < t.len; e += B) s += to_f32(x[e]);
-      mu = group_sum<B>(s, lds, turn) * inv;
+      wide_loop<B, V>(t.len, [&](int e, int n) {
+        read_some<V>(x + e, n, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += v[j];
+      });
+      mu = group_sum<B>(s, sums, turn) * inv;
     }
-    for (int e = threadIdx.x; e < t.len; e += B) {
-      const float v = to_f32(x[e]) - mu;
-      q += v * v;
-    }
-    const float rstd = 1.0f / sqrtf(group_sum<B>(q, lds, turn) * inv + a.eps);
-    for (int e = threadIdx.x; e < t.len; e += B) {
-      const int c = t.d == 1 ? e : int(__umulhi(uint32_t(e), t.inv_d));
-      const float w = a.weight ? load_either<T>(a.weight, a.weight_f32, t.w_off + c) : 1.0f;
-      const float b = a.bias && centred ? load_either<T>(a.bias, a.weight_f32, t.b_off + c) : 0.0f;
-      y[e] = from_f32<T>((to_f32(x[e]) - mu) * rstd * w + b);
-    }
+    wide_loop<B, V>(t.len, [&](int e, int n) {
+      read_some<V>(x + e, n, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) q += j < n ? (v[j] - mu) * (v[j] - mu) : 0.0f;
+    });
+    const float rstd = 1.0f / sqrtf(group_sum<B>(q, sums, turn) * inv + a.eps);
+    wide_loop<B, V>(t.len, [&](int e, int n) {
+      float w[V], b[V];
+      read_some<V>(x + e, n, v);
+      some_weights<V, T>(a.weight, a.weight_f32, t.w_off, t, e, n, 1.0f, w);
+      some_weights<V, T>(centred ? a.bias : nullptr, a.weight_f32, t.b_off, t, e, n, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = (v[j] - mu) * rstd * w[j] + b[j];
+      write_some<V>(y + e, n, v);
+    });
     if (a.stats && threadIdx.x == 0) {
       a.stats[r * n_terms + index] = mu;
       a.stats[(a.rows + r) * n_terms + index] = rstd;
     }
   }
 }
-template <int B, typename T>
-__device__ inline void bwd_wide(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
+// dx only: norm_wide_w_kernel adds the weight's gradient.
+template <typename T>
+__global__ __launch_bounds__(kWideBlock) void norm_bwd_wide_kernel(NormCall a, TermArgs t, int n_terms, int index) {
+  __shared__ float sums[kSumLds];
+  constexpr int B = kWideBlock;
+  constexpr int V = 16 / int(sizeof(T));
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
   int turn = 0;
-  for (int64_t r = block; a.y && r < a.rows; r += t.n_blocks) {
+  float xv[V], gv[V];
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ld_x + t.off;
     const T* g = static_cast<const T*>(a.grad_out) + r * a.ld_g + t.off;
     T* y = static_cast<T*>(a.y) + r * a.ld_y + t.off;
     const float mu = a.stats[r * n_terms + index], rstd = a.stats[(a.rows + r) * n_terms + index];
-    auto weight = [&](int e) {
-      const int c = t.d == 1 ? e : int(__umulhi(uint32_t(e), t.inv_d));
-      return a.weight ? load_either<T>(a.weight, a.weight_f32, t.w_off + c) : 1.0f;
+    auto read = [&](int e, int n) {   // h and a = g w
+      float w[V];
+      read_some<V>(x + e, n, xv);
+      read_some<V>(g + e, n, gv);
+      some_weights<V, T>(a.weight, a.weight_f32, t.w_off, t, e, n, 1.0f, w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        xv[j] = (xv[j] - mu) * rstd;
+        gv[j] *= w[j];
+      }
     };
     float sa = 0, sh = 0;
-    for (int e = threadIdx.x; e < t.len; e += B) {
-      const float v = to_f32(g[e]) * weight(e);
-      sa += v;
-      sh += v * ((to_f32(x[e]) - mu) * rstd);
-    }
-    group_sum2<B>(sa, sh, lds, turn);
+    wide_loop<B, V>(t.len, [&](int e, int n) {
+      read(e, n);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sa += j < n ? gv[j] : 0.0f;
+        sh += j < n ? gv[j] * xv[j] : 0.0f;
+      }
+    });
+    group_sum2<B>(sa, sh, sums, turn);
     sa = centred ? sa * inv : 0.0f;
     sh *= inv;
-    for (int e = threadIdx.x; e < t.len; e += B)
-      y[e] = from_f32<T>((to_f32(g[e]) * weight(e) - sa - (to_f32(x[e]) - mu) * rstd * sh) * rstd);
-  }
-  if (!a.grad_weight && !a.grad_bias) return;
-  // the sums of the workgroup's rows, column by column
-  float* part = a.part + t.part + int64_t(block) * t.len;
-  for (int e = threadIdx.x; e < t.len; e += B) {
-    float sw = 0, sb = 0;
-    for (int64_t r = block; r < a.rows; r += t.n_blocks) {
-      const float v = to_f32((static_cast<const T*>(a.grad_out) + r * a.ld_g + t.off)[e]);
-      const float mu = a.stats[r * n_terms + index], rstd = a.stats[(a.rows + r) * n_terms + index];
-      sw += v * ((to_f32((static_cast<const T*>(a.x) + r * a.ld_x + t.off)[e]) - mu) * rstd);
-      sb += v;
-    }
-    part[e] = sw;
-    if (centred) part[int64_t(t.n_blocks) * t.len + e] = sb;
+    wide_loop<B, V>(t.len, [&](int e, int n) {
+      read(e, n);
+#pragma unroll
+      for (int j = 0; j < V; ++j) gv[j] = (gv[j] - sa - xv[j] * sh) * rstd;
+      write_some<V>(y + e, n, gv);
+    });
   }
 }
 
@@ -472,7 +541,6 @@ __global__ __launch_bounds__(B) void norm_fwd_kernel(NormArgs<Cap> a) {
   const int k = term_of(a);
   const TermArgs& t = a.term[k];
   const int block = int(blockIdx.x) - a.first_block[k];
-  if (t.variant == kWide) return fwd_wide<B, T>(a.c, t, a.n_terms, k, block, lds);
   CGTP_NORM_VARIANTS(fwd_rows)
 }
 
@@ -483,8 +551,29 @@ __global__ __launch_bounds__(B) void norm_bwd_kernel(NormArgs<Cap> a) {
   const int k = term_of(a);
   const TermArgs& t = a.term[k];
   const int block = int(blockIdx.x) - a.first_block[k];
-  if (t.variant == kWide) return bwd_wide<B, T>(a.c, t, a.n_terms, k, block, sums);
   CGTP_NORM_VARIANTS(bwd_rows, sums, a.direct)
+}
+
+// The partial sums of wide stretches, column by column: a thread's column over every
+// kWideSlices-th row.
+constexpr int kWideSlices = 32;
+constexpr int kWideThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kWideThreads) void norm_wide_w_kernel(NormCall a, TermArgs t, int n_terms, int index) {
+  const int e = int(blockIdx.x) * kWideThreads + int(threadIdx.x);
+  if (e >= t.len) return;
+  const T* x = static_cast<const T*>(a.x) + t.off + e;
+  const T* g = static_cast<const T*>(a.grad_out) + t.off + e;
+  float sw = 0, sb = 0;
+#pragma unroll 4
+  for (int64_t r = blockIdx.y; r < a.rows; r += kWideSlices) {
+    const float v = to_f32(g[r * a.ld_g]);
+    sw += v * ((to_f32(x[r * a.ld_x]) - a.stats[r * n_terms + index]) * a.stats[(a.rows + r) * n_terms + index]);
+    sb += v;
+  }
+  float* part = a.part + t.part + int64_t(blockIdx.y) * t.len + e;
+  part[0] = sw;
+  if (t.b_off >= 0) part[int64_t(t.n_parts) * t.len] = sb;
 }
 
 // The weight's and bias's gradients from the workgroups' sums, in a fixed order.  A
@@ -507,21 +596,21 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) 
   float sw = 0, sb = 0;
   if (lane < tile && first + lane < t.len) {
     const float* part = a.c.part + t.part + first + lane;
-    const float* part_b = part + int64_t(t.n_blocks) * t.len;
-    for (int b0 = threadIdx.x / Tile; b0 < t.n_blocks; b0 += slices * kInFlight) {
+    const float* part_b = part + int64_t(t.n_parts) * t.len;
+    for (int b0 = threadIdx.x / Tile; b0 < t.n_parts; b0 += slices * kInFlight) {
       // past the end the last one is read again and left out: loads under a condition wait
       // for one another
       float vw[kInFlight], vb[kInFlight];
 #pragma unroll
-      for (int q = 0; q < kInFlight; ++q) vw[q] = part[int64_t(min(b0 + q * slices, t.n_blocks - 1)) * t.len];
+      for (int q = 0; q < kInFlight; ++q) vw[q] = part[int64_t(min(b0 + q * slices, t.n_parts - 1)) * t.len];
       if (want_b) {
 #pragma unroll
-        for (int q = 0; q < kInFlight; ++q) vb[q] = part_b[int64_t(min(b0 + q * slices, t.n_blocks - 1)) * t.len];
+        for (int q = 0; q < kInFlight; ++q) vb[q] = part_b[int64_t(min(b0 + q * slices, t.n_parts - 1)) * t.len];
 #pragma unroll
-        for (int q = 0; q < kInFlight; ++q) sb += b0 + q * slices < t.n_blocks ? vb[q] : 0.0f;
+        for (int q = 0; q < kInFlight; ++q) sb += b0 + q * slices < t.n_parts ? vb[q] : 0.0f;
       }
 #pragma unroll
-      for (int q = 0; q < kInFlight; ++q) sw += b0 + q * slices < t.n_blocks ? vw[q] : 0.0f;
+      for (int q = 0; q < kInFlight; ++q) sw += b0 + q * slices < t.n_parts ? vw[q] : 0.0f;
     }
   }
 #pragma unroll
@@ -572,7 +661,7 @@ struct Layout {
   bool direct;                    // backward: one workgroup per term
   int max_e;                      // most elements per lane
   int64_t part;                   // backward: floats of partial sums
-  int variant[kMaxNormTerms], n_blocks[kMaxNormTerms];
+  int variant[kMaxNormTerms], n_blocks[kMaxNormTerms], n_parts[kMaxNormTerms];
 };
 
 Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) {
@@ -592,7 +681,7 @@ Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) 
     if (v == kWide || rows > 4 * (y.block / g)) y.direct = false;
     y.max_e = std::max(y.max_e, v == kElem8 || v == kWide ? 1 : c * 16 / elem_bytes);
     // what a stretch costs: its lanes, for its vectors and a part that every stretch has
-    each[k] = v == kWide ? 2 * int64_t(p.terms[k].len) : int64_t(g) * (c + 1);
+    each[k] = v == kWide ? 0 : int64_t(g) * (c + 1);
     cost += each[k];
   }
   const int64_t total = (backward ? (y.stream ? kBackwardBlocksStream : kBackwardBlocks)
@@ -600,8 +689,11 @@ Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) 
   for (int k = 0; k < p.n_terms; ++k) {
     const int64_t groups = y.block / lanes_of(y.variant[k], y.block);
     const int64_t want = std::max<int64_t>((rows + groups - 1) / groups, 1);
-    y.n_blocks[k] = y.direct ? 1 : int(std::min(want, std::max<int64_t>(total * each[k] / cost, 1)));
-    part += int64_t(y.n_blocks[k]) * p.terms[k].len * (p.terms[k].b_off >= 0 ? 2 : 1);
+    y.n_blocks[k] = y.variant[k] == kWide ? 0   // launched by itself
+                    : y.direct            ? 1
+                                          : int(std::min(want, std::max<int64_t>(total * each[k] / cost, 1)));
+    y.n_parts[k] = y.variant[k] == kWide ? kWideSlices : y.n_blocks[k];
+    part += int64_t(y.n_parts[k]) * p.terms[k].len * (p.terms[k].b_off >= 0 ? 2 : 1);
   }
   y.part = y.direct ? 0 : part;
   return y;
@@ -618,11 +710,11 @@ int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, const Layout& 
   for (int k = 0; k < Cap; ++k) a.first_block[k] = 0x7fffffff;
   for (int k = 0; k < p.n_terms; ++k) {
     const NormTerm& t = p.terms[k];
-    a.term[k] = TermArgs{t.off, t.len, t.d, t.w_off, t.b_off, y.variant[k], y.n_blocks[k],
+    a.term[k] = TermArgs{t.off, t.len, t.d, t.w_off, t.b_off, y.variant[k], y.n_blocks[k], y.n_parts[k],
                          t.d > 1 ? uint32_t(((uint64_t(1) << 32) + uint64_t(t.d) - 1) / uint64_t(t.d)) : 0u, part};
     a.first_block[k] = at;
     at += y.n_blocks[k];
-    part += int64_t(y.n_blocks[k]) * t.len * (t.b_off >= 0 ? 2 : 1);
+    part += int64_t(y.n_parts[k]) * t.len * (t.b_off >= 0 ? 2 : 1);
   }
   return at;
 }
@@ -667,11 +759,18 @@ void backward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s
     hipLaunchKernelGGL((norm_bwd_kernel<T, 128, 8, Cap, Stream>), grid, block, 0, s, a);
 }
 
+unsigned wide_blocks(int64_t rows) { return unsigned(std::min<int64_t>(rows, kForwardBlocks)); }
+
 template <typename T, int Cap>
 hipError_t forward(const NormCall& c, const NormShape& p, hipStream_t s) {
   NormArgs<Cap> a;
   const Layout y = lay_out(c.rows, p, int(sizeof(T)), false);
   const int blocks = fill(a, c, p, y);
+  for (int k = 0; k < p.n_terms; ++k)
+    if (y.variant[k] == kWide)
+      hipLaunchKernelGGL(norm_fwd_wide_kernel<T>, dim3(wide_blocks(c.rows)), dim3(kWideBlock), 0, s, c, a.term[k],
+                         p.n_terms, k);
+  if (blocks == 0) return hipGetLastError();
   if (y.stream)
     forward<T, Cap, Cap == kCapSmall>(a, blocks, y, s);
   else
@@ -684,18 +783,27 @@ hipError_t backward(const NormCall& c, const NormShape& p, hipStream_t s) {
   NormArgs<Cap> a;
   const Layout y = lay_out(c.rows, p, int(sizeof(T)), true);
   const int blocks = fill(a, c, p, y);
-  if (y.stream)
+  for (int k = 0; k < p.n_terms; ++k)
+    if (y.variant[k] == kWide && c.y && c.rows > 0)
+      hipLaunchKernelGGL(norm_bwd_wide_kernel<T>, dim3(wide_blocks(c.rows)), dim3(kWideBlock), 0, s, c, a.term[k],
+                         p.n_terms, k);
+  if (blocks > 0 && y.stream)
     backward<T, Cap, Cap == kCapSmall>(a, blocks, y, s);
-  else
+  else if (blocks > 0)
     backward<T, Cap, false>(a, blocks, y, s);
   if ((c.grad_weight || c.grad_bias) && !y.direct) {
+    for (int k = 0; k < p.n_terms; ++k)
+      if (y.variant[k] == kWide) {
+        const dim3 grid(unsigned((p.terms[k].len + kWideThreads - 1) / kWideThreads), kWideSlices);
+        hipLaunchKernelGGL(norm_wide_w_kernel<T>, grid, dim3(kWideThreads), 0, s, c, a.term[k], p.n_terms, k);
+      }
     // Wide tiles read whole lines (a tile that ends inside one has it fetched again by
     // another die's L2), narrow ones spread short stretches over more workgroups: 9088
     // columns took 10.1 us in tiles of 16 and 5.4 in tiles of 64, 481 columns 6.6 and 10.2.
     int tiles = 0, most = 0;
     for (int k = 0; k < p.n_terms; ++k) {
       tiles += p.terms[k].len / 64;
-      most = std::max(most, y.n_blocks[k]);
+      most = std::max(most, y.n_parts[k]);
     }
     const int wide = tiles >= 16 ? 64 : 16;
     int at = 0;

@@ -317,7 +317,7 @@ def _scale(params, t):
 
 def _laid(params, tensors, what):
     p = params.pointers(tensors)
-    if len(p.tensors) != len(params.sizes) or p.sizes != params.sizes:
+    if p.sizes is not params.sizes and p.sizes != params.sizes:
         raise ValueError(f"{what} were laid out for another set")
     if p.device is not None and p.device != params.device:
         raise ValueError(f"{what} must be on the set's device")
