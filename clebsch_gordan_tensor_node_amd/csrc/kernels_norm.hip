@@ -64,11 +64,16 @@ enum Variant : int {
   kWide     // any: the row is read again for each sum
 };
 
-// Elements per lane, as long as a workgroup's lanes reach.  The more, the fewer waves fit a
-// SIMD's registers; the fewer, the more waves share a stretch and wait for one another.
-// Measured with 8 and with 16: forward of 2048 bf16 columns 91 and 186 us, of 1024 fp32
-// columns TBD; backward of 1024 fp32 columns TBD, of 512 bf16 columns TBD.
-int elems_of(int elem_bytes, bool backward) { return backward || elem_bytes == 2 ? 8 : 16; }
+// Elements per lane for a plan whose longest stretch is `longest`, as long as a workgroup's
+// lanes reach.  The more, the fewer waves fit a SIMD's registers; the fewer, the more waves
+// share a stretch and wait for one another.  With 8 and with 16, us for 400 MB: forward of
+// 4096 columns 73 and 78 (fp32), 92 and 109 (bf16), of 8192 87 and 83 (fp32), 95 and 112
+// (bf16); backward of 1024 columns 100 and 86 (fp32), 108 and 116 (bf16), of 4096 88 and 98
+// (fp32), 97 and 135 (bf16), of 8192 101 and 117 (fp32), 139 and 133 (bf16).
+int elems_of(int longest, int elem_bytes, bool backward) {
+  if (longest > 4096) return (elem_bytes == 4) != backward ? 16 : 8;
+  return longest > 512 && longest <= 1024 && backward && elem_bytes == 4 ? 16 : 8;
+}
 constexpr int kMaxE = 16;
 constexpr int kWideOver = 1024 * kMaxE;
 
@@ -544,8 +549,11 @@ __global__ __launch_bounds__(B) void norm_fwd_kernel(NormArgs<Cap> a) {
   CGTP_NORM_VARIANTS(fwd_rows)
 }
 
+// 16 elements of 16 bits a lane fit the registers of 4 waves per SIMD without spilling (8138
+// x 8192 133 us, 162 with the compiler's 3); 16 of 32 bits do not (1024 columns: 96 us, 86
+// with 3).
 template <typename T, int B, int E, int Cap, bool Stream>
-__global__ __launch_bounds__(B) void norm_bwd_kernel(NormArgs<Cap> a) {
+__global__ __launch_bounds__(B, E > 8 && sizeof(T) == 2 ? 4 : 1) void norm_bwd_kernel(NormArgs<Cap> a) {
   __shared__ __align__(16) float lds[B * E];
   __shared__ float sums[kSumLds];
   const int k = term_of(a);
@@ -666,7 +674,7 @@ struct Layout {
 
 Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) {
   Layout y;
-  const int e = elems_of(elem_bytes, backward);
+  const int e = elems_of(longest(p), elem_bytes, backward);
   y.block = block_of(longest(p), e);
   // rows that outgrow the last-level cache, in plans of up to kCapSmall terms
   y.stream = p.n_terms <= kCapSmall && rows * p.features * elem_bytes * (backward ? 3 : 2) > kCacheBytes;
@@ -719,37 +727,40 @@ int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, const Layout& 
   return at;
 }
 
+// 16 elements a lane: the pairs of type and workgroup that elems_of asks for.
 template <typename T, int Cap, bool Stream>
 void forward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s) {
   const dim3 grid{unsigned(blocks)}, block{unsigned(y.block)};
-  if (y.max_e <= 8) {
-    if (y.block == 256)
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 256, 8, Cap, Stream>), grid, block, 0, s, a);
-    else if (y.block == 512)
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 512, 8, Cap, Stream>), grid, block, 0, s, a);
-    else if (y.block == 1024)
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, 8, Cap, Stream>), grid, block, 0, s, a);
-    else
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 128, 8, Cap, Stream>), grid, block, 0, s, a);
-  } else if constexpr (sizeof(T) == 4) {
-    if (y.block == 256)
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 256, kMaxE, Cap, Stream>), grid, block, 0, s, a);
-    else if (y.block == 512)
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 512, kMaxE, Cap, Stream>), grid, block, 0, s, a);
-    else if (y.block == 1024)
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
-    else
-      hipLaunchKernelGGL((norm_fwd_kernel<T, 128, kMaxE, Cap, Stream>), grid, block, 0, s, a);
-  } else {
+  if (y.max_e > 8) {
+    if constexpr (sizeof(T) == 4)
+      if (y.block == 512) {
+        hipLaunchKernelGGL((norm_fwd_kernel<T, 512, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+        return;
+      }
     hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+    return;
   }
+  if (y.block == 256)
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 256, 8, Cap, Stream>), grid, block, 0, s, a);
+  else if (y.block == 512)
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 512, 8, Cap, Stream>), grid, block, 0, s, a);
+  else if (y.block == 1024)
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, 8, Cap, Stream>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_fwd_kernel<T, 128, 8, Cap, Stream>), grid, block, 0, s, a);
 }
 template <typename T, int Cap, bool Stream>
 void backward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s) {
   const dim3 grid{unsigned(blocks)}, block{unsigned(y.block)};
-  if (y.max_e > 8)   // 8 elements a lane reach 8192: the workgroup is the largest
-    hipLaunchKernelGGL((norm_bwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
-  else if (y.block == 256)
+  constexpr int kB = sizeof(T) == 4 ? 256 : 512;
+  if (y.max_e > 8) {
+    if (y.block == kB)
+      hipLaunchKernelGGL((norm_bwd_kernel<T, kB, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((norm_bwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
+    return;
+  }
+  if (y.block == 256)
     hipLaunchKernelGGL((norm_bwd_kernel<T, 256, 8, Cap, Stream>), grid, block, 0, s, a);
   else if (y.block == 512)
     hipLaunchKernelGGL((norm_bwd_kernel<T, 512, 8, Cap, Stream>), grid, block, 0, s, a);

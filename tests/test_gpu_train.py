@@ -23,9 +23,10 @@ C = pytest.importorskip("clebsch_gordan_tensor_node_amd")
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
-SPECS = [1, 2, 5, 16, 63, 64, 65, 128, 129, 480, 1312, 2048, 2049, 8192, 8193, 32768, 40001,
-         "16x0e+8x1e+16x1o", "1x0e", "1x0o+1x1o+1x6e", "128x0e+64x1o+32x2e+32x3o", "640x0e+1024x1o+1280x2e",
-         "5x0e+3x0o+7x4e+2x0e", "+".join(["3x0e+1x1o"] * 32)]
+SPECS = [1, 2, 3, 4, 5, 8, 16, 17, 63, 64, 65, 128, 129, 257, 480, 512, 513, 1024, 1025, 1312, 2048, 2049, 4096, 4097, 8192,
+         8193, 16384, 16385, 40001, "16x0e+8x1e+16x1o", "1x0e", "1x0o+1x1o+1x6e", "128x0e+64x1o+32x2e+32x3o",
+         "640x0e+1024x1o+1280x2e", "5x0e+3x0o+7x4e+2x0e", "+".join(["3x0e+1x1o"] * 32), "20000x0e+3x1o+7000x1o+600x0e",
+         "1152x4e+9x0e+2000x0o"]
 
 
 @pytest.fixture(scope="module")
@@ -110,17 +111,44 @@ def test_norm_widths(spec, dev):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("spec", [5, 64, 129, 1312, 4097, 20000, "128x0e+64x1o+32x2e+32x3o", "5x0e+3x0o+7x4e+2x0e"],
-                         ids=str)
+@pytest.mark.parametrize("spec", [1, 5, 7, 8, 33, 64, 129, 257, 513, 1025, 1312, 2049, 4097, 8193, 16384, 20000,
+                                  "128x0e+64x1o+32x2e+32x3o", "5x0e+3x0o+7x4e+2x0e", "18000x0e+3x1o+300x2e"], ids=str)
 def test_norm_types(spec, dtype, dev):
     _check(spec, 9, dtype, torch.float32, dev)
     _check(spec, 9, dtype, dtype, dev, pad=3, first=1)
 
 
 @pytest.mark.parametrize("rows", [1, 2, 31, 257, 4000])
-@pytest.mark.parametrize("spec", [16, 77, 480, "16x0e+8x1e+16x1o"], ids=str)
+@pytest.mark.parametrize("spec", [3, 7, 16, 30, 77, 128, 480, 1030, "16x0e+8x1e+16x1o"], ids=str)
 def test_norm_row_counts(spec, rows, dev):
+    # one workgroup per term, and many with their partial sums
     _check(spec, rows, torch.float32, torch.float32, dev)
+    if rows > 31:
+        _check(spec, rows, torch.bfloat16, torch.float32, dev)
+
+
+@pytest.mark.parametrize("spec,rows", [(1312, 60000), ("128x0e+64x1o+32x2e+32x3o", 100000)], ids=str)
+def test_norm_rows_that_outgrow_the_cache(spec, rows, dev):
+    # more than 256 MB: every row is what it is in a call of its own size, bit for bit, and the
+    # weight's gradient is the sum of the parts'
+    terms, f, nw, nb = _shape(spec)
+    gen = torch.Generator(device=dev).manual_seed(0)
+    x, g = (torch.randn(rows, f, device=dev, generator=gen) for _ in range(2))
+    w, b = torch.randn(nw, device=dev, generator=gen), torch.randn(nb, device=dev, generator=gen)
+    y, st = _call(spec, x, w, b)
+    gx, gw, gb = _grads(spec, g, x, st, w)
+    sw, sb = torch.zeros(nw, dtype=torch.float64, device=dev), torch.zeros(nb, dtype=torch.float64, device=dev)
+    for r in range(0, rows, 5000):
+        yr, sr = _call(spec, x[r:r + 5000], w, b)
+        assert torch.equal(y[r:r + 5000], yr)
+        gxr, gwr, gbr = _grads(spec, g[r:r + 5000], x[r:r + 5000], sr, w)
+        assert torch.equal(gx[r:r + 5000], gxr)
+        sw += gwr
+        sb += gbr
+    # sums of `rows` terms of size below 25 |g| |h| in 5000-row and in longer chains: 100 u of
+    # the sum of magnitudes, which is below 13 rows for the widest channel
+    bound = 100 * U * 13 * rows
+    assert (gw - sw).abs().max() < bound and (gb - sb).abs().max() < bound
 
 
 @pytest.mark.parametrize("pad,first", [(1, 0), (1, 1), (7, 3), (64, 32)])
@@ -450,6 +478,36 @@ def test_adamw_repeats_bitwise_and_in_a_graph(dev):
         graph.replay()
         torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((*p, *st, norm), (*q, *su, norm2)))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_set_that_outgrows_the_cache(bits, dev):
+    # more than 256 MB: each tensor is what it is in a set of its own, bit for bit (8-bit states
+    # round by their place in the set: the last tensor's are checked against the reference)
+    sizes = [9000001, 5, 8000000]
+    gen = torch.Generator(device=dev).manual_seed(0)
+    p, g = ([torch.randn(n, device=dev, generator=gen) for n in sizes] for _ in range(2))
+    start, s = [t.clone() for t in p], C.ParamSet(sizes, 0.1)
+    state = C.adamw_state(s, bits)
+    C.adamw_step(s, p, g, state, lr=1e-2, step=1, seed=9)
+    for k, n in enumerate(sizes):
+        one, alone = C.ParamSet([n], 0.1), [start[k]]
+        st = C.adamw_state(one, bits)
+        C.adamw_step(one, alone, [g[k]], st, lr=1e-2, step=1, seed=9)
+        assert torch.equal(alone[0], p[k])
+        if bits == 32:
+            at = slice(s.offsets[k], s.offsets[k] + n)
+            assert all(torch.equal(a[at], b[:n]) for a, b in zip(state, st))
+    if bits == 8:
+        n = 64 * 1000
+        at = s.offsets[2] + sizes[2] - n
+        zero = np.zeros(n, np.float32)
+        _, m, _, root = T.adamw_f32(zero, g[2][-n:].cpu().numpy(), zero, zero, 1e-2, 0.9, 0.999, 1e-8, 1)
+        h = T.random_bits(np.arange(at, at + n), 9)
+        for values, u, signed, c, e in ((m, h & 0xffff, True, state[0], state[2]), (root, h >> 16, False, state[1], state[3])):
+            code, exp = T.encode(values, u, signed)
+            assert np.array_equal(c[at:at + n].cpu().numpy(), code)
+            assert np.array_equal(e[at // 64:(at + n) // 64].cpu().numpy(), exp)
 
 
 def test_adamw_tensor_past_32_bits(dev):
