@@ -58,6 +58,7 @@ enum Variant : int {
   kG64C1,   // nv <= 64
   kG64C2,   // nv <= 128, if a lane holds that many elements
   kG64C4,   // nv <= 256, likewise
+  kG64C6,   // nv <= 384, likewise
   kGBC1,    // nv <= B
   kGBC2,    // nv <= 2 B, likewise
   kGBC4,    // nv <= 4 B, likewise
@@ -72,6 +73,7 @@ enum Variant : int {
 // (fp32), 97 and 135 (bf16), of 8192 101 and 117 (fp32), 139 and 133 (bf16).
 int elems_of(int longest, int elem_bytes, bool backward) {
   if (longest > 4096) return (elem_bytes == 4) != backward ? 16 : 8;
+  if (longest > 1024 && longest <= 1536 && !backward && elem_bytes == 4) return 24;
   return longest > 512 && longest <= 1024 && backward && elem_bytes == 4 ? 16 : 8;
 }
 constexpr int kMaxE = 16;
@@ -94,16 +96,17 @@ int variant_of(int len, int elem_bytes, int block, int e) {
   if (nv <= 64) return kG64C1;
   if (nv <= 128 && e >= 2 * v) return kG64C2;
   if (nv <= 256 && e >= 4 * v) return kG64C4;
+  if (nv <= 384 && e >= 6 * v) return kG64C6;
   if (nv <= block) return kGBC1;
   return nv <= 2 * block ? kGBC2 : kGBC4;
 }
 // Lanes per stretch and vectors per lane.
 int lanes_of(int variant, int block) {
-  constexpr int g[] = {8, 4, 8, 16, 32, 64, 64, 64};
-  return variant <= kG64C4 ? g[variant] : block;
+  constexpr int g[] = {8, 4, 8, 16, 32, 64, 64, 64, 64};
+  return variant <= kG64C6 ? g[variant] : block;
 }
 int vectors_of(int variant) {
-  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : 1;
+  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : variant == kG64C6 ? 6 : 1;
 }
 
 template <typename T, int V>
@@ -538,6 +541,9 @@ __device__ inline int term_of(const NormArgs<Cap>& a) {
         if (t.variant == kG64C4) FN<B, Stream, T, V, 64, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
         if (t.variant == kGBC4) FN<B, Stream, T, V, B, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
       }                                                                                                 \
+      if constexpr (E >= 6 * V) {                                                                       \
+        if (t.variant == kG64C6) FN<B, Stream, T, V, 64, 6>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
+      }                                                                                                 \
   }
 
 template <typename T, int B, int E, int Cap, bool Stream>
@@ -732,11 +738,16 @@ template <typename T, int Cap, bool Stream>
 void forward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s) {
   const dim3 grid{unsigned(blocks)}, block{unsigned(y.block)};
   if (y.max_e > 8) {
-    if constexpr (sizeof(T) == 4)
+    if constexpr (sizeof(T) == 4) {
+      if (y.block == 256) {
+        hipLaunchKernelGGL((norm_fwd_kernel<T, 256, 24, Cap, Stream>), grid, block, 0, s, a);
+        return;
+      }
       if (y.block == 512) {
         hipLaunchKernelGGL((norm_fwd_kernel<T, 512, kMaxE, Cap, Stream>), grid, block, 0, s, a);
         return;
       }
+    }
     hipLaunchKernelGGL((norm_fwd_kernel<T, 1024, kMaxE, Cap, Stream>), grid, block, 0, s, a);
     return;
   }
