@@ -58,9 +58,9 @@ enum Variant : int {
   kG64C1,   // nv <= 64
   kG64C2,   // nv <= 128, if a lane holds that many elements
   kG64C4,   // nv <= 256, likewise
-  kG64C6,   // nv <= 384, likewise
   kGBC1,    // nv <= B
   kGBC2,    // nv <= 2 B, likewise
+  kGBC3,    // nv <= 3 B, likewise
   kGBC4,    // nv <= 4 B, likewise
   kWide     // any: the row is read again for each sum
 };
@@ -70,10 +70,12 @@ enum Variant : int {
 // share a stretch and wait for one another.  With 8 and with 16, us for 400 MB: forward of
 // 4096 columns 73 and 78 (fp32), 92 and 109 (bf16), of 8192 87 and 83 (fp32), 95 and 112
 // (bf16); backward of 1024 columns 100 and 86 (fp32), 108 and 116 (bf16), of 4096 88 and 98
-// (fp32), 97 and 135 (bf16), of 8192 101 and 117 (fp32), 139 and 133 (bf16).
+// (fp32), 97 and 135 (bf16), of 8192 101 and 117 (fp32), 139 and 133 (bf16).  12 lets a
+// workgroup of 128 hold 1536 fp32 columns, where 256 leave a third of their lanes idle:
+// forward of 20060 x 1312 42 us, with 8 46; of 114688 x 1312 230 and 236.
 int elems_of(int longest, int elem_bytes, bool backward) {
   if (longest > 4096) return (elem_bytes == 4) != backward ? 16 : 8;
-  if (longest > 1024 && longest <= 1536 && !backward && elem_bytes == 4) return 24;
+  if (longest > 1024 && longest <= 1536 && !backward && elem_bytes == 4) return 12;
   return longest > 512 && longest <= 1024 && backward && elem_bytes == 4 ? 16 : 8;
 }
 constexpr int kMaxE = 16;
@@ -96,17 +98,16 @@ int variant_of(int len, int elem_bytes, int block, int e) {
   if (nv <= 64) return kG64C1;
   if (nv <= 128 && e >= 2 * v) return kG64C2;
   if (nv <= 256 && e >= 4 * v) return kG64C4;
-  if (nv <= 384 && e >= 6 * v) return kG64C6;
   if (nv <= block) return kGBC1;
-  return nv <= 2 * block ? kGBC2 : kGBC4;
+  return nv <= 2 * block ? kGBC2 : nv <= 3 * block && e == 12 ? kGBC3 : kGBC4;
 }
 // Lanes per stretch and vectors per lane.
 int lanes_of(int variant, int block) {
-  constexpr int g[] = {8, 4, 8, 16, 32, 64, 64, 64, 64};
-  return variant <= kG64C6 ? g[variant] : block;
+  constexpr int g[] = {8, 4, 8, 16, 32, 64, 64, 64};
+  return variant <= kG64C4 ? g[variant] : block;
 }
 int vectors_of(int variant) {
-  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : variant == kG64C6 ? 6 : 1;
+  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : variant == kGBC3 ? 3 : 1;
 }
 
 template <typename T, int V>
@@ -537,12 +538,12 @@ __device__ inline int term_of(const NormArgs<Cap>& a) {
         if (t.variant == kG64C2) FN<B, Stream, T, V, 64, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
         if (t.variant == kGBC2) FN<B, Stream, T, V, B, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
       }                                                                                                 \
+      if constexpr (E >= 3 * V) {                                                                       \
+        if (t.variant == kGBC3) FN<B, Stream, T, V, B, 3>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
+      }                                                                                                 \
       if constexpr (E >= 4 * V) {                                                                       \
         if (t.variant == kG64C4) FN<B, Stream, T, V, 64, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
         if (t.variant == kGBC4) FN<B, Stream, T, V, B, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
-      }                                                                                                 \
-      if constexpr (E >= 6 * V) {                                                                       \
-        if (t.variant == kG64C6) FN<B, Stream, T, V, 64, 6>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
       }                                                                                                 \
   }
 
@@ -658,7 +659,11 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) 
 // backward no more, since each leaves a row of partial sums.  Measured: forward of 114688 x
 // 1312 fp32 232, 222 and 219 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 38, 36
 // and 41; backward and sums of 768 x 9088 (cached) 23.3, 23.3, 25.0 and 27.8 us with 512,
-// 768, 1024 and 1536, of 32768 x 704 82, 67, 60 and 56.
+// 768, 1024 and 1536, of 32768 x 704 82, 67, 60 and 56.  Past the cache the forward takes
+// more, as long as each has 28 / element bytes turns for the weights that it loads: 114688 x
+// 1312 fp32 in 8192 workgroups of 128 228 us, in 16384 219, but 30000 x 1400 70 and 78; 24414
+// x 4096 bf16 with 12 turns 92 us, with 7 104.
+constexpr int kTurnBytes = 28;
 constexpr int kForwardBlocks = 2048, kForwardBlocksStream = 4096;
 constexpr int kBackwardBlocks = 768, kBackwardBlocksStream = 1536;
 
@@ -701,11 +706,15 @@ Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) 
   const int64_t total = (backward ? (y.stream ? kBackwardBlocksStream : kBackwardBlocks)
                                   : (y.stream ? kForwardBlocksStream : kForwardBlocks)) * 256 / y.block;
   for (int k = 0; k < p.n_terms; ++k) {
-    const int64_t groups = y.block / lanes_of(y.variant[k], y.block);
-    const int64_t want = std::max<int64_t>((rows + groups - 1) / groups, 1);
-    y.n_blocks[k] = y.variant[k] == kWide ? 0   // launched by itself
-                    : y.direct            ? 1
-                                          : int(std::min(want, std::max<int64_t>(total * each[k] / cost, 1)));
+    if (y.variant[k] == kWide) {
+      y.n_blocks[k] = 0;   // launched by itself
+    } else {
+      const int64_t groups = y.block / lanes_of(y.variant[k], y.block);
+      const int64_t want = std::max<int64_t>((rows + groups - 1) / groups, 1);
+      int64_t most = std::max<int64_t>(total * each[k] / cost, 1);
+      if (y.stream && !backward) most = std::max(most, want * elem_bytes / kTurnBytes);
+      y.n_blocks[k] = y.direct ? 1 : int(std::min(want, most));
+    }
     y.n_parts[k] = y.variant[k] == kWide ? kWideSlices : y.n_blocks[k];
     part += int64_t(y.n_parts[k]) * p.terms[k].len * (p.terms[k].b_off >= 0 ? 2 : 1);
   }
@@ -733,14 +742,14 @@ int fill(NormArgs<Cap>& a, const NormCall& c, const NormShape& p, const Layout& 
   return at;
 }
 
-// 16 elements a lane: the pairs of type and workgroup that elems_of asks for.
+// More than 8 elements a lane: the pairs of type and workgroup that elems_of asks for.
 template <typename T, int Cap, bool Stream>
 void forward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s) {
   const dim3 grid{unsigned(blocks)}, block{unsigned(y.block)};
   if (y.max_e > 8) {
     if constexpr (sizeof(T) == 4) {
-      if (y.block == 256) {
-        hipLaunchKernelGGL((norm_fwd_kernel<T, 256, 24, Cap, Stream>), grid, block, 0, s, a);
+      if (y.block == 128) {
+        hipLaunchKernelGGL((norm_fwd_kernel<T, 128, 12, Cap, Stream>), grid, block, 0, s, a);
         return;
       }
       if (y.block == 512) {

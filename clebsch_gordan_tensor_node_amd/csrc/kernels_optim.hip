@@ -274,27 +274,35 @@ __device__ inline double block_sum(double v, double* lds) {
   return s;
 }
 
-// The sum of a chunk's squares over the lanes of one wave (Lanes = 64) or of a workgroup.
-// In fp64: no gradient's square overflows or underflows.
+// A lane's part of a chunk, over the lanes of one wave (Lanes = 64) or of a workgroup.
+template <int Lanes>
+struct Part {
+  static constexpr int kReads = kChunk / (Lanes * kVec);
+  float v[kReads][kVec];
+};
 template <int Lanes, typename G>
-__device__ inline double chunk_squares(const GradNormArgs& a, int index) {
-  constexpr int kReads = kChunk / (Lanes * kVec);
+__device__ inline Part<Lanes> chunk_part(const GradNormArgs& a, int index) {
+  Part<Lanes> p;
   const Chunk c = a.chunks[index];
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
   const unsigned lane = threadIdx.x % Lanes;
-  float v[kReads][kVec];
   if (c.n == kChunk) {
 #pragma unroll
-    for (int k = 0; k < kReads; ++k) load4<true, false>(g, (k * Lanes + lane) * kVec, kChunk, v[k]);
+    for (int k = 0; k < p.kReads; ++k) load4<true, false>(g, (k * Lanes + lane) * kVec, kChunk, p.v[k]);
   } else {
 #pragma unroll
-    for (int k = 0; k < kReads; ++k) load4<false, false>(g, (k * Lanes + lane) * kVec, unsigned(c.n), v[k]);
+    for (int k = 0; k < p.kReads; ++k) load4<false, false>(g, (k * Lanes + lane) * kVec, unsigned(c.n), p.v[k]);
   }
+  return p;
+}
+// In fp64: no gradient's square overflows or underflows.
+template <int Lanes>
+__device__ inline double squares(const Part<Lanes>& p) {
   double s = 0;
 #pragma unroll
-  for (int k = 0; k < kReads; ++k)
+  for (int k = 0; k < p.kReads; ++k)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) s += double(v[k][j]) * double(v[k][j]);
+    for (int j = 0; j < kVec; ++j) s += double(p.v[k][j]) * double(p.v[k][j]);
   return s;
 }
 
@@ -302,7 +310,7 @@ template <typename G>
 __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) {
   __shared__ double lds[kThreads / 64];
   double s = 0;
-  for (int c = blockIdx.x; c < a.n_chunks; c += int(gridDim.x)) s += chunk_squares<kThreads, G>(a, c);
+  for (int c = blockIdx.x; c < a.n_chunks; c += int(gridDim.x)) s += squares(chunk_part<kThreads, G>(a, c));
   s = block_sum(s, lds);
   if (threadIdx.x == 0) a.part[blockIdx.x] = s;
 }
@@ -324,14 +332,18 @@ __global__ __launch_bounds__(kFinish) void grad_norm_kernel(const double* part, 
   if (threadIdx.x == 0) write_norm(s, grad_scale, max_norm, out);
 }
 
-// Small sets: a chunk to each wave of one workgroup, and the norm in the same launch.
+// Small sets, in one workgroup and launch: two chunks to each wave, read together.
 template <typename G>
 __global__ __launch_bounds__(kFinish) void grad_norm_small_kernel(GradNormArgs a, const float* grad_scale,
                                                                   float max_norm, float* out) {
-  __shared__ double lds[kFinish / 64];
-  double s = 0;
-  for (int c = threadIdx.x / 64; c < a.n_chunks; c += kFinish / 64) s += chunk_squares<64, G>(a, c);
-  s = block_sum(s, lds);
+  constexpr int kWaves = kFinish / 64;
+  static_assert(kSmallChunks <= 2 * kWaves, "two chunks to a wave");
+  __shared__ double lds[kWaves];
+  const int c = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64);
+  Part<64> p = {}, q = {};
+  if (c < a.n_chunks) p = chunk_part<64, G>(a, c);
+  if (c + kWaves < a.n_chunks) q = chunk_part<64, G>(a, c + kWaves);
+  const double s = block_sum(squares(p) + squares(q), lds);
   if (threadIdx.x == 0) write_norm(s, grad_scale, max_norm, out);
 }
 

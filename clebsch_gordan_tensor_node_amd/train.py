@@ -35,10 +35,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() makes an o
 
 def _on(t, name, dev):
     """Checks that t is a tensor on device number `dev`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a device (cuda) tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on device {t.get_device()}, expected {dev}")
+    at = t.get_device() if isinstance(t, torch.Tensor) else -1   # -1: on the host
+    if at != dev:
+        if at < 0:
+            raise TypeError(f"{name} must be a device (cuda) tensor")
+        raise ValueError(f"{name} is on device {at}, expected {dev}")
 
 
 def _rows(t, name, shape=None, dtype=None):
@@ -216,11 +217,14 @@ class _Pointers:
         if len(tensors) != len(sizes):
             raise ValueError(f"{len(tensors)} tensors, the set has {len(sizes)}")
         for k, (t, n) in enumerate(zip(tensors, sizes)):
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            at = t.get_device() if isinstance(t, torch.Tensor) else -1
+            if at < 0:
                 raise TypeError(f"tensor {k} must be a device (cuda) tensor")
-            if t.dtype != tensors[0].dtype or t.dtype not in ELEM:
+            if k == 0:
+                dev, dtype = at, t.dtype
+            if t.dtype is not dtype or dtype not in ELEM:
                 raise TypeError(f"tensor {k} is {t.dtype}: one type, float32, bfloat16 or float16")
-            if t.device != tensors[0].device:
+            if at != dev:
                 raise ValueError("the tensors of a set are on one device")
             if t.numel() != n:
                 raise ValueError(f"tensor {k} has {t.numel()} elements, expected {n}")
@@ -254,7 +258,8 @@ class ParamSet:
         b = ctypes.c_size_t()
         check(lib.cgtp_grad_norm_workspace_size(h, ctypes.byref(b)))
         self.grad_norm_workspace_size = b.value
-        self.device = None if host_only else torch.device("cuda", torch.cuda.current_device())
+        self.index = None if host_only else torch.cuda.current_device()
+        self.device = None if host_only else torch.device("cuda", self.index)
 
     @property
     def handle(self):
@@ -295,13 +300,14 @@ def _state(params, state):
     if len(state) not in (2, 4):
         raise ValueError("a state is (m, v) or (m codes, r codes, m exponents, r exponents)")
     dtype = torch.float32 if len(state) == 2 else torch.uint8
-    at = []
+    dev, n, at = params.index, params.state_elems, []
     for k, t in enumerate(state):
-        _on(t, "a state", params.device.index)
+        _on(t, "a state", dev)
         if t.dtype != dtype:
             raise TypeError(f"a state is {t.dtype}, expected {dtype}")
-        n = params.state_elems // (64 if k > 1 else 1)
-        if t.shape != (n,) or not t.is_contiguous():
+        if k == 2:
+            n //= 64
+        if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
             raise ValueError(f"a state has shape {tuple(t.shape)}, expected ({n},), contiguous")
         at.append(t.data_ptr())
     return at
@@ -310,7 +316,7 @@ def _state(params, state):
 def _scale(params, t):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.get_device() != params.device.index or t.dtype != torch.float32 or t.numel() != 1:
+    if not isinstance(t, torch.Tensor) or t.get_device() != params.index or t.dtype != torch.float32 or t.numel() != 1:
         raise TypeError("grad_scale must be a float32 tensor of one element on the set's device")
     return t.data_ptr()
 
@@ -333,7 +339,7 @@ def adamw_step(params: ParamSet, tensors, grads, state, lr: float, betas=(0.9, 0
     scale) that multiplies the gradients; NaN skips the step.  With 8-bit states, seed
     chooses the rounding: pass another each step.  Asynchronous on the current stream."""
     p, g = _laid(params, tensors, "tensors"), _laid(params, grads, "grads")
-    s, scale, stream = _state(params, state), _scale(params, grad_scale), _raw_stream(params.device.index)
+    s, scale, stream = _state(params, state), _scale(params, grad_scale), _raw_stream(params.index)
     lib = load()
     if len(s) == 2:
         check(lib.cgtp_adamw_step(params.handle, p.type, p.array, g.type, g.array, *s, lr, betas[0], betas[1], eps,
@@ -351,7 +357,7 @@ def adamw_moments(params: ParamSet, state):
         return state
     m, r = (torch.empty(params.state_elems, dtype=torch.bfloat16, device=params.device) for _ in range(2))
     check(load().cgtp_adamw_read_8bit(params.handle, *s, m.data_ptr(), r.data_ptr(),
-                                      _raw_stream(params.device.index)))
+                                      _raw_stream(params.index)))
     return m, r
 
 
@@ -362,10 +368,10 @@ def grad_norm(params: ParamSet, grads, max_norm: float = float("inf"), grad_scal
     g = _laid(params, grads, "grads")
     out = torch.empty(2, dtype=torch.float32, device=params.device)
     if workspace is not None:
-        _on(workspace, "workspace", params.device.index)
+        _on(workspace, "workspace", params.index)
     elif params.grad_norm_workspace_size:
         workspace = torch.empty(params.grad_norm_workspace_size, dtype=torch.uint8, device=params.device)
     check(load().cgtp_grad_norm(params.handle, g.type, g.array, _scale(params, grad_scale), max_norm, out.data_ptr(),
                                 _at(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                _raw_stream(params.device.index)))
+                                _raw_stream(params.index)))
     return out
