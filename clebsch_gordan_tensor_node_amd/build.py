@@ -91,7 +91,7 @@ def build(incremental: bool = False, jobs: int | None = None, verbose: bool = Tr
     t0 = time.time()
     # the slowest units (the backward's edge pass, the l >= 4 conv classes) start first
     slow = {"kernels_conv_c6.o": 0, "kernels_conv_c7.o": 1, "kernels_conv_c8.o": 2, "kernels_conv_c1.o": 3,
-            "kernels_conv_c5.o": 4, "kernels_bwd.o": 5, "kernels_conv_c4.o": 6}
+            "kernels_conv_c5.o": 4, "kernels_bwd.o": 5, "kernels_conv_c4.o": 6, "kernels_norm.o": 7}
     order = sorted(range(len(_units())), key=lambda k: slow.get(_units()[k][2], 99))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         done = dict(zip(order, ex.map(compile_one, [_units()[k] for k in order])))

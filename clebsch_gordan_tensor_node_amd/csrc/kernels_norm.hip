@@ -16,7 +16,11 @@
 // the hardware takes 16-byte accesses at any element's address.  The last vector of a
 // stretch that V does not divide is moved back to end with the stretch; the elements that
 // it repeats are left out of the sums, and written twice with the same value.
-// A workgroup keeps its weights in registers over all its rows (workgroup, then stride).
+// A workgroup keeps its weights over all its rows (first its own number, then in strides).
+// Measured, with 4.75 TB/s for a large device copy: forward of 114688 x 1312 fp32 212 us
+// (5.7 TB/s), of 4096 x 5472 in four terms 38 us (4.7); backward with all gradients of 32768
+// x 704 in four terms 55 us (5.1), of 114688 x 128 bf16 22 + 5 us for the sums of the
+// weight's gradient, which wait for the memory's latency (as do rows of a few lanes).
 #include <algorithm>
 
 #include "elem.hpp"
@@ -112,17 +116,17 @@ int vectors_of(int variant) {
 
 template <typename T, int V>
 struct Vec {
-  typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T) * V / 4), aligned(sizeof(T))));
+  typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T) * V / 4), aligned(sizeof(T)), may_alias));
   T v[V];
 };
 template <>
 struct Vec<Bf16, 1> {
-  typedef uint16_t Bits;
+  typedef uint16_t Bits __attribute__((may_alias));
   Bf16 v[1];
 };
 template <>
 struct Vec<F16, 1> {
-  typedef uint16_t Bits;
+  typedef uint16_t Bits __attribute__((may_alias));
   F16 v[1];
 };
 // 16 bytes (or one element) at any element's address.  Stream: the access does not keep
@@ -654,7 +658,7 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) 
   }
 }
 
-// Workgroups of a launch, shared among the terms by their length: enough to keep the
+// Workgroups of a launch, shared among the terms by their cost: enough to keep the
 // memory busy, which takes more of them where every access goes to HBM, and in the
 // backward no more, since each leaves a row of partial sums.  Measured: forward of 114688 x
 // 1312 fp32 232, 222 and 219 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 38, 36

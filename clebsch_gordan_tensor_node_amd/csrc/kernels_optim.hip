@@ -81,12 +81,12 @@ constexpr int kPasses = kChunk / (kThreads * kVec);
 // written.  Stream: the access does not keep the line in the caches.
 template <typename T>
 struct Four {
-  typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T)), aligned(sizeof(T))));
+  typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T)), aligned(sizeof(T)), may_alias));
   T v[kVec];
 };
 template <>
 struct Four<uint8_t> {
-  typedef uint32_t Bits;
+  typedef uint32_t Bits __attribute__((may_alias));
   uint8_t v[kVec];
 };
 template <bool Stream, typename T>
@@ -254,6 +254,12 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float sca
   }
 }
 
+// Bound by HBM with 32-bit states: 49.8 M elements, 28 bytes each, 201 us (6.9 TB/s of
+// algorithmic bytes, a part of the gradients still cached from their norm).  With 8-bit
+// states 37.3 M elements of 16 bytes take 106 us (5.6 TB/s) and some 85 operations each, two
+// thirds of the time that the bytes need at that rate: every operation added here costs.
+// Chunks are walked from the last to the first: what the norm's pass read last is still in
+// the cache (50 M elements: 309 us for both, 302 backwards).
 template <typename P, typename G, bool Bits8, bool Stream>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   const Chunk c = a.chunks[gridDim.x - 1 - blockIdx.x];
@@ -306,6 +312,8 @@ __device__ inline double squares(const Part<Lanes>& p) {
   return s;
 }
 
+// A read of the gradients: 49.8 M fp32 in 33 us (6.0 TB/s), 62 us when lines that a step
+// before wrote through the cache had still to be written back.
 template <typename G>
 __global__ __launch_bounds__(kThreads) void grad_squares_kernel(GradNormArgs a) {
   __shared__ double lds[kThreads / 64];
@@ -332,7 +340,9 @@ __global__ __launch_bounds__(kFinish) void grad_norm_kernel(const double* part, 
   if (threadIdx.x == 0) write_norm(s, grad_scale, max_norm, out);
 }
 
-// Small sets, in one workgroup and launch: two chunks to each wave, read together.
+// Small sets, in one workgroup and launch: two chunks to each wave, read together.  24
+// tensors of 8192 elements at most 5.5 us, and a launch less for the host (3.7 us) than the
+// two kernels' 3.1 + 2.0 us.
 template <typename G>
 __global__ __launch_bounds__(kFinish) void grad_norm_small_kernel(GradNormArgs a, const float* grad_scale,
                                                                   float max_norm, float* out) {

@@ -13,7 +13,9 @@ enum class Elem : int { f32 = 0, bf16 = 1, f16 = 2 };
 
 // What the last-level cache holds.  A call that moves more has nothing of it left in the
 // caches when it ends: its accesses pass them by (non-temporal), which keeps the lines that
-// it writes from being written back during the next kernel.
+// it writes from being written back during the next kernel.  Measured without and with: a
+// clipped AdamW step of 1.4 GB 302 and 245 us, layer norm of 1.2 GB 232 and 218 us; but a
+// backward of 84 MB, whose rows the caches hold, 27 and 33 us.
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
 
 // ---- normalisation -----------------------------------------------------------------
@@ -66,6 +68,7 @@ constexpr int kStateBlock = 64;          // elements that share an exponent in 8
 // gradient norm's first pass over 50 M 34, 34 and 52 us.
 constexpr int kChunk = 2048;
 constexpr int kTensorsPerLaunch = 232;   // tensors whose pointers fit the kernel arguments
+constexpr int kChunksPerLaunch = 1 << 22;   // a grid's threads stay below 2^32
 
 // A stretch of one tensor that one workgroup handles.
 struct alignas(32) Chunk {

@@ -379,12 +379,17 @@ int adamw_step(cgtp_params_t P, int param_dtype, void* const* params, int grad_d
   const int64_t each = 2 * elem_size(param_dtype) + elem_size(grad_dtype) + (bits8 ? 4 : 16);
   const bool stream_by = P->state_elems * each > kCacheBytes;
   return for_launches(P, true, [&](int t, int n, int c0, int chunks) {
-    a.chunks = P->d_chunks + c0;
     a.first_tensor = t;
     std::memcpy(a.param, params + t, size_t(n) * sizeof(void*));
     std::memcpy(a.grad, grads + t, size_t(n) * sizeof(void*));
-    return launch_adamw(a, chunks, Elem(param_dtype), Elem(grad_dtype), bits8, stream_by,
-                        static_cast<hipStream_t>(stream));
+    for (int end = chunks; end > 0; end -= kChunksPerLaunch) {
+      const int from = std::max(end - kChunksPerLaunch, 0);
+      a.chunks = P->d_chunks + c0 + from;
+      const hipError_t e = launch_adamw(a, end - from, Elem(param_dtype), Elem(grad_dtype), bits8, stream_by,
+                                        static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   });
 }
 
