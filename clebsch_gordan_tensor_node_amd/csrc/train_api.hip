@@ -33,6 +33,7 @@ struct cgtp_params_s {
 namespace {
 
 constexpr int64_t kMaxInt32 = 0x7fffffff;
+constexpr int64_t kMostElems = int64_t(1) << 37;   // of a tensor and of the set before it: past 288 GB
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -246,8 +247,8 @@ int cgtp_params_create(const int64_t* numel, const double* weight_decay, int n_t
       if (numel[t] < 0) return fail(CGTP_ERR_INVALID_ARG, "tensor %d has a negative size", t);
       if (!(wd >= 0) || !std::isfinite(wd))
         return fail(CGTP_ERR_INVALID_ARG, "weight decay of tensor %d must be finite and not negative", t);
-      if (numel[t] > (int64_t(1) << 40) || chunks.size() + size_t(numel[t] / kChunk) + 1 > size_t(kMaxInt32))
-        return fail(CGTP_ERR_UNSUPPORTED, "too many elements");
+      if (numel[t] > kMostElems || P.state_elems > kMostElems)
+        return fail(CGTP_ERR_UNSUPPORTED, "more than 2^37 elements");
       P.numel.push_back(numel[t]);
       P.offset.push_back(P.state_elems);
       for (int64_t at = 0; at < numel[t]; at += kChunk)

@@ -388,6 +388,44 @@ def test_adamw_steps_bitwise(sizes, bits, pt, gt, skip, dev):
             assert np.array_equal(vr.double().cpu().numpy(), T.decode(codes[1], codes[3], False))
 
 
+@pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-20, 1e10, 1e17])
+def test_adamw8_codes_of_extreme_moments(size, dev):
+    # the block exponent spans fp32's range, subnormal moments and vanishing squares included
+    rng = np.random.default_rng(13)
+    s = C.ParamSet([1000])
+    p, state = _tensors(rng, [1000], torch.float32, dev), C.adamw_state(s, 8)
+    n = s.state_elems
+    codes = [np.zeros(k, np.uint8) for k in (n, n, n // 64, n // 64)]
+    pr = _flat(s, p)
+    for t in (1, 2, 3):
+        g = _tensors(rng, [1000], torch.float32, dev, scale=size)
+        C.adamw_step(s, p, g, state, lr=1e-2, step=t, seed=t)
+        m, v = T.decode(codes[0], codes[2], True).astype(np.float32), T.decode(codes[1], codes[3], False).astype(np.float32)
+        pr, m, _, root = T.adamw_f32(pr, _flat(s, g), m, v * v, 1e-2, 0.9, 0.999, 1e-8, t)
+        h = T.random_bits(np.arange(n), t)
+        (codes[0], codes[2]), (codes[1], codes[3]) = T.encode(m, h & 0xffff, True), T.encode(root, h >> 16, False)
+        for name, a, b in zip(("m", "r", "m exponents", "r exponents"), state, codes):
+            assert np.array_equal(a.cpu().numpy(), b), (t, name, (a.cpu().numpy() != b).sum())
+        assert np.array_equal(_flat(s, p)[:1000], pr[:1000])
+
+
+def test_adamw8_rounds_by_the_seed(dev):
+    g = [torch.randn(6400, device=dev, generator=torch.Generator(device=dev).manual_seed(0))]
+    s = C.ParamSet([6400])
+    got = []
+    for seed in (1, 1, 2, -3, (1 << 32) + 1):
+        state = C.adamw_state(s, 8)
+        C.adamw_step(s, [torch.zeros(6400, device=dev)], g, state, lr=1e-2, step=1, seed=seed)
+        got.append(state)
+    same = [[torch.equal(a, b) for a, b in zip(got[0], q)] for q in got]
+    assert all(same[1]) and all(same[4])               # the seed's low 32 bits
+    for q in (same[2], same[3]):
+        assert q == [False, False, True, True]         # exponents do not hang on it
+    # between two seeds' codes lies at most one step
+    d = (got[0][1].int() - got[2][1].int()).abs()
+    assert d.max() == 1 and 0.2 < (d > 0).float().mean() < 0.5   # two draws differ with probability 2 f (1 - f), a third on average
+
+
 def test_adamw_against_64_bits(dev):
     rng = np.random.default_rng(8)
     sizes = [5000, 77]
