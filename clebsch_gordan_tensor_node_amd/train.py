@@ -42,11 +42,10 @@ def _on(t, name, dev):
         raise ValueError(f"{name} is on device {at}, expected {dev}")
 
 
-def _rows(t, name, shape=None, dtype=None):
-    """Checks a [rows, width] device tensor whose rows are dense; its row stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a device (cuda) tensor")
-    if (t.dtype != dtype) if dtype is not None else (t.dtype not in ELEM):
+def _rows(t, name, dev, shape=None, dtype=None):
+    """Checks a [rows, width] tensor on device `dev` whose rows are dense; its row stride."""
+    _on(t, name, dev)
+    if (t.dtype is not dtype) if dtype is not None else (t.dtype not in ELEM):
         raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
     if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {'(rows, width)' if shape is None else tuple(shape)}")
@@ -54,7 +53,7 @@ def _rows(t, name, shape=None, dtype=None):
     ld, inner = t.stride()
     if (inner != 1 and f > 1) or (ld < f and n > 1):
         raise ValueError(f"{name} must have dense rows that do not overlap, got strides {t.stride()}")
-    return max(ld, f)
+    return ld if ld > f else f
 
 
 def _vec(t, n, name, x, dev):
@@ -62,23 +61,22 @@ def _vec(t, n, name, x, dev):
     if t is None:
         return None, None
     _on(t, name, dev)
-    if t.dtype != torch.float32 and t.dtype != x.dtype:
-        raise TypeError(f"{name} must be float32 or {x.dtype}, got {t.dtype}")
-    if t.shape != (n,):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({n},)")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr(), t.dtype
+    d = t.dtype
+    if d is not torch.float32 and d is not x.dtype:
+        raise TypeError(f"{name} must be float32 or {x.dtype}, got {d}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape ({n},), got {tuple(t.shape)}")
+    return t.data_ptr(), d
 
 
 def _head(plan, x):
     """The leading arguments of a norm call, and x's row stride, weights, biases, shape of
     stats and device.  The library's calls run on the current device: x has to be there."""
-    ld = _rows(x, "x")
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a device (cuda) tensor")
+    dev = torch.cuda.current_device()
+    ld = _rows(x, "x", dev)
     n, f = x.shape
-    dev = x.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"x is on device {dev}, the current device is {torch.cuda.current_device()}")
     if plan is None:
         return (ELEM[x.dtype], n, f), ld, f, f, (2, n), dev
     if f != plan.n_features:
@@ -89,14 +87,13 @@ def _head(plan, x):
 def _forward(call, plan, x, weight, bias, eps, out):
     head, ld, nw, nb, stats_shape, dev = _head(plan, x)
     (w, tw), (b, tb) = _vec(weight, nw, "weight", x, dev), _vec(bias, nb, "bias", x, dev)
-    if tw is not None and tb is not None and tw != tb:
+    if tw is not tb and tw is not None and tb is not None:
         raise TypeError(f"weight ({tw}) and bias ({tb}) must have one type")
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
         ld_y = x.shape[1]
     else:
-        _on(out, "out", dev)
-        ld_y = _rows(out, "out", x.shape, x.dtype)
+        ld_y = _rows(out, "out", dev, x.shape, x.dtype)
     stats = x.new_empty(stats_shape, dtype=torch.float32)
     check(call(*head, x.data_ptr(), ld, ELEM[tw or tb or torch.float32], w, b, eps, out.data_ptr(), ld_y,
                stats.data_ptr(), _raw_stream(dev)))
@@ -105,8 +102,7 @@ def _forward(call, plan, x, weight, bias, eps, out):
 
 def _backward(call, size, plan, grad_out, x, stats, weight, need, workspace):
     head, ld, nw, nb, stats_shape, dev = _head(plan, x)
-    _on(grad_out, "grad_out", dev)
-    ld_g = _rows(grad_out, "grad_out", x.shape, x.dtype)
+    ld_g = _rows(grad_out, "grad_out", dev, x.shape, x.dtype)
     w, wt = _vec(weight, nw, "weight", x, dev)
     wt = wt or torch.float32
     _on(stats, "stats", dev)
