@@ -24,6 +24,7 @@ CGTP_PATHS_ALL = 0
 CGTP_PATHS_PARITY = 1
 CGTP_PLAN_HOST_ONLY = 1
 CGTP_PLAN_FP64 = 2
+CGTP_ADAMW_SCALARS_BYTES = 24
 ELEM = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # CGTP_F32, CGTP_BF16, CGTP_F16
 
 EXPORTED = [
@@ -35,8 +36,8 @@ EXPORTED = [
     "cgtp_layer_norm_forward", "cgtp_layer_norm_backward_workspace_size", "cgtp_layer_norm_backward",
     "cgtp_norm_create", "cgtp_norm_info", "cgtp_norm_destroy", "cgtp_irreps_norm_forward",
     "cgtp_irreps_norm_backward_workspace_size", "cgtp_irreps_norm_backward", "cgtp_params_create",
-    "cgtp_params_info", "cgtp_params_destroy", "cgtp_adamw_step", "cgtp_adamw_step_8bit", "cgtp_adamw_read_8bit",
-    "cgtp_grad_norm_workspace_size", "cgtp_grad_norm",
+    "cgtp_params_info", "cgtp_params_destroy", "cgtp_adamw_step", "cgtp_adamw_scalars",
+    "cgtp_adamw_step_8bit", "cgtp_adamw_read_8bit", "cgtp_grad_norm_workspace_size", "cgtp_grad_norm",
 ]
 
 
@@ -102,8 +103,9 @@ def load():
         "cgtp_params_create": ([ctypes.POINTER(I64), DP, I32, ctypes.c_uint, ctypes.POINTER(P)], I32),
         "cgtp_params_info": ([P, ctypes.POINTER(I32), ctypes.POINTER(I64), ctypes.POINTER(I64)], I32),
         "cgtp_params_destroy": ([P], None),
-        "cgtp_adamw_step": ([P, I32, P, I32, P, P, P, F64, F64, F64, F64, I64, P, P], I32),
-        "cgtp_adamw_step_8bit": ([P, I32, P, I32, P, P, P, P, P, F64, F64, F64, F64, I64, U32, P, P], I32),
+        "cgtp_adamw_step": ([P, I32, P, I32, P, P, P, F64, F64, F64, F64, I64, P, P, P], I32),
+        "cgtp_adamw_scalars": ([P, P, F64, F64, F64, U32, P, P, P], I32),
+        "cgtp_adamw_step_8bit": ([P, I32, P, I32, P, P, P, P, P, F64, F64, F64, F64, I64, U32, P, P, P], I32),
         "cgtp_adamw_read_8bit": ([P, P, P, P, P, P, P, P], I32),
         "cgtp_grad_norm_workspace_size": ([P, ctypes.POINTER(SZ)], I32),
         "cgtp_grad_norm": ([P, I32, P, P, F64, P, P, SZ, P], I32),

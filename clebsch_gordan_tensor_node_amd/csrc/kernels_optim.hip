@@ -62,14 +62,15 @@ __device__ inline float nan() { return __builtin_nanf(""); }
 struct Moments {
   float p, m, v, root;
 };
-__device__ inline Moments adamw(const AdamwArgs& a, float p, float g, float m, float v, float kept) {
+__device__ inline Moments adamw(const AdamwArgs& a, const AdamwScalars& h, float p, float g, float m, float v,
+                                float kept) {
 #pragma clang fp contract(off)
   Moments o;
   o.p = p * kept;
   o.m = m * a.b1 + g * a.c1;
   o.v = v * a.b2 + g * g * a.c2;
   o.root = sqrtf(o.v);
-  o.p = o.p - o.m * a.step_size / (o.root * a.inv_root + a.eps);
+  o.p = o.p - o.m * h.step_size / (o.root * h.inv_root + a.eps);
   return o;
 }
 
@@ -144,13 +145,13 @@ static_assert(kStateBlock == 16 * kVec, "a block of states is 16 lanes");
 
 // One chunk.  Full: all kChunk elements are there, nothing is guarded.
 template <typename P, typename G, bool Bits8, bool Stream, bool Full>
-__device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float scale) {
+__device__ inline void adamw_chunk(const AdamwArgs& a, const AdamwScalars& h, const Chunk& c, float scale) {
   P* p = static_cast<P*>(a.param[c.tensor - a.first_tensor]) + c.start;
   const G* g = static_cast<const G*>(a.grad[c.tensor - a.first_tensor]) + c.start;
   float *m = a.m + c.state, *v = a.v + c.state;
   uint8_t *m_code = a.m_code + c.state, *r_code = a.r_code + c.state;
   uint8_t *m_exp = a.m_exp + c.state / kStateBlock, *r_exp = a.r_exp + c.state / kStateBlock;
-  const float kept = float(1.0 - a.lr * c.decay);
+  const float kept = float(1.0 - h.lr * c.decay);
   const unsigned n = Full ? kChunk : unsigned(c.n), whole = (n + kStateBlock - 1) / kStateBlock * kStateBlock;
   float pv[kPasses][kVec], gv[kPasses][kVec], mv[kPasses][kVec], vv[kPasses][kVec];
   uint32_t mc[kPasses], rc[kPasses];
@@ -194,7 +195,7 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float sca
     float root[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      const Moments o = adamw(a, pv[k][j], gv[k][j] * scale, mv[k][j], vv[k][j], kept);
+      const Moments o = adamw(a, h, pv[k][j], gv[k][j] * scale, mv[k][j], vv[k][j], kept);
       pv[k][j] = o.p;
       mv[k][j] = o.m;
       vv[k][j] = o.v;
@@ -223,7 +224,7 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const Chunk& c, float sca
         tr = block_max(tr);
       }
       const int em = int(tm >> 23), er = int(tr >> 23), sm = max(em, 1) - 14, sr = max(er, 1) - 14;
-      const uint32_t h0 = place(c.state + i, a.seed);
+      const uint32_t h0 = place(c.state + i, h.seed);
       uint32_t cm = 0, cr = 0;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
@@ -265,10 +266,29 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   const Chunk c = a.chunks[gridDim.x - 1 - blockIdx.x];
   const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
   if (scale != scale) return;   // the gradients are not finite: the step is skipped
+  const AdamwScalars h = a.device ? *a.device : a.here;
   if (c.n == kChunk)
-    adamw_chunk<P, G, Bits8, Stream, true>(a, c, scale);
+    adamw_chunk<P, G, Bits8, Stream, true>(a, h, c, scale);
   else
-    adamw_chunk<P, G, Bits8, Stream, false>(a, c, scale);
+    adamw_chunk<P, G, Bits8, Stream, false>(a, h, c, scale);
+}
+
+// One thread, before the step and on its stream: bound by the launch (norm, count and step
+// of 24 small tensors replay in 18 us; called, the count adds 5 us to 20).  A kernel of its own,
+// so that the step's workgroups read 24 bytes and only one thread raises to powers (in 64
+// bits, as the host does: 1 - b^t loses most of its digits at the first steps).
+__global__ void adamw_scalars_kernel(int64_t* step, const float* lr_device, double lr, double beta1, double beta2,
+                                     uint32_t seed, const float* grad_scale, AdamwScalars* out) {
+  if (grad_scale && *grad_scale != *grad_scale) return;   // skipped: not a step
+  const int64_t t = ++*step;
+  if (lr_device) lr = *lr_device;
+  AdamwScalars h;
+  h.lr = lr;
+  h.step_size = float(lr / (1 - pow(beta1, double(t))));
+  h.inv_root = float(1 / sqrt(1 - pow(beta2, double(t))));
+  h.seed = (seed + uint32_t(t)) * kSeedFactor;
+  h.unused = 0;
+  *out = h;
 }
 
 __device__ inline double block_sum(double v, double* lds) {
@@ -406,6 +426,13 @@ hipError_t launch_adamw(const AdamwArgs& a, int n_chunks, Elem param, Elem grad,
                         hipStream_t s) {
   return param == Elem::f32 ? adamw_p<float>(a, n_chunks, grad, bits8, stream, s)
          : param == Elem::bf16 ? adamw_p<Bf16>(a, n_chunks, grad, bits8, stream, s) : adamw_p<F16>(a, n_chunks, grad, bits8, stream, s);
+}
+
+hipError_t launch_adamw_scalars(int64_t* step, const float* lr_device, double lr, double beta1, double beta2,
+                                uint32_t seed, const float* grad_scale, AdamwScalars* out, hipStream_t s) {
+  hipLaunchKernelGGL(adamw_scalars_kernel, dim3(1), dim3(1), 0, s, step, lr_device, lr, beta1, beta2, seed, grad_scale,
+                     out);
+  return hipGetLastError();
 }
 
 hipError_t launch_grad_squares(const GradNormArgs& a, Elem grad, hipStream_t s) {

@@ -80,6 +80,15 @@ struct alignas(32) Chunk {
 };
 static_assert(sizeof(Chunk) == 32, "Chunk is 32 bytes");
 
+// What a step's number and rate give.
+struct AdamwScalars {
+  double lr;
+  float step_size, inv_root;     // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  uint32_t seed;                 // already multiplied
+  uint32_t unused;
+};
+constexpr uint32_t kSeedFactor = 0x3C6EF373u;
+
 struct AdamwArgs {
   const Chunk* chunks;           // this launch's
   float* m;                      // 32-bit states
@@ -87,15 +96,20 @@ struct AdamwArgs {
   uint8_t *m_code, *r_code;      // 8-bit states: codes and block exponents
   uint8_t *m_exp, *r_exp;
   const float* grad_scale;       // may be null (1)
-  double lr;
+  const AdamwScalars* device;    // null: `here`
+  AdamwScalars here;
   float b1, c1, b2, c2;          // beta and 1 - beta
-  float step_size, inv_root, eps;   // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
-  uint32_t seed;                 // already multiplied
+  float eps;
   int32_t first_tensor;          // of this launch
   void* param[kTensorsPerLaunch];
   const void* grad[kTensorsPerLaunch];
 };
 static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments are limited to 4 KiB");
+
+// Advances *step by one, unless *grad_scale (may be null) is NaN, and writes the scalars of
+// the step with that number; lr_device (may be null) replaces lr.
+hipError_t launch_adamw_scalars(int64_t* step, const float* lr_device, double lr, double beta1, double beta2,
+                                uint32_t seed, const float* grad_scale, AdamwScalars* out, hipStream_t s);
 
 struct GradNormArgs {
   const Chunk* chunks;

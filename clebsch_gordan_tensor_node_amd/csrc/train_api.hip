@@ -357,25 +357,42 @@ int norm_parts(cgtp_params_t P) {
   return parts;
 }
 
-int adamw_step(cgtp_params_t P, int param_dtype, void* const* params, int grad_dtype, const void* const* grads,
-               AdamwArgs& a, bool bits8, double lr, double beta1, double beta2, double eps, int64_t step,
-               const float* grad_scale, void* stream) {
-  if (int rc = check_tensors(P, param_dtype, params, "params")) return rc;
-  if (int rc = check_tensors(P, grad_dtype, grads, "grads")) return rc;
-  if (!(lr >= 0) || !std::isfinite(lr)) return fail(CGTP_ERR_INVALID_ARG, "lr must be finite and not negative");
+int check_betas(double beta1, double beta2) {
   if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1))
     return fail(CGTP_ERR_INVALID_ARG, "betas must be in [0, 1)");
+  return CGTP_OK;
+}
+int check_lr(double lr) {
+  if (!(lr >= 0) || !std::isfinite(lr)) return fail(CGTP_ERR_INVALID_ARG, "lr must be finite and not negative");
+  return CGTP_OK;
+}
+
+// step: counted on the host; scalars (not null): those that cgtp_adamw_scalars wrote, and lr,
+// step and the seed are not read.
+int adamw_step(cgtp_params_t P, int param_dtype, void* const* params, int grad_dtype, const void* const* grads,
+               AdamwArgs& a, bool bits8, double lr, double beta1, double beta2, double eps, int64_t step, uint32_t seed,
+               const void* scalars, const float* grad_scale, void* stream) {
+  if (int rc = check_tensors(P, param_dtype, params, "params")) return rc;
+  if (int rc = check_tensors(P, grad_dtype, grads, "grads")) return rc;
+  if (int rc = check_betas(beta1, beta2)) return rc;
   if (!(eps >= 0) || !std::isfinite(eps)) return fail(CGTP_ERR_INVALID_ARG, "eps must be finite and not negative");
-  if (step < 1) return fail(CGTP_ERR_INVALID_ARG, "step counts from 1");
   if (!aligned(grad_scale, 4)) return fail(CGTP_ERR_INVALID_ARG, "misaligned grad_scale");
+  if (scalars) {
+    if (!aligned(scalars, 8)) return fail(CGTP_ERR_INVALID_ARG, "scalars must be 8-byte aligned");
+    a.device = static_cast<const AdamwScalars*>(scalars);
+  } else {
+    if (int rc = check_lr(lr)) return rc;
+    if (step < 1) return fail(CGTP_ERR_INVALID_ARG, "step counts from 1");
+    a.here.lr = lr;
+    a.here.step_size = float(lr / (1 - std::pow(beta1, double(step))));
+    a.here.inv_root = float(1 / std::sqrt(1 - std::pow(beta2, double(step))));
+    a.here.seed = seed * kSeedFactor;
+  }
   a.grad_scale = grad_scale;
-  a.lr = lr;
   a.b1 = float(beta1);
   a.c1 = float(1 - beta1);
   a.b2 = float(beta2);
   a.c2 = float(1 - beta2);
-  a.step_size = float(lr / (1 - std::pow(beta1, double(step))));
-  a.inv_root = float(1 / std::sqrt(1 - std::pow(beta2, double(step))));
   a.eps = float(eps);
   const int64_t each = 2 * elem_size(param_dtype) + elem_size(grad_dtype) + (bits8 ? 4 : 16);
   const bool stream_by = P->state_elems * each > kCacheBytes;
@@ -400,21 +417,21 @@ extern "C" {
 
 int cgtp_adamw_step(cgtp_params_t P, int param_dtype, void* const* params, int grad_dtype, const void* const* grads,
                     float* m, float* v, double lr, double beta1, double beta2, double eps, int64_t step,
-                    const float* grad_scale, void* stream) {
+                    const void* scalars, const float* grad_scale, void* stream) {
   if (int rc = check_set(P)) return rc;
   if (P->state_elems > 0 && (!m || !v)) return fail(CGTP_ERR_INVALID_ARG, "NULL state");
   if (!aligned(m, 16) || !aligned(v, 16)) return fail(CGTP_ERR_INVALID_ARG, "states must be 16-byte aligned");
   AdamwArgs a{};
   a.m = m;
   a.v = v;
-  return adamw_step(P, param_dtype, params, grad_dtype, grads, a, false, lr, beta1, beta2, eps, step, grad_scale,
-                    stream);
+  return adamw_step(P, param_dtype, params, grad_dtype, grads, a, false, lr, beta1, beta2, eps, step, 0, scalars,
+                    grad_scale, stream);
 }
 
 int cgtp_adamw_step_8bit(cgtp_params_t P, int param_dtype, void* const* params, int grad_dtype,
                          const void* const* grads, uint8_t* m_code, uint8_t* r_code, uint8_t* m_exp, uint8_t* r_exp,
                          double lr, double beta1, double beta2, double eps, int64_t step, uint32_t seed,
-                         const float* grad_scale, void* stream) {
+                         const void* scalars, const float* grad_scale, void* stream) {
   if (int rc = check_set(P)) return rc;
   if (P->state_elems > 0 && (!m_code || !r_code || !m_exp || !r_exp)) return fail(CGTP_ERR_INVALID_ARG, "NULL state");
   if (!aligned(m_code, 16) || !aligned(r_code, 16)) return fail(CGTP_ERR_INVALID_ARG, "codes must be 16-byte aligned");
@@ -423,9 +440,22 @@ int cgtp_adamw_step_8bit(cgtp_params_t P, int param_dtype, void* const* params, 
   a.r_code = r_code;
   a.m_exp = m_exp;
   a.r_exp = r_exp;
-  a.seed = seed * 0x3C6EF373u;
-  return adamw_step(P, param_dtype, params, grad_dtype, grads, a, true, lr, beta1, beta2, eps, step, grad_scale,
-                    stream);
+  return adamw_step(P, param_dtype, params, grad_dtype, grads, a, true, lr, beta1, beta2, eps, step, seed, scalars,
+                    grad_scale, stream);
+}
+
+int cgtp_adamw_scalars(int64_t* step, const float* lr_device, double lr, double beta1, double beta2, uint32_t seed,
+                       const float* grad_scale, void* scalars, void* stream) {
+  static_assert(sizeof(AdamwScalars) == CGTP_ADAMW_SCALARS_BYTES, "size in cgtp.h");
+  if (!step || !scalars) return fail(CGTP_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned(step, 8) || !aligned(scalars, 8) || !aligned(lr_device, 4) || !aligned(grad_scale, 4))
+    return fail(CGTP_ERR_INVALID_ARG, "misaligned pointer");
+  if (!lr_device)
+    if (int rc = check_lr(lr)) return rc;
+  if (int rc = check_betas(beta1, beta2)) return rc;
+  CGTP_HIP(launch_adamw_scalars(step, lr_device, lr, beta1, beta2, seed, grad_scale,
+                                static_cast<AdamwScalars*>(scalars), static_cast<hipStream_t>(stream)));
+  return ok();
 }
 
 int cgtp_adamw_read_8bit(cgtp_params_t P, const uint8_t* m_code, const uint8_t* r_code, const uint8_t* m_exp,

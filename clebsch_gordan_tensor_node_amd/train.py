@@ -326,23 +326,45 @@ def _laid(params, tensors, what):
     return p
 
 
-def adamw_step(params: ParamSet, tensors, grads, state, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
-               step: int = 1, grad_scale=None, seed: int = 0):
+def _scalars(params, lr, betas, step, scale, seed, stream):
+    """The scalars of a step that is counted on the device; the tensor that holds them."""
+    if step.get_device() != params.index or step.dtype != torch.int64 or step.numel() != 1:
+        raise TypeError("step must be an int, or an int64 tensor of one element on the set's device")
+    lr_at = None
+    if isinstance(lr, torch.Tensor):
+        if lr.get_device() != params.index or lr.dtype != torch.float32 or lr.numel() != 1:
+            raise TypeError("lr must be a number, or a float32 tensor of one element on the set's device")
+        lr, lr_at = 0.0, lr.data_ptr()
+    out = torch.empty(_lib.CGTP_ADAMW_SCALARS_BYTES // 8, dtype=torch.int64, device=params.device)
+    check(load().cgtp_adamw_scalars(step.data_ptr(), lr_at, lr, betas[0], betas[1], seed & 0xffffffff, scale,
+                                    out.data_ptr(), stream))
+    return out
+
+
+def adamw_step(params: ParamSet, tensors, grads, state, lr, betas=(0.9, 0.999), eps: float = 1e-8, step=1,
+               grad_scale=None, seed: int = 0):
     """One AdamW step of the set, in place on `tensors` and `state`; step counts from 1.
 
     tensors and grads: lists of contiguous device tensors (or params.pointers of them).
     grad_scale: a device tensor of one fp32 (grad_norm's second value, or an inverse loss
     scale) that multiplies the gradients; NaN skips the step.  With 8-bit states, seed
-    chooses the rounding: pass another each step.  Asynchronous on the current stream."""
+    chooses the rounding: pass another each step.  Asynchronous on the current stream.
+
+    For steps in a captured graph, step is an int64 device tensor of one element, 0 before
+    the first step: the call advances it (unless the step is skipped), and adds its number
+    to the seed.  lr may then be a device tensor of one fp32."""
     p, g = _laid(params, tensors, "tensors"), _laid(params, grads, "grads")
     s, scale, stream = _state(params, state), _scale(params, grad_scale), _raw_stream(params.index)
-    lib = load()
+    lib, at = load(), None
+    if isinstance(step, torch.Tensor):
+        scalars = _scalars(params, lr, betas, step, scale, seed, stream)
+        lr, step, at = 0.0, 1, scalars.data_ptr()
     if len(s) == 2:
         check(lib.cgtp_adamw_step(params.handle, p.type, p.array, g.type, g.array, *s, lr, betas[0], betas[1], eps,
-                                  step, scale, stream))
+                                  step, at, scale, stream))
     else:
         check(lib.cgtp_adamw_step_8bit(params.handle, p.type, p.array, g.type, g.array, *s, lr, betas[0], betas[1],
-                                       eps, step, seed & 0xffffffff, scale, stream))
+                                       eps, step, seed & 0xffffffff, at, scale, stream))
 
 
 def adamw_moments(params: ParamSet, state):

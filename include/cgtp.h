@@ -354,11 +354,22 @@ void cgtp_params_destroy(cgtp_params_t set);
  *   p <- p - (lr / (1 - beta1^step)) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  * grad_scale (device fp32, NULL = 1): the inverse of a loss scale, or the factor that
  * cgtp_grad_norm writes; where it is NaN the whole step is skipped, params and states
- * untouched.  Asynchronous on `stream`; bitwise reproducible.  The scalars travel in the
- * launch: a captured graph repeats the step number it was captured with. */
+ * untouched.  Asynchronous on `stream`; bitwise reproducible.  lr and step travel in the
+ * launch, so that a captured graph would repeat the step that it was captured with; with
+ * scalars (device, not NULL) both come from cgtp_adamw_scalars instead. */
 int cgtp_adamw_step(cgtp_params_t set, int param_dtype, void* const* params, int grad_dtype, const void* const* grads,
                     float* m, float* v, double lr, double beta1, double beta2, double eps, int64_t step,
-                    const float* grad_scale, void* stream);
+                    const void* scalars, const float* grad_scale, void* stream);
+
+/* A step counter on the device, for steps in a captured graph: advances step[0] (device, 0
+ * before the first step) by one and writes into scalars (device, CGTP_ADAMW_SCALARS_BYTES,
+ * 8-byte aligned) what the step with that number takes from lr, the betas and the seed (of
+ * the 8-bit states; the step's number is added to it).  lr_device (device, may be NULL)
+ * replaces lr, unchecked.  Where grad_scale (may be NULL) is NaN nothing is advanced or written: the
+ * step behind it is skipped.  Runs on `stream` before that step, with its betas. */
+#define CGTP_ADAMW_SCALARS_BYTES 24
+int cgtp_adamw_scalars(int64_t* step, const float* lr_device, double lr, double beta1, double beta2, uint32_t seed,
+                       const float* grad_scale, void* scalars, void* stream);
 
 /* The same step with the states in 8 bits: codes of m and of r = sqrt(v) [state_elems each,
  * 16-byte aligned] and one exponent byte per block of 64 elements [state_elems / 64 each];
@@ -374,7 +385,7 @@ int cgtp_adamw_step(cgtp_params_t set, int param_dtype, void* const* params, int
 int cgtp_adamw_step_8bit(cgtp_params_t set, int param_dtype, void* const* params, int grad_dtype,
                          const void* const* grads, uint8_t* m_code, uint8_t* r_code, uint8_t* m_exp, uint8_t* r_exp,
                          double lr, double beta1, double beta2, double eps, int64_t step, uint32_t seed,
-                         const float* grad_scale, void* stream);
+                         const void* scalars, const float* grad_scale, void* stream);
 
 /* The values that 8-bit states stand for, m and r [state_elems] in bf16 (which holds them
  * exactly), 16-byte aligned: for checkpoints and inspection. */

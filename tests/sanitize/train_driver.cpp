@@ -74,10 +74,17 @@ int main() {
   EXPECT(elems == at);
   EXPECT(cgtp_grad_norm_workspace_size(set, &bytes) == CGTP_OK && bytes > 0);
   std::vector<void*> ptr(sizes.size(), buf);
-  EXPECT(cgtp_adamw_step(set, 0, ptr.data(), 0, ptr.data(), buf, buf, 1e-3, 0.9, 0.999, 1e-8, 1, nullptr, nullptr) ==
+  EXPECT(cgtp_adamw_step(set, 0, ptr.data(), 0, ptr.data(), buf, buf, 1e-3, 0.9, 0.999, 1e-8, 1, nullptr, nullptr,
+                         nullptr) ==
          CGTP_ERR_INVALID_ARG);
   EXPECT(std::strstr(cgtp_last_error(), "HOST_ONLY") != nullptr);
   cgtp_params_destroy(set);
+  int64_t step = 0;
+  EXPECT(cgtp_adamw_scalars(nullptr, nullptr, 1e-3, 0.9, 0.999, 0, nullptr, buf, nullptr) == CGTP_ERR_INVALID_ARG);
+  EXPECT(cgtp_adamw_scalars(&step, nullptr, -1.0, 0.9, 0.999, 0, nullptr, buf, nullptr) == CGTP_ERR_INVALID_ARG);
+  EXPECT(cgtp_adamw_scalars(&step, nullptr, 1e-3, 1.0, 0.999, 0, nullptr, buf, nullptr) == CGTP_ERR_INVALID_ARG);
+  EXPECT(cgtp_adamw_scalars(&step, nullptr, 1e-3, 0.9, 0.999, 0, nullptr, buf + 1, nullptr) == CGTP_ERR_INVALID_ARG);
+  EXPECT(step == 0);
   sizes[3] = -1;
   EXPECT(cgtp_params_create(sizes.data(), nullptr, 5, CGTP_PLAN_HOST_ONLY, &set) == CGTP_ERR_INVALID_ARG && !set);
   sizes[3] = int64_t(1) << 41;

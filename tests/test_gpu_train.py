@@ -548,6 +548,60 @@ def test_adamw_set_that_outgrows_the_cache(bits, dev):
             assert np.array_equal(e[at // 64:(at + n) // 64].cpu().numpy(), exp)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_counts_on_the_device(bits, dev):
+    # steps counted on the device equal the host's bit for bit, eager and replayed in a graph; a
+    # skipped step does not count; the rate may change between replays
+    rng = np.random.default_rng(14)
+    sizes = [3000, 70]
+    s = C.ParamSet(sizes, 0.1)
+    start = _tensors(rng, sizes, torch.float32, dev)
+    p, q = [t.clone() for t in start], [t.clone() for t in start]
+    g = s.pointers([torch.empty(n, device=dev) for n in sizes])
+    st, su = C.adamw_state(s, bits), C.adamw_state(s, bits)
+    count = torch.zeros(1, dtype=torch.int64, device=dev)
+    lr, scale = torch.empty(1, device=dev), torch.ones(1, device=dev)
+
+    def step():
+        C.adamw_step(s, q, g, su, lr=lr, betas=(0.9, 0.99), step=count, grad_scale=scale, seed=5)
+
+    def same():
+        assert all(torch.equal(a, b) for a, b in zip((*p, *st), (*q, *su)))
+
+    def draw():
+        for t in g.tensors:
+            t.copy_(torch.from_numpy(rng.normal(size=t.numel())))
+
+    graph = None
+    for t in range(1, 8):
+        draw()
+        rate = 1e-2 / t
+        lr.fill_(rate)
+        C.adamw_step(s, p, g, st, lr=float(np.float32(rate)), betas=(0.9, 0.99), step=t, grad_scale=scale, seed=5 + t)
+        if t == 4:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        if graph is None:
+            step()
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        same()
+        assert int(count) == t
+        if t == 5:
+            scale.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            same()
+            assert int(count) == t
+            scale.fill_(1.0)
+    for bad in (dict(lr=1.0, step=count.int()), dict(lr=lr.double(), step=count), dict(lr=1.0, step=count.cpu())):
+        with pytest.raises(TypeError):
+            C.adamw_step(s, q, g, su, **bad)
+
+
 def test_adamw_tensor_past_32_bits(dev):
     # one tensor of 2^32 + 1000 elements in bf16 with 8-bit states: its last elements move as
     # those of a small one at the same places, and the first ones too

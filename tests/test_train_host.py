@@ -99,7 +99,8 @@ def test_irreps_norm_and_set_refusals():
     # a set without a device is refused by every device call
     s = C.ParamSet([4], host_only=True)
     none = ctypes.c_void_p()
-    assert lib.cgtp_adamw_step(s.handle, F32, none, F32, none, None, None, 1e-3, 0.9, 0.999, 1e-8, 1, None, None) == INVALID
+    assert lib.cgtp_adamw_step(s.handle, F32, none, F32, none, None, None, 1e-3, 0.9, 0.999, 1e-8, 1, None, None,
+                               None) == INVALID
     assert b"HOST_ONLY" in lib.cgtp_last_error()
     assert lib.cgtp_grad_norm(s.handle, F32, none, None, 1.0, None, None, 0, None) == INVALID
     lib.cgtp_norm_destroy(None)
