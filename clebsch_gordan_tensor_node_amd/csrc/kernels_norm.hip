@@ -37,7 +37,7 @@ struct TermArgs {
   int32_t variant;        // which (V, G, C) handles it
   int32_t n_blocks;       // its workgroups
   int32_t n_parts;        // backward: its partial sums
-  uint32_t inv_d;         // ceil(2^32 / d) for d > 1: e / d = (e * inv_d) >> 32 for e < 2^32 / d
+  uint32_t inv_d;         // ceil(2^32 / d) for d > 1: e / d = (e * inv_d) >> 32 for e < 2^29
   int64_t part;           // backward: its partial sums in `part`: [n_parts][len] of the weight's
                           // gradient, then (centred terms) as much of the bias's
 };
@@ -692,7 +692,7 @@ Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) 
   const int e = elems_of(longest(p), elem_bytes, backward);
   y.block = block_of(longest(p), e);
   // rows that outgrow the last-level cache, in plans of up to kCapSmall terms
-  y.stream = p.n_terms <= kCapSmall && rows * p.features * elem_bytes * (backward ? 3 : 2) > kCacheBytes;
+  y.stream = p.n_terms <= kCapSmall && double(rows) * p.features * elem_bytes * (backward ? 3 : 2) > kCacheBytes;
   // rows so few that one workgroup per term takes them all, in at most four turns: it then
   // writes the weight's and bias's gradients itself
   y.direct = backward;

@@ -104,6 +104,7 @@ int norm_forward(const NormShape& p, int dtype, int64_t rows, const void* x, int
 int norm_backward_workspace(const NormShape& p, int64_t rows, size_t* bytes) {
   if (!bytes) return fail(CGTP_ERR_INVALID_ARG, "NULL argument");
   if (rows < 0) return fail(CGTP_ERR_INVALID_ARG, "negative size");
+  rows = std::min(rows, kMaxInt32);   // more are refused by the call itself
   *bytes = (norm_part_floats(rows, p) * sizeof(float) + 255) / 256 * 256;
   return ok();
 }
@@ -186,7 +187,8 @@ int cgtp_norm_create(const char* irreps, cgtp_norm_t* out) {
         return fail(CGTP_ERR_UNSUPPORTED, "irrep %dx%d: need l <= 6 and mul > 0", r.mul, r.l);
       const bool centred = r.l == 0 && r.p == 1;
       const int64_t d = 2 * r.l + 1, len = r.mul * d;
-      if (P.features + len > kMaxInt32 / 2) return fail(CGTP_ERR_UNSUPPORTED, "row wider than 2^30 - 1");
+      // up to here the kernels' e / d = (e * inv_d) >> 32 is exact for every d <= 13
+      if (P.features + len > int64_t(1) << 29) return fail(CGTP_ERR_UNSUPPORTED, "irreps row wider than 2^29");
       P.terms.push_back(NormTerm{int32_t(P.features), int32_t(len), int32_t(d), int32_t(P.weights),
                                  centred ? int32_t(P.biases) : -1});
       P.features += len;

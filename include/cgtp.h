@@ -313,7 +313,7 @@ int cgtp_layer_norm_backward(int dtype, int64_t n_rows, int64_t width, const voi
  * would break equivariance under rotation, or under inversion for 0o): with
  *   s2 = sum(x^2) / (mul (2l+1)), rstd = 1/sqrt(s2 + eps),  y[u, m] = x[u, m] rstd weight[u].
  * The plan holds host memory only and belongs to no device; it may be shared by threads
- * and streams.  At most 64 terms, l <= 6. */
+ * and streams.  At most 64 terms, l <= 6, rows of at most 2^29 values. */
 typedef struct cgtp_norm_s* cgtp_norm_t;
 int cgtp_norm_create(const char* irreps, cgtp_norm_t* out);
 

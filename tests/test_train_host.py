@@ -107,6 +107,24 @@ def test_irreps_norm_and_set_refusals():
     lib.cgtp_params_destroy(None)
 
 
+def test_norm_size_limits():
+    # 2^29 values per irreps row, where the kernels' quotient e / (2l + 1) = e m >> 32 is exact
+    for d in (3, 5, 7, 9, 11, 13):
+        m = -(-2 ** 32 // d)
+        assert all(e * m >> 32 == e // d for q in (1, 2 ** 28 // d, 2 ** 29 // d) for e in (q * d - 1, q * d))
+        assert (2 ** 29 - 1) * (m * d - 2 ** 32) < 2 ** 32
+    lib, h, ws = C._lib.load(), ctypes.c_void_p(), ctypes.c_size_t()
+    assert lib.cgtp_norm_create(f"{2 ** 29 // 9 + 1}x4e".encode(), ctypes.byref(h)) == UNSUPPORTED and not h
+    assert lib.cgtp_norm_create(f"{2 ** 28}x0e+{2 ** 28 + 1}x0o".encode(), ctypes.byref(h)) == UNSUPPORTED and not h
+    assert lib.cgtp_norm_create(f"{2 ** 29 // 9}x4e".encode(), ctypes.byref(h)) == 0
+    sizes = []
+    for rows in (2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1):   # more rows than a call takes: the largest call's
+        assert lib.cgtp_irreps_norm_backward_workspace_size(h, rows, ctypes.byref(ws)) == 0
+        sizes.append(ws.value)
+    assert sizes[0] > 0 and len(set(sizes)) == 1
+    lib.cgtp_norm_destroy(h)
+
+
 def test_python_refuses_host_tensors():
     x = torch.zeros(3, 8)
     with pytest.raises(TypeError):
