@@ -202,8 +202,10 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const AdamwScalars& h, co
       root[j] = o.root;
     }
     if constexpr (Bits8) {
-      // the block's largest magnitudes; where one is not finite, the largest finite ones
-      uint32_t tm = 0, tr = 0;
+      // the block's largest magnitudes; where one is not finite, the largest finite ones.  A
+      // moment that is not finite is encoded as 0, under the code of NaN: an encoded infinity
+      // has more than 8 bits and would reach into the next element's.
+      uint32_t tm = 0, tr = 0, nm = 0, nr = 0;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         tm = max(tm, bits_of(mv[k][j]) & 0x7fffffffu);
@@ -216,30 +218,28 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const AdamwScalars& h, co
         tm = tr = 0;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-          const uint32_t bm = bits_of(mv[k][j]) & 0x7fffffffu, br = bits_of(root[j]) & 0x7fffffffu;
-          tm = max(tm, bm < kInf ? bm : 0u);
-          tr = max(tr, br < kInf ? br : 0u);
+          if (!(fabsf(mv[k][j]) < float_of(kInf))) {
+            nm |= (kMNan | (mv[k][j] < 0 ? 0x80u : 0u)) << (8 * j);
+            mv[k][j] = 0;
+          }
+          if (!(root[j] < float_of(kInf))) {
+            nr |= kRNan << (8 * j);
+            root[j] = 0;
+          }
+          tm = max(tm, bits_of(mv[k][j]) & 0x7fffffffu);
+          tr = max(tr, bits_of(root[j]));
         }
         tm = block_max(tm);
         tr = block_max(tr);
       }
       const int em = int(tm >> 23), er = int(tr >> 23), sm = max(em, 1) - 14, sr = max(er, 1) - 14;
       const uint32_t h0 = place(c.state + i, h.seed);
-      uint32_t cm = 0, cr = 0;
+      uint32_t cm = nm, cr = nr;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         const uint32_t u = mix(h0 + j * kGolden);
         cm |= encode_m(mv[k][j], sm, u & 0xffff) << (8 * j);
         cr |= encode_r(root[j], sr, u >> 16) << (8 * j);
-      }
-      if (bad) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const uint32_t sign = bits_of(mv[k][j]) >> 31 << 7;
-          if (!(fabsf(mv[k][j]) < float_of(kInf)))
-            cm = (cm & ~(0xffu << (8 * j))) | (kMNan | (mv[k][j] < 0 ? sign : 0u)) << (8 * j);
-          if (!(root[j] < float_of(kInf))) cr |= kRNan << (8 * j);
-        }
       }
       write4<Stream>(m_code + i, __builtin_bit_cast(Four<uint8_t>, cm));
       write4<Stream>(r_code + i, __builtin_bit_cast(Four<uint8_t>, cr));

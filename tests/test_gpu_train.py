@@ -463,6 +463,41 @@ def test_adamw8_follows_adamw32(dev):
     assert abs((r.float()[:20000] / r32[:20000]).mean() - 1) < 0.05
 
 
+@pytest.mark.parametrize("place", range(4))
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 1e30])
+def test_adamw8_moments_that_are_not_finite_leave_their_block_alone(bad, place, dev):
+    # one such gradient at each place of a lane's four, beside zeros, small values and the
+    # block's largest (1e30: the square overflows, the first moment does not): codes and
+    # exponents of the whole block equal the reference's, then and in the step after
+    rng = np.random.default_rng(15)
+    n = 64 * 48
+    s = C.ParamSet([n])
+    p, state = _tensors(rng, [n], torch.float32, dev), C.adamw_state(s, 8)
+    codes = [np.zeros(k, np.uint8) for k in (n, n, n // 64, n // 64)]
+    pr = _flat(s, p)
+    for t in (1, 2, 3):
+        v = rng.normal(size=n) * np.where(rng.random(n) < 0.3, 1e-3, 1.0) * (rng.random(n) < 0.7)
+        if t > 1:
+            for k in range(48):   # every block: beside a zero, a small value, the largest
+                at = 64 * k + 4 * (k % 16) + place
+                near = 64 * k + (at + 1 if k % 2 else at - 1) % 64
+                v[near] = (0.0, 1e-3, 4.0)[k % 3]
+                if t == 2:
+                    v[at] = bad
+        g = [torch.from_numpy(v).float().to(dev)]
+        C.adamw_step(s, p, g, state, lr=1e-2, step=t, seed=t)
+        m, v = T.decode(codes[0], codes[2], True).astype(np.float32), T.decode(codes[1], codes[3], False).astype(np.float32)
+        pr, m, _, root = T.adamw_f32(pr, _flat(s, g), m, v * v, 1e-2, 0.9, 0.999, 1e-8, t)
+        assert t == 1 or (~np.isfinite(root)).sum() == 48
+        h = T.random_bits(np.arange(n), t)
+        (codes[0], codes[2]), (codes[1], codes[3]) = T.encode(m, h & 0xffff, True), T.encode(root, h >> 16, False)
+        got = [a.cpu().numpy() for a in state]
+        codes[0][codes[0] == 128] = got[0][got[0] == 128] = 0   # a zero's sign is free
+        for name, a, b in zip(("m", "r", "m exponents", "r exponents"), got, codes):
+            assert np.array_equal(a, b), (t, name, (a != b).sum())
+        assert np.array_equal(_flat(s, p), pr, equal_nan=True)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_skips_on_nan_scale_and_contains_bad_gradients(bits, dev):
     rng = np.random.default_rng(10)
