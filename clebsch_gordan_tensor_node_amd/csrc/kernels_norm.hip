@@ -7,7 +7,9 @@
 // Backward, a = g w:  dx = rstd (a - h sum(a h)/F - sum(a)/F), the last only if centred;
 //   dw = sum over rows (and a channel's components) of g h, db = sum over rows of g.
 // Sums and statistics are fp32 whatever the element type.  s2 is summed from x - mu, not
-// from x^2: a row with a large common offset keeps its digits.
+// from x^2: a row with a large common offset keeps its digits.  mu, an fp32 sum times the
+// rounded 1/F, may miss by some ulp; x - mu is summed along with s2 and corrects both.  A
+// constant row (60000 in 7 columns: y off by 0.78 without) is its bias then.
 //
 // Both passes are bound by HBM: 2 (forward) or 3 (backward) elements moved per element for
 // 8 to 14 operations.  So a stretch is read once into registers: G lanes hold it, C
@@ -196,6 +198,40 @@ __device__ inline float group_sum(float v, float* lds, int& turn) {
   return v;
 }
 
+// The mean from a sum, rounded before anything is taken from it: fused into x - mu it would
+// leave differences about another mean than the one that about_mean moves.
+__device__ inline float mean_of(float sum, float inv) {
+#pragma clang fp contract(off)
+  return sum * inv;
+}
+// Moves mu, a rounded mean, by s1, the mean of x - mu, and returns the variance about it, of
+// which s2 is the mean of (x - mu)^2.  Where that is not finite, both stay as they are.
+__device__ inline float about_mean(float s1, float s2, float& mu) {
+  if (!(s2 < __builtin_inff())) return s2;
+  mu += s1;
+  return fmaxf(s2 - s1 * s1, 0.0f);
+}
+
+// Waits for a row's loads here, on every path.  Left to itself the compiler waits where the
+// values are used, and, as some paths use none, again before the registers' next load, for
+// the row's store too: 100000 x 704 fp32 in four terms 130 us, with this 107, 32768 rows 41
+// and 38.  In 16 bits it costs more than it saves (4096 x 5472 30 and 32 us).
+template <int V, int C>
+__device__ inline void arrived(float (&x)[C][V]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < V; ++j) asm volatile("" : "+v"(x[c][j]));
+}
+// Takes `by` off the lane's elements.
+template <int V, int C>
+__device__ inline void shift(float (&x)[C][V], float by) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[c][j] -= by;
+}
+
 // Where a lane's vectors of a stretch lie.
 template <int V, int G, int C>
 struct Place {
@@ -255,6 +291,29 @@ __device__ inline float own_sum(const Place<V, G, C>& p, F&& f) {
   }
   return s;
 }
+// Adds the lane's own elements to s1, and their squares to s2.
+template <int V, int G, int C>
+__device__ inline void own_sums(const Place<V, G, C>& p, const float (&x)[C][V], float& s1, float& s2) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (c < p.last) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        s1 += x[c][j];
+        s2 += x[c][j] * x[c][j];
+      }
+    } else if (c == p.last) {
+      const bool has = p.has(c);
+      const int skip = p.skip(c);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float v = has && j >= skip ? x[c][j] : 0.0f;
+        s1 += v;
+        s2 += v * v;
+      }
+    }
+  }
+}
 // The channels' weights (or biases) at the lane's elements; `none` where there are none.
 template <typename T, int V, int G, int C>
 __device__ inline void load_weights(const Place<V, G, C>& p, const void* w, int f32, int off, const TermArgs& t,
@@ -283,14 +342,25 @@ __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_term
   int turn = 0;
   for (int64_t r = int64_t(block) * kGroups + threadIdx.x / G; r < a.rows; r += int64_t(t.n_blocks) * kGroups) {
     widen(read_row<Stream>(p, static_cast<const T*>(a.x) + r * a.ld_x + t.off), x);
-    float mu = 0;
-    if (centred) mu = group_sum<G>(own_sum(p, [&](int c, int j) { return x[c][j]; }), lds, turn) * inv;
-    const float s2 = group_sum<G>(own_sum(p, [&](int c, int j) { return (x[c][j] - mu) * (x[c][j] - mu); }), lds, turn);
-    const float rstd = 1.0f / sqrtf(s2 * inv + a.eps);
+    if constexpr (sizeof(T) == 4) arrived(x);
+    float mu = 0, s1 = 0, s2 = 0;
+    if (centred) {
+      mu = mean_of(group_sum<G>(own_sum(p, [&](int c, int j) { return x[c][j]; }), lds, turn), inv);
+      shift(x, mu);
+    }
+    own_sums(p, x, s1, s2);
+    group_sum2<G>(s1, s2, lds, turn);
+    float var = s2 * inv;
+    if (centred) {
+      const float first = mu;
+      var = about_mean(s1 * inv, var, mu);
+      shift(x, mu - first);   // x - mu now, of the mean that the stats hold
+    }
+    const float rstd = 1.0f / sqrtf(var + a.eps);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[c][j] = (x[c][j] - mu) * rstd * w[c][j] + b[c][j];
+      for (int j = 0; j < V; ++j) x[c][j] = x[c][j] * rstd * w[c][j] + b[c][j];
     store_row<Stream>(p, static_cast<T*>(a.y) + r * a.ld_y + t.off, x);
     if (a.stats && p.lane == 0) {
       a.stats[r * n_terms + index] = mu;
@@ -438,7 +508,7 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(NormCall a, T
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ld_x + t.off;
     T* y = static_cast<T*>(a.y) + r * a.ld_y + t.off;
-    float mu = 0, q = 0;
+    float mu = 0, s1 = 0, s2 = 0;
     if (centred) {
       float s = 0;
       wide_loop<B, V>(t.len, [&](int e, int n) {
@@ -446,14 +516,20 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(NormCall a, T
 #pragma unroll
         for (int j = 0; j < V; ++j) s += v[j];
       });
-      mu = group_sum<B>(s, sums, turn) * inv;
+      mu = mean_of(group_sum<B>(s, sums, turn), inv);
     }
     wide_loop<B, V>(t.len, [&](int e, int n) {
       read_some<V>(x + e, n, v);
 #pragma unroll
-      for (int j = 0; j < V; ++j) q += j < n ? (v[j] - mu) * (v[j] - mu) : 0.0f;
+      for (int j = 0; j < V; ++j) {
+        const float d = j < n ? v[j] - mu : 0.0f;
+        s1 += d;
+        s2 += d * d;
+      }
     });
-    const float rstd = 1.0f / sqrtf(group_sum<B>(q, sums, turn) * inv + a.eps);
+    group_sum2<B>(s1, s2, sums, turn);
+    const float var = centred ? about_mean(s1 * inv, s2 * inv, mu) : s2 * inv;
+    const float rstd = 1.0f / sqrtf(var + a.eps);
     wide_loop<B, V>(t.len, [&](int e, int n) {
       float w[V], b[V];
       read_some<V>(x + e, n, v);

@@ -213,6 +213,40 @@ def test_norm_rows_that_are_constant_or_not_finite(dev):
         assert gx[7].isnan().all() and gx[keep].isfinite().all() and gb.isfinite().all()
 
 
+@pytest.mark.parametrize("spec", [7, 13, 14, 41, 100, 1000, 1025, 1312, 5000, 8193, 16385, 40001, "7x0e+5x1o+13x0e",
+                                  "3x1e+20000x0e+41x0e"], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_norm_constant_rows_are_their_bias(dtype, spec, dev):
+    # A row of one value c.  The first mean misses c by at most k u c, k = 70 roundings (chain,
+    # tree and quotient); x - mean is exact there, and its own mean, which is added to the
+    # first, misses by 2 k u of that, far below half an ulp: the mean is c, and y = bias,
+    # exactly.  The variance keeps at most 4 k u (k u c)^2, the difference of two equal terms.
+    terms, f, nw, nb = _shape(spec)
+    values = [100.0, 1000.0, -60000.0, 0.1, 8192.0, 3.0]
+    x = torch.zeros(len(values), f, dtype=dtype, device=dev)
+    for off, m, d, _, b0 in terms:
+        if b0 is not None:
+            x[:, off:off + m] = torch.tensor(values, device=dev)[:, None].to(dtype)
+    w, b = torch.linspace(0.5, 1.5, nw, device=dev), torch.linspace(-1, 1, nb, device=dev)
+    y, st = _call(spec, x, w, b)
+    gen = torch.Generator(device=dev).manual_seed(3)
+    g = torch.randint(-4, 5, x.shape, device=dev, generator=gen).to(dtype)
+    gx, gw, gb = _grads(spec, g, x, st, w)
+    for k, (off, m, d, w0, b0) in enumerate(terms):
+        if b0 is None:
+            continue
+        at = slice(off, off + m)
+        assert torch.equal(st[0, :, k], x[:, off].float())
+        off_by = 4 * U + 2 * (70 * U) ** 3 * x[:, off].double() ** 2 / 1e-5   # of rstd, relative
+        assert ((st[1, :, k].double() * 1e-5 ** 0.5 - 1).abs() <= off_by).all()
+        assert torch.equal(y[:, at], b[b0:b0 + m].to(dtype).expand(len(values), m))
+        assert (gw[w0:w0 + m] == 0).all() and torch.equal(gb[b0:b0 + m], g[:, at].float().sum(0))   # h = 0; small integers
+        a = g[:, at].double() * w[w0:w0 + m].double()
+        # rstd (a - mean a), |a| <= 6, mean a by some 100 u
+        want = ((a - a.mean(1, keepdim=True)) * 1e-5 ** -0.5).cpu().numpy()
+        _near(gx[:, at], want, 6 * 100 * U * 1e-5 ** -0.5 + (off_by[:, None].cpu().numpy() + 4 * U) * np.abs(want), "grad_x")
+
+
 def test_norm_gradient_by_differences(dev):
     for spec in (48, "16x0e+8x1e+16x1o"):
         rng = np.random.default_rng(3)
