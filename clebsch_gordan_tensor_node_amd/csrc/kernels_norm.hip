@@ -23,10 +23,8 @@
 // (5.7 TB/s), of 4096 x 5472 in four terms 38 us (4.7); backward with all gradients of 32768
 // x 704 in four terms 55 us (5.1), of 114688 x 128 bf16 22 + 5 us for the sums of the
 // weight's gradient, which wait for the memory's latency (as do rows of a few lanes).
-#include <algorithm>
-
 #include "elem.hpp"
-#include "launch_train.hpp"
+#include "norm_layout.hpp"
 
 namespace cgtp {
 namespace {
@@ -51,70 +49,6 @@ struct NormArgs {
   int32_t first_block[Cap];   // of each term (INT32_MAX past the last)
   TermArgs term[Cap];
 };
-constexpr int kCapSmall = 8;
-
-// How many lanes G hold a stretch, and in how many vectors C each: the first that has room
-// for its nv = ceil(len / V) vectors.  B is the workgroup's size.
-enum Variant : int {
-  kElem8,   // V = 1, G = 8: shorter than a vector
-  kG4C1,    // nv <= 4
-  kG8C1,    // nv <= 8
-  kG16C1,   // nv <= 16
-  kG32C1,   // nv <= 32
-  kG64C1,   // nv <= 64
-  kG64C2,   // nv <= 128, if a lane holds that many elements
-  kG64C4,   // nv <= 256, likewise
-  kGBC1,    // nv <= B
-  kGBC2,    // nv <= 2 B, likewise
-  kGBC3,    // nv <= 3 B, likewise
-  kGBC4,    // nv <= 4 B, likewise
-  kWide     // any: the row is read again for each sum
-};
-
-// Elements per lane for a plan whose longest stretch is `longest`, as long as a workgroup's
-// lanes reach.  The more, the fewer waves fit a SIMD's registers; the fewer, the more waves
-// share a stretch and wait for one another.  With 8 and with 16, us for 400 MB: forward of
-// 4096 columns 73 and 78 (fp32), 92 and 109 (bf16), of 8192 87 and 83 (fp32), 95 and 112
-// (bf16); backward of 1024 columns 100 and 86 (fp32), 108 and 116 (bf16), of 4096 88 and 98
-// (fp32), 97 and 135 (bf16), of 8192 101 and 117 (fp32), 139 and 133 (bf16).  12 lets a
-// workgroup of 128 hold 1536 fp32 columns, where 256 leave a third of their lanes idle:
-// forward of 20060 x 1312 42 us, with 8 46; of 114688 x 1312 230 and 236.
-int elems_of(int longest, int elem_bytes, bool backward) {
-  if (longest > 4096) return (elem_bytes == 4) != backward ? 16 : 8;
-  if (longest > 1024 && longest <= 1536 && !backward && elem_bytes == 4) return 12;
-  return longest > 512 && longest <= 1024 && backward && elem_bytes == 4 ? 16 : 8;
-}
-constexpr int kMaxE = 16;
-constexpr int kWideOver = 1024 * kMaxE;
-
-// The workgroup that the longest stretch of a plan needs, with e elements per lane.
-int block_of(int longest, int e) {
-  return longest <= 64 * e ? 256 : longest <= 128 * e ? 128 : longest <= 256 * e ? 256 : longest <= 512 * e ? 512 : 1024;
-}
-
-int variant_of(int len, int elem_bytes, int block, int e) {
-  const int v = 16 / elem_bytes;
-  if (len > block * kMaxE) return kWide;
-  if (len < v) return kElem8;
-  const int nv = (len + v - 1) / v;
-  if (nv <= 4) return kG4C1;
-  if (nv <= 8) return kG8C1;
-  if (nv <= 16) return kG16C1;
-  if (nv <= 32) return kG32C1;
-  if (nv <= 64) return kG64C1;
-  if (nv <= 128 && e >= 2 * v) return kG64C2;
-  if (nv <= 256 && e >= 4 * v) return kG64C4;
-  if (nv <= block) return kGBC1;
-  return nv <= 2 * block ? kGBC2 : nv <= 3 * block && e == 12 ? kGBC3 : kGBC4;
-}
-// Lanes per stretch and vectors per lane.
-int lanes_of(int variant, int block) {
-  constexpr int g[] = {8, 4, 8, 16, 32, 64, 64, 64};
-  return variant <= kG64C4 ? g[variant] : block;
-}
-int vectors_of(int variant) {
-  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : variant == kGBC3 ? 3 : 1;
-}
 
 template <typename T, int V>
 struct Vec {
@@ -651,7 +585,6 @@ __global__ __launch_bounds__(B, E > 8 && sizeof(T) == 2 ? 4 : 1) void norm_bwd_k
 
 // The partial sums of wide stretches, column by column: a thread's column over every
 // kWideSlices-th row.
-constexpr int kWideSlices = 32;
 constexpr int kWideThreads = 256;
 template <typename T>
 __global__ __launch_bounds__(kWideThreads) void norm_wide_w_kernel(NormCall a, TermArgs t, int n_terms, int index) {
@@ -676,9 +609,6 @@ __global__ __launch_bounds__(kWideThreads) void norm_wide_w_kernel(NormCall a, T
 // adds every n-th partial sum, 16 loads of each kind in flight at once (the kernel is a
 // chain of memory latencies, not of bytes), then LDS joins the slices and a channel's
 // components.
-constexpr int kSumThreads = 1024;
-constexpr int kInFlight = 16;
-
 template <typename T, int Cap, int Tile>
 __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) {
   __shared__ float lds[2][kSumThreads / kWave][Tile];
@@ -732,74 +662,6 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormArgs<Cap> a) 
     if (q == 0 && a.c.grad_weight) store_either<T>(a.c.grad_weight, a.c.weight_f32, t.w_off + ch, v);
     if (q == 1 && want_b) store_either<T>(a.c.grad_bias, a.c.weight_f32, t.b_off + ch, v);
   }
-}
-
-// Workgroups of a launch, shared among the terms by their cost: enough to keep the
-// memory busy, which takes more of them where every access goes to HBM, and in the
-// backward no more, since each leaves a row of partial sums.  Measured: forward of 114688 x
-// 1312 fp32 232, 222 and 219 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 38, 36
-// and 41; backward and sums of 768 x 9088 (cached) 23.3, 23.3, 25.0 and 27.8 us with 512,
-// 768, 1024 and 1536, of 32768 x 704 82, 67, 60 and 56.  Past the cache the forward takes
-// more, as long as each has 28 / element bytes turns for the weights that it loads: 114688 x
-// 1312 fp32 in 8192 workgroups of 128 228 us, in 16384 219, but 30000 x 1400 70 and 78; 24414
-// x 4096 bf16 with 12 turns 92 us, with 7 104.
-constexpr int kTurnBytes = 28;
-constexpr int kForwardBlocks = 2048, kForwardBlocksStream = 4096;
-constexpr int kBackwardBlocks = 768, kBackwardBlocksStream = 1536;
-
-int longest(const NormShape& p) {
-  int n = 0;
-  for (int k = 0; k < p.n_terms; ++k) n = std::max(n, p.terms[k].len);
-  return n;
-}
-
-// How the rows are laid over workgroups.
-struct Layout {
-  int block;                      // threads of a workgroup
-  bool stream;                    // rows pass by the last-level cache
-  bool direct;                    // backward: one workgroup per term
-  int max_e;                      // most elements per lane
-  int64_t part;                   // backward: floats of partial sums
-  int variant[kMaxNormTerms], n_blocks[kMaxNormTerms], n_parts[kMaxNormTerms];
-};
-
-Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool backward) {
-  Layout y;
-  const int e = elems_of(longest(p), elem_bytes, backward);
-  y.block = block_of(longest(p), e);
-  // rows that outgrow the last-level cache, in plans of up to kCapSmall terms
-  y.stream = p.n_terms <= kCapSmall && double(rows) * p.features * elem_bytes * (backward ? 3 : 2) > kCacheBytes;
-  // rows so few that one workgroup per term takes them all, in at most four turns: it then
-  // writes the weight's and bias's gradients itself
-  y.direct = backward;
-  y.max_e = 1;
-  int64_t cost = 0, part = 0, each[kMaxNormTerms];
-  for (int k = 0; k < p.n_terms; ++k) {
-    const int v = variant_of(p.terms[k].len, elem_bytes, y.block, e), g = lanes_of(v, y.block), c = vectors_of(v);
-    y.variant[k] = v;
-    if (v == kWide || rows > 4 * (y.block / g)) y.direct = false;
-    y.max_e = std::max(y.max_e, v == kElem8 || v == kWide ? 1 : c * 16 / elem_bytes);
-    // what a stretch costs: its lanes, for its vectors and a part that every stretch has
-    each[k] = v == kWide ? 0 : int64_t(g) * (c + 1);
-    cost += each[k];
-  }
-  const int64_t total = (backward ? (y.stream ? kBackwardBlocksStream : kBackwardBlocks)
-                                  : (y.stream ? kForwardBlocksStream : kForwardBlocks)) * 256 / y.block;
-  for (int k = 0; k < p.n_terms; ++k) {
-    if (y.variant[k] == kWide) {
-      y.n_blocks[k] = 0;   // launched by itself
-    } else {
-      const int64_t groups = y.block / lanes_of(y.variant[k], y.block);
-      const int64_t want = std::max<int64_t>((rows + groups - 1) / groups, 1);
-      int64_t most = std::max<int64_t>(total * each[k] / cost, 1);
-      if (y.stream && !backward) most = std::max(most, want * elem_bytes / kTurnBytes);
-      y.n_blocks[k] = y.direct ? 1 : int(std::min(want, most));
-    }
-    y.n_parts[k] = y.variant[k] == kWide ? kWideSlices : y.n_blocks[k];
-    part += int64_t(y.n_parts[k]) * p.terms[k].len * (p.terms[k].b_off >= 0 ? 2 : 1);
-  }
-  y.part = y.direct ? 0 : part;
-  return y;
 }
 
 // A launch's arguments; returns its workgroups.
@@ -908,28 +770,17 @@ hipError_t backward(const NormCall& c, const NormShape& p, hipStream_t s) {
         const dim3 grid(unsigned((p.terms[k].len + kWideThreads - 1) / kWideThreads), kWideSlices);
         hipLaunchKernelGGL(norm_wide_w_kernel<T>, grid, dim3(kWideThreads), 0, s, c, a.term[k], p.n_terms, k);
       }
-    // Wide tiles read whole lines (a tile that ends inside one has it fetched again by
-    // another die's L2), narrow ones spread short stretches over more workgroups: 9088
-    // columns took 10.1 us in tiles of 16 and 5.4 in tiles of 64, 481 columns 6.6 and 10.2.
-    int tiles = 0, most = 0;
-    for (int k = 0; k < p.n_terms; ++k) {
-      tiles += p.terms[k].len / 64;
-      most = std::max(most, y.n_parts[k]);
-    }
-    const int wide = tiles >= 16 ? 64 : 16;
+    const SumGrid g = lay_out_sums(p, y);
     int at = 0;
     for (int k = 0; k < p.n_terms; ++k) {
-      const int tile = wide / p.terms[k].d * p.terms[k].d;
       a.first_block[k] = at;
-      at += (p.terms[k].len + tile - 1) / tile;
+      at += sum_blocks(p.terms[k], g.tile);
     }
-    // as many slices as keep every load in flight, two at least
-    const int want = (most + kInFlight - 1) / kInFlight * wide;
-    const int threads = want <= 128 ? 128 : want <= 256 ? 256 : want <= 512 ? 512 : kSumThreads;
-    if (wide == 64)
-      hipLaunchKernelGGL((norm_sum_kernel<T, Cap, 64>), dim3(unsigned(at)), dim3(unsigned(threads)), 0, s, a);
+    const dim3 grid{unsigned(g.blocks)}, block{unsigned(g.threads)};
+    if (g.tile == 64)
+      hipLaunchKernelGGL((norm_sum_kernel<T, Cap, 64>), grid, block, 0, s, a);
     else
-      hipLaunchKernelGGL((norm_sum_kernel<T, Cap, 16>), dim3(unsigned(at)), dim3(unsigned(threads)), 0, s, a);
+      hipLaunchKernelGGL((norm_sum_kernel<T, Cap, 16>), grid, block, 0, s, a);
   }
   return hipGetLastError();
 }
