@@ -12,6 +12,7 @@ constexpr int kCapSmall = 8;      // terms of the plans that most launches are m
 constexpr int kWideSlices = 32;   // partial sums of a wide stretch
 constexpr int kSumThreads = 1024; // most threads of a workgroup that joins partial sums
 constexpr int kInFlight = 16;     // of which a thread reads this many at once
+constexpr int64_t kGridThreads = (int64_t(1) << 32) - 1;   // most threads of a launch
 
 // How many lanes G hold a stretch, and in how many vectors C each: the first that has room
 // for its nv = ceil(len / V) vectors.  B is the workgroup's size.
@@ -134,6 +135,7 @@ inline Layout lay_out(int64_t rows, const NormShape& p, int elem_bytes, bool bac
       const int64_t want = std::max<int64_t>((rows + groups - 1) / groups, 1);
       int64_t most = std::max<int64_t>(total * each[k] / cost, 1);
       if (y.stream && !backward) most = std::max(most, want * elem_bytes / kTurnBytes);
+      most = std::min(most, kGridThreads / y.block / p.n_terms);
       y.n_blocks[k] = y.direct ? 1 : int(std::min(want, most));
     }
     y.n_parts[k] = y.variant[k] == kWide ? kWideSlices : y.n_blocks[k];
@@ -169,6 +171,7 @@ inline SumGrid lay_out_sums(const NormShape& p, const Layout& y) {
   // as many slices as keep every load in flight, two at least
   const int want = (most + kInFlight - 1) / kInFlight * g.tile;
   g.threads = want <= 128 ? 128 : want <= 256 ? 256 : want <= 512 ? 512 : kSumThreads;
+  while (int64_t(g.blocks) * g.threads > kGridThreads) g.threads /= 2;   // 2^24 tiles at most: 128 fit
   return g;
 }
 
