@@ -113,19 +113,26 @@ def _backward(call, size, plan, grad_out, x, stats, weight, need, workspace):
     gx = torch.empty_like(x, memory_format=torch.contiguous_format) if "x" in need else None
     gw = x.new_empty(nw, dtype=wt) if "weight" in need else None
     gb = x.new_empty(nb, dtype=wt) if "bias" in need else None
-    if workspace is not None:
-        _on(workspace, "workspace", dev)
-    elif gw is not None or gb is not None:
+    if workspace is None and (gw is not None or gb is not None):
         need_bytes = size(x.shape[0])
         workspace = x.new_empty(need_bytes, dtype=torch.uint8) if need_bytes else None
     check(call(*head, grad_out.data_ptr(), ld_g, x.data_ptr(), ld, stats.data_ptr(), ELEM[wt], w, _at(gx), x.shape[1],
-               _at(gw), _at(gb), _at(workspace),
-               0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev)))
+               _at(gw), _at(gb), *_room(workspace, dev), _raw_stream(dev)))
     return gx, gw, gb
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
+
+
+def _room(workspace, dev):
+    """Checks a workspace (may be None); its address and bytes."""
+    if workspace is None:
+        return None, 0
+    _on(workspace, "workspace", dev)
+    if not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous, got strides {workspace.stride()}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None):
@@ -385,11 +392,8 @@ def grad_norm(params: ParamSet, grads, max_norm: float = float("inf"), grad_scal
     finite.  Asynchronous on the current stream; bitwise reproducible."""
     g = _laid(params, grads, "grads")
     out = torch.empty(2, dtype=torch.float32, device=params.device)
-    if workspace is not None:
-        _on(workspace, "workspace", params.index)
-    elif params.grad_norm_workspace_size:
+    if workspace is None and params.grad_norm_workspace_size:
         workspace = torch.empty(params.grad_norm_workspace_size, dtype=torch.uint8, device=params.device)
     check(load().cgtp_grad_norm(params.handle, g.type, g.array, _scale(params, grad_scale), max_norm, out.data_ptr(),
-                                _at(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                _raw_stream(params.index)))
+                                *_room(workspace, params.index), _raw_stream(params.index)))
     return out

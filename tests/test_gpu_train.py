@@ -737,3 +737,21 @@ def test_optimiser_argument_checks(dev):
         with pytest.raises(TypeError):
             f()
     assert all((t == 0).all() for t in (*p, *st))
+
+
+def test_workspaces_are_contiguous(dev):
+    # an expanded or strided tensor has more elements than the memory that follows its address
+    x = torch.zeros(1000, 8, device=dev)
+    _, st = C.layer_norm_forward(x)
+    p, s = C.NormPlan("8x0e"), C.ParamSet([100000])
+    _, sti = C.irreps_norm_forward(p, x)
+    one = torch.empty(1, dtype=torch.uint8, device=dev)
+    for ws in (one.expand(1 << 20), torch.empty(1 << 20, 2, dtype=torch.uint8, device=dev)[:, 0]):
+        for f in (lambda: C.layer_norm_backward(x, x, st, workspace=ws),
+                  lambda: C.irreps_norm_backward(p, x, x, sti, workspace=ws),
+                  lambda: C.grad_norm(s, [torch.zeros(100000, device=dev)], workspace=ws)):
+            with pytest.raises(ValueError):
+                f()
+    for f in (lambda: C.layer_norm_backward(x, x, st, workspace=one.cpu()), lambda: C.layer_norm_backward(x, x, st, workspace=7)):
+        with pytest.raises(TypeError):
+            f()
