@@ -755,3 +755,36 @@ def test_workspaces_are_contiguous(dev):
     for f in (lambda: C.layer_norm_backward(x, x, st, workspace=one.cpu()), lambda: C.layer_norm_backward(x, x, st, workspace=7)):
         with pytest.raises(TypeError):
             f()
+
+
+def test_layouts_keep_their_memory_and_notice_other_tensors_memory(dev):
+    # laid out once, then tensors are given other memory: a call neither reads nor writes memory
+    # that was freed, and where all have moved it is refused
+    s = C.ParamSet([300, 70, 1])
+
+    def fresh():
+        p, g = ([torch.ones(n, device=dev) for n in s.sizes] for _ in range(2))
+        return p, g, C.adamw_state(s), s.pointers(p), s.pointers(g)
+
+    changes = (lambda t: setattr(t, "data", torch.ones(t.shape, device=dev)), lambda t: t.set_(torch.ones(t.shape, device=dev)))
+    for change in changes:
+        for which in ((0,), (2,), (0, 1, 2)):
+            p, g, state, laid, grads = fresh()
+            for k in which:
+                change(p[k])
+                change(g[k])
+            for f in (lambda: C.adamw_step(s, laid, g, state, lr=1e-2, step=1), lambda: C.grad_norm(s, grads),
+                      lambda: C.adamw_step(s, p, grads, state, lr=1e-2, step=1)):
+                with pytest.raises(ValueError, match="other memory"):
+                    f()
+            assert all((t == 1).all() for t in p) and all((t == 0).all() for t in state)
+            C.adamw_step(s, s.pointers(p), s.pointers(g), state, lr=1e-2, step=1)
+            assert all((t < 1).all() for t in p)
+        # one between them: the layout goes on with the memory that it keeps
+        p, g, state, laid, grads = fresh()
+        at = p[1].data_ptr()
+        change(p[1])
+        others = [torch.full((70,), 5.0, device=dev) for _ in range(50)]   # would reuse freed memory
+        assert at not in [t.data_ptr() for t in others]
+        C.adamw_step(s, laid, grads, state, lr=1e-2, step=1)
+        assert (p[1] == 1).all() and all((t == 5).all() for t in others) and (p[0] < 1).all()
