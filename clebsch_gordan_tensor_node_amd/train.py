@@ -30,7 +30,13 @@ __all__ = ["layer_norm_forward", "layer_norm_backward", "NormPlan", "irreps_norm
            "ParamSet", "adamw_state", "adamw_step", "adamw_moments", "grad_norm"]
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() makes an object: 3 us a call
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# current_stream() makes an object, 3 us a call.  A torch without devices lacks the other name
+# and calls neither.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _on(t, name, dev):

@@ -1,6 +1,9 @@
 """CPU checks of the training operators' entry points: plan and set bookkeeping and every
 refusal that happens on the host before a launch.  No device work is done here."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -142,3 +145,18 @@ def test_python_refuses_host_tensors():
         s.pointers([x, x])
     with pytest.raises(ValueError):
         C.adamw_state(s, bits=16)
+
+
+def test_import_without_device_support():
+    # a torch built without devices has no raw stream: the package imports, host-only plans work
+    code = """
+import torch
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    del torch._C._cuda_getCurrentRawStream
+import clebsch_gordan_tensor_node_amd as C
+assert C.NormPlan("8x0e+2x1o").n_features == 14 and C.ParamSet([5], host_only=True).state_elems == 64
+assert callable(C.train._raw_stream)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
