@@ -3,7 +3,9 @@ its equivariant form over irreps, and the AdamW step over many tensors with 32-b
 8-bit moments and a gradient norm.
 
 Argument marshalling over libcgtp.so as in the package's other calls: device tensors in,
-the HIP kernels on the caller's current torch stream, no fallback.  The formulas stand in
+the HIP kernels on the caller's current torch stream, no fallback.  Like conv_forward they
+stand outside autograd: results carry no history.  examples/train_potential.py wraps them in
+torch.autograd.Function; there are no second derivatives.  The formulas stand in
 include/cgtp.h beside each entry point.
 
     y, stats = layer_norm_forward(hidden, gamma, beta)

@@ -6,7 +6,9 @@ a network around the convolution takes, on synthetic energies.
 Every edge's convolution weights come from a radial network (layer norm inside), the
 convolution's output is normalised term by term (irreps norm), its scalars give the
 energy, and the gradients pass back through the same operators into AdamW, clipped by
-their norm on the device.  Dense products and pointwise functions are torch's.
+their norm on the device.  Dense products and pointwise functions are torch's.  The
+operators have first derivatives only: a second one (create_graph=True, forces in the loss)
+raises.
 """
 import argparse
 import math
@@ -24,6 +26,19 @@ import clebsch_gordan_tensor_node_amd as C  # noqa: E402
 import workloads as WL  # noqa: E402
 
 
+class Derivative(torch.autograd.Function):
+    """Gradients call(*tensors) that depend on the tensors and cannot be differentiated: a
+    second derivative that passes through them raises, and no part of it is lost."""
+
+    @staticmethod
+    def forward(ctx, call, *tensors):
+        return call(*tensors)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the library's operators have no second derivative")
+
+
 class LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias):
@@ -34,7 +49,7 @@ class LayerNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         x, stats, weight = ctx.saved_tensors
-        return C.layer_norm_backward(grad.contiguous(), x, stats, weight)
+        return Derivative.apply(lambda g, x, w: C.layer_norm_backward(g, x, stats, w), grad.contiguous(), x, weight)
 
 
 class IrrepsNorm(torch.autograd.Function):
@@ -48,7 +63,8 @@ class IrrepsNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         x, stats, weight = ctx.saved_tensors
-        return (None, *C.irreps_norm_backward(ctx.plan, grad.contiguous(), x, stats, weight))
+        return (None, *Derivative.apply(lambda g, x, w: C.irreps_norm_backward(ctx.plan, g, x, stats, w),
+                                        grad.contiguous(), x, weight))
 
 
 class Conv(torch.autograd.Function):
@@ -61,8 +77,8 @@ class Conv(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         x, w = ctx.saved_tensors
-        gx, gw, _ = C.conv_backward(ctx.plan, *ctx.graph, x, w, grad.contiguous(), need=("x", "w"))
-        return None, None, gx, gw
+        return (None, None, *Derivative.apply(lambda g, x, w: C.conv_backward(ctx.plan, *ctx.graph, x, w, g,
+                                                                              need=("x", "w"))[:2], grad.contiguous(), x, w))
 
 
 class Potential:
