@@ -148,7 +148,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None):
     1/sqrt(variance + eps), fp32) for the backward.
 
     x is fp32, bf16 or fp16 with dense rows any stride apart; weight and bias [width] are
-    fp32 or x's type (None: 1, 0).  Asynchronous on the current stream."""
+    fp32 or x's type (None: 1, 0).  out: rows for y, any stride apart; x itself for a call in
+    place, otherwise apart from x.  Asynchronous on the current stream."""
     return _forward(load().cgtp_layer_norm_forward, None, x, weight, bias, eps, out)
 
 

@@ -281,11 +281,12 @@ enum { CGTP_F32 = 0, CGTP_BF16 = 1, CGTP_F16 = 2 };
  *   mu = sum(x)/width, s2 = sum((x - mu)^2)/width, rstd = 1/sqrt(s2 + eps),
  *   y = (x - mu) rstd weight + bias
  * x and y are device arrays of type dtype whose rows lie ld_x / ld_y elements apart (>=
- * width) and hold consecutive elements; they need the alignment of one element only and
- * may not overlap.  weight and bias [width] (each may be NULL: 1, 0) are of type
- * weight_dtype, CGTP_F32 or dtype.  stats [2, n_rows] fp32 (may be NULL) receives mu and
- * rstd, which the backward reads.  n_rows may be 0; a row of one element gives y = bias.
- * Asynchronous on `stream`; bitwise reproducible. */
+ * width) and hold consecutive elements; they need the alignment of one element only.  y may
+ * be x itself (ld_y = ld_x): every row is read before it is written, but the backward has no
+ * x then.  Rows may not overlap otherwise.  weight and bias [width] (each may be NULL: 1,
+ * 0) are of type weight_dtype, CGTP_F32 or dtype.  stats [2, n_rows] fp32 (may be NULL)
+ * receives mu and rstd, which the backward reads.  n_rows may be 0; a row of one element
+ * gives y = bias.  Asynchronous on `stream`; bitwise reproducible. */
 int cgtp_layer_norm_forward(int dtype, int64_t n_rows, int64_t width, const void* x, int64_t ld_x, int weight_dtype,
                             const void* weight, const void* bias, double eps, void* y, int64_t ld_y, float* stats,
                             void* stream);
@@ -299,8 +300,8 @@ int cgtp_layer_norm_backward_workspace_size(int64_t n_rows, int64_t width, size_
  * weight:
  *   grad_x = rstd (a - sum(a)/width - h sum(a h)/width)        rows ld_gx elements apart
  *   grad_weight[c] = sum over rows of grad_out h, grad_bias[c] = sum over rows of grad_out
- * Each output may be NULL to skip it, and is overwritten; grad_weight and grad_bias are of
- * type weight_dtype (with n_rows = 0 they are 0).  workspace: 256-byte aligned, not needed
+ * Each output may be NULL to skip it, and is overwritten; it may not overlap an input.
+ * grad_weight and grad_bias are of type weight_dtype (with n_rows = 0 they are 0).  workspace: 256-byte aligned, not needed
  * (NULL) when both are NULL.  No atomics: bitwise reproducible. */
 int cgtp_layer_norm_backward(int dtype, int64_t n_rows, int64_t width, const void* grad_out, int64_t ld_g,
                              const void* x, int64_t ld_x, const float* stats, int weight_dtype, const void* weight,

@@ -165,6 +165,23 @@ def test_norm_strides(spec, pad, first, dev):
         assert (wide[:, :first] == 7).all() and (wide[:, first + f:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("spec,rows", [(3, 500), (7, 500), (100, 500), (481, 300), (700, 300), (1312, 300), (2049, 100), (5000, 50),
+                                       (12001, 40), (16384, 40), (30001, 40), ("5x0e+3x0o+7x4e+2x0e", 500), (700, 140000),
+                                       ("20000x0e+3x1o+7000x1o+600x0e", 30), ("128x0e+64x1o+32x2e+32x3o", 70000)], ids=str)
+def test_norm_in_place(spec, rows, dtype, dev):
+    # y in x's place, in every layout, within and past the cache: bit for bit what it is elsewhere
+    terms, f, nw, nb = _shape(spec)
+    gen = torch.Generator(device=dev).manual_seed(4)
+    wide = torch.randn(rows, f + 3, device=dev, generator=gen).to(dtype)
+    x, before = wide[:, 1:f + 1], wide.clone()
+    w, b = torch.randn(nw, device=dev, generator=gen), torch.randn(nb, device=dev, generator=gen)
+    y, st = _call(spec, x, w, b)
+    got, st2 = _call(spec, x, w, b, out=x)
+    assert got.data_ptr() == x.data_ptr() and torch.equal(x, y) and torch.equal(st, st2)
+    assert torch.equal(wide[:, 0], before[:, 0]) and torch.equal(wide[:, f + 1:], before[:, f + 1:])
+
+
 def test_norm_optional_arguments(dev):
     for spec in (65, "5x0e+3x1o"):
         rng = np.random.default_rng(1)
