@@ -339,7 +339,8 @@ int cgtp_irreps_norm_backward(cgtp_norm_t plan, int dtype, int64_t n_rows, const
  * small table on the current device, and no pointer to them.  Optimiser states of the whole
  * set are flat arrays of state_elems elements: tensor t's begin at offsets[t], a multiple
  * of 64.  flags: 0, or CGTP_PLAN_HOST_ONLY (sizes only, no device).  May be shared by
- * threads and streams; freed by cgtp_params_destroy (NULL is ignored). */
+ * threads and streams; freed by cgtp_params_destroy (NULL is ignored), but not before
+ * captured graphs that hold its calls. */
 typedef struct cgtp_params_s* cgtp_params_t;
 int cgtp_params_create(const int64_t* numel, const double* weight_decay, int n_tensors, unsigned flags,
                        cgtp_params_t* out);
@@ -353,6 +354,9 @@ void cgtp_params_destroy(cgtp_params_t set);
  *   g = grad grad_scale[0];  p <- p (1 - lr decay);  m <- beta1 m + (1 - beta1) g;
  *   v <- beta2 v + (1 - beta2) g^2;
  *   p <- p - (lr / (1 - beta1^step)) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * 16-bit parameters are rounded to nearest: a step below half the distance of their values
+ * (2^-9 to 2^-8 of a bf16 parameter) leaves them as they are, step after step.  At such rates
+ * hold the parameters in fp32 and copy them to 16 bits for the network.
  * grad_scale (device fp32, NULL = 1): the inverse of a loss scale, or the factor that
  * cgtp_grad_norm writes; where it is NaN the whole step is skipped, params and states
  * untouched.  Asynchronous on `stream`; bitwise reproducible.  lr and step travel in the
