@@ -151,6 +151,60 @@ def test_norm_rows_that_outgrow_the_cache(spec, rows, dev):
     assert (gw - sw).abs().max() < bound and (gb - sb).abs().max() < bound
 
 
+def _small_integers(shape, dtype, dev, gen):
+    return torch.randint(-3, 4, shape, device=dev, generator=gen).to(dtype)
+
+
+@pytest.mark.parametrize("spec", [33, 700, 1000, 3000, 5000, 12000, "128x0e+64x1o+32x2e+32x3o"], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_norm_past_the_cache_in_every_type(dtype, spec, dev):
+    # calls that move more than 256 MB, forward and backward: rows bit for bit as in smaller
+    # calls; of small integers with mean 0 and rstd 1 (h = x) the sums of the weight's and bias's
+    # gradients are whole numbers below 2^24, so that a row too few or too many shows
+    terms, f, nw, nb = _shape(spec)
+    rows = (1 << 28) // (2 * f * torch.finfo(dtype).bits // 8) + 77
+    gen = torch.Generator(device=dev).manual_seed(1)
+    x = torch.randn(rows, f, device=dev, generator=gen).to(dtype)
+    w, b = torch.randn(nw, device=dev, generator=gen), torch.randn(nb, device=dev, generator=gen)
+    y, st = _call(spec, x, w, b)
+    part = (rows + 3) // 4
+    for r in range(0, rows, part):
+        yr, sr = _call(spec, x[r:r + part], w, b)
+        assert torch.equal(y[r:r + part], yr) and torch.equal(st[:, r:r + part], sr)
+    del y
+    x, g = _small_integers((rows, f), dtype, dev, gen), _small_integers((rows, f), dtype, dev, gen)
+    st = torch.stack([torch.zeros(rows, len(terms), device=dev), torch.ones(rows, len(terms), device=dev)])
+    gx, gw, gb = _grads(spec, g, x, st, w)
+    for r in range(0, rows, part):
+        gxr, _, _ = _grads(spec, g[r:r + part], x[r:r + part], st[:, r:r + part].contiguous(), w)
+        assert torch.equal(gx[r:r + part], gxr)
+    _check_whole_sums(terms, g, x, gw, gb)
+
+
+def _check_whole_sums(terms, g, x, gw, gb):
+    for off, m, d, w0, b0 in terms:
+        q, h = g[:, off:off + m * d].float(), x[:, off:off + m * d].float()
+        want = (q * h).sum(0, dtype=torch.float64).view(m, d).sum(1)
+        assert torch.equal(gw[w0:w0 + m].double(), want)
+        if b0 is not None:
+            assert torch.equal(gb[b0:b0 + m].double(), q.sum(0, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("spec", ["5x0e+3x0o+7x4e+2x0e+9x1o+33x0e+8x2e+1x0o+64x0e", "+".join(["3x0e+1x1o"] * 32), 600, 1000, 1024,
+                                  "1x0e+700x0e+100x1o"], ids=lambda s: str(s)[:30])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_partial_sums_of_many_rows(dtype, spec, dev):
+    # more than 8 terms, and 16 elements a lane: several workgroups per term and the second launch
+    _check(spec, 4000, dtype, torch.float32, dev)
+    terms, f, nw, nb = _shape(spec)
+    gen = torch.Generator(device=dev).manual_seed(2)
+    for rows in (200, 9001):
+        x, g = _small_integers((rows, f), dtype, dev, gen), _small_integers((rows, f), dtype, dev, gen)
+        st = torch.stack([torch.zeros(rows, len(terms), device=dev), torch.ones(rows, len(terms), device=dev)])
+        _, gw, gb = _grads(spec, g, x, st, torch.ones(nw, device=dev))
+        _check_whole_sums(terms, g, x, gw, gb)
+
+
 @pytest.mark.parametrize("pad,first", [(1, 0), (1, 1), (7, 3), (64, 32)])
 @pytest.mark.parametrize("spec", [64, 65, 1312, "128x0e+64x1o+32x2e+32x3o"], ids=str)
 def test_norm_strides(spec, pad, first, dev):
@@ -632,6 +686,30 @@ def test_adamw_set_that_outgrows_the_cache(bits, dev):
             code, exp = T.encode(values, u, signed)
             assert np.array_equal(c[at:at + n].cpu().numpy(), code)
             assert np.array_equal(e[at // 64:(at + n) // 64].cpu().numpy(), exp)
+
+
+@pytest.mark.parametrize("pt,gt", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32), (torch.float32, torch.float16)])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_past_the_cache_in_16_bits(bits, pt, gt, dev):
+    # as above, 16-bit parameters and gradients: parameters as in sets of their own, and the states
+    # of the first tensor, whose places are the same there
+    sizes = [30000001, 7, 9000000] if bits == 8 else [12000001, 7, 4000000]
+    gen = torch.Generator(device=dev).manual_seed(0)
+    p = [torch.randn(n, device=dev, generator=gen).to(pt) for n in sizes]
+    g = [torch.randn(n, device=dev, generator=gen).to(gt) for n in sizes]
+    start, s = [t.clone() for t in p], C.ParamSet(sizes, 0.1)
+    state = C.adamw_state(s, bits)
+    C.adamw_step(s, p, g, state, lr=1e-2, step=1, seed=9)
+    for k, n in enumerate(sizes):
+        for from_, to in ((0, n // 3), (n // 3, n)):   # in pieces that stay in the cache
+            one, alone = C.ParamSet([to - from_], 0.1), [start[k][from_:to].clone()]
+            st = C.adamw_state(one, bits)
+            C.adamw_step(one, alone, [g[k][from_:to].clone()], st, lr=1e-2, step=1, seed=9)
+            assert torch.equal(alone[0], p[k][from_:to])
+            if k == 0 and from_ == 0:
+                m = (to - from_) // 64 * 64
+                assert all(torch.equal(a[:m], c[:m]) for a, c in zip(state[:2], st[:2]))
+                assert all(torch.equal(a[:m // 64], c[:m // 64]) for a, c in zip(state[2:], st[2:]))
 
 
 @pytest.mark.parametrize("bits", [32, 8])
