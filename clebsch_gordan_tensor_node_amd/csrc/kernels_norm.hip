@@ -552,9 +552,6 @@ __device__ inline int term_of(const NormArgs<Cap>& a) {
         if (t.variant == kG64C2) FN<B, Stream, T, V, 64, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
         if (t.variant == kGBC2) FN<B, Stream, T, V, B, 2>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
       }                                                                                                 \
-      if constexpr (E >= 3 * V) {                                                                       \
-        if (t.variant == kGBC3) FN<B, Stream, T, V, B, 3>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
-      }                                                                                                 \
       if constexpr (E >= 4 * V) {                                                                       \
         if (t.variant == kG64C4) FN<B, Stream, T, V, 64, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__); \
         if (t.variant == kGBC4) FN<B, Stream, T, V, B, 4>(a.c, t, a.n_terms, k, block, lds, ##__VA_ARGS__);   \
@@ -690,10 +687,6 @@ void forward(const NormArgs<Cap>& a, int blocks, const Layout& y, hipStream_t s)
   const dim3 grid{unsigned(blocks)}, block{unsigned(y.block)};
   if (y.max_e > 8) {
     if constexpr (sizeof(T) == 4) {
-      if (y.block == 128) {
-        hipLaunchKernelGGL((norm_fwd_kernel<T, 128, 12, Cap, Stream>), grid, block, 0, s, a);
-        return;
-      }
       if (y.block == 512) {
         hipLaunchKernelGGL((norm_fwd_kernel<T, 512, kMaxE, Cap, Stream>), grid, block, 0, s, a);
         return;

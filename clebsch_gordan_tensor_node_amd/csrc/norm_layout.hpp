@@ -27,7 +27,6 @@ enum Variant : int {
   kG64C4,   // nv <= 256, likewise
   kGBC1,    // nv <= B
   kGBC2,    // nv <= 2 B, likewise
-  kGBC3,    // nv <= 3 B, likewise
   kGBC4,    // nv <= 4 B, likewise
   kWide     // any: the row is read again for each sum
 };
@@ -35,14 +34,12 @@ enum Variant : int {
 // Elements per lane for a plan whose longest stretch is `longest`, as long as a workgroup's
 // lanes reach.  The more, the fewer waves fit a SIMD's registers; the fewer, the more waves
 // share a stretch and wait for one another.  With 8 and with 16, us for 400 MB: forward of
-// 4096 columns 73 and 78 (fp32), 92 and 109 (bf16), of 8192 87 and 83 (fp32), 95 and 112
-// (bf16); backward of 1024 columns 100 and 86 (fp32), 108 and 116 (bf16), of 4096 88 and 98
-// (fp32), 97 and 135 (bf16), of 8192 101 and 117 (fp32), 139 and 133 (bf16).  12 lets a
-// workgroup of 128 hold 1536 fp32 columns, where 256 leave a third of their lanes idle:
-// forward of 20060 x 1312 42 us, with 8 46; of 114688 x 1312 230 and 236.
+// 4096 columns 75 and 78 (fp32), 94 and 108 (bf16), of 4097 93 and 81 (fp32), of 6000 84 and
+// 81 (fp32), of 8192 76 and 79 (fp32), 97 and 112 (bf16); backward of 1024 columns 99 and 86
+// (fp32), 107 and 115 (bf16), of 4096 88 and 95 (fp32), 94 and 132 (bf16), of 8192 98 and 108
+// (fp32), 135 and 133 (bf16).
 inline int elems_of(int longest, int elem_bytes, bool backward) {
   if (longest > 4096) return (elem_bytes == 4) != backward ? 16 : 8;
-  if (longest > 1024 && longest <= 1536 && !backward && elem_bytes == 4) return 12;
   return longest > 512 && longest <= 1024 && backward && elem_bytes == 4 ? 16 : 8;
 }
 constexpr int kMaxE = 16;
@@ -65,7 +62,7 @@ inline int variant_of(int len, int elem_bytes, int block, int e) {
   if (nv <= 128 && e >= 2 * v) return kG64C2;
   if (nv <= 256 && e >= 4 * v) return kG64C4;
   if (nv <= block) return kGBC1;
-  return nv <= 2 * block ? kGBC2 : nv <= 3 * block && e == 12 ? kGBC3 : kGBC4;
+  return nv <= 2 * block ? kGBC2 : kGBC4;
 }
 // Lanes per stretch and vectors per lane.
 inline int lanes_of(int variant, int block) {
@@ -73,18 +70,18 @@ inline int lanes_of(int variant, int block) {
   return variant <= kG64C4 ? g[variant] : block;
 }
 inline int vectors_of(int variant) {
-  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : variant == kGBC3 ? 3 : 1;
+  return variant == kG64C2 || variant == kGBC2 ? 2 : variant == kG64C4 || variant == kGBC4 ? 4 : 1;
 }
 
 // Workgroups of a launch, shared among the terms by their cost: enough to keep the
 // memory busy, which takes more of them where every access goes to HBM, and in the
 // backward no more, since each leaves a row of partial sums.  Measured: forward of 114688 x
-// 1312 fp32 232, 222 and 219 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 38, 36
-// and 41; backward and sums of 768 x 9088 (cached) 23.3, 23.3, 25.0 and 27.8 us with 512,
-// 768, 1024 and 1536, of 32768 x 704 82, 67, 60 and 56.  Past the cache the forward takes
-// more, as long as each has 28 / element bytes turns for the weights that it loads: 114688 x
-// 1312 fp32 in 8192 workgroups of 128 228 us, in 16384 219, but 30000 x 1400 70 and 78; 24414
-// x 4096 bf16 with 12 turns 92 us, with 7 104.
+// 1312 fp32 217, 229 and 223 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 48, 37 and
+// 40, of 300000 x 64 (cached) 31, 32 and 32; backward and sums of 768 x 9088 (cached) 23.3,
+// 23.3, 25.0 and 27.8 us with 512, 768, 1024 and 1536, of 32768 x 704 82, 67, 60 and 56.  Past
+// the cache the forward takes more, as long as each has 28 / element bytes turns for the
+// weights that it loads: without, with 28 and with 14, 114688 x 1312 fp32 223, 212 and 209 us,
+// 100000 x 704 113, 107 and 107; 24414 x 4096 bf16 94, 94 and 105.
 constexpr int kTurnBytes = 28;
 constexpr int kForwardBlocks = 2048, kForwardBlocksStream = 4096;
 constexpr int kBackwardBlocks = 768, kBackwardBlocksStream = 1536;

@@ -1,6 +1,7 @@
 // Prints the launches that the normalisations' layout asks for, one line per call read
 // from standard input:  rows elem_bytes backward n_terms (len d centred)...
-//   -> threads of a workgroup, workgroups, threads and workgroups of the partial sums
+//   -> threads of a workgroup, workgroups, threads and workgroups of the partial sums, most
+//      elements of a lane
 #include <cstdio>
 #include <vector>
 
@@ -26,7 +27,7 @@ int main() {
     long long blocks = 0;
     for (int k = 0; k < n; ++k) blocks += y.n_blocks[k];
     const SumGrid g = lay_out_sums(p, y);
-    std::printf("%d %lld %d %d\n", y.block, blocks, g.threads, g.blocks);
+    std::printf("%d %lld %d %d %d\n", y.block, blocks, g.threads, g.blocks, y.max_e);
   }
   return 0;
 }
