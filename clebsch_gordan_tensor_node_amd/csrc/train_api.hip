@@ -334,13 +334,12 @@ int check_tensors(cgtp_params_t P, int dtype, const void* const* t, const char* 
 }
 
 // Calls launch(first tensor, tensors, first chunk, chunks) for ranges of tensors whose
-// pointers fit one launch's kernel arguments, from the last range to the first if `back`.
+// pointers fit one launch's kernel arguments.
 template <typename F>
-int for_launches(cgtp_params_t P, bool back, F&& launch) {
-  const int n = int(P->numel.size()), ranges = (n + kTensorsPerLaunch - 1) / kTensorsPerLaunch;
-  for (int r = 0; r < ranges; ++r) {
-    const int t = (back ? ranges - 1 - r : r) * kTensorsPerLaunch, to = std::min(n, t + kTensorsPerLaunch);
-    const int c0 = P->first_chunk[t], c1 = P->first_chunk[to];
+int for_launches(cgtp_params_t P, F&& launch) {
+  const int n = int(P->numel.size());
+  for (int t = 0; t < n; t += kTensorsPerLaunch) {
+    const int to = std::min(n, t + kTensorsPerLaunch), c0 = P->first_chunk[t], c1 = P->first_chunk[to];
     if (c1 > c0) CGTP_HIP(launch(t, to - t, c0, c1 - c0));
   }
   return ok();
@@ -398,15 +397,14 @@ int adamw_step(cgtp_params_t P, int param_dtype, void* const* params, int grad_d
   a.eps = float(eps);
   const int64_t each = 2 * elem_size(param_dtype) + elem_size(grad_dtype) + (bits8 ? 4 : 16);
   const bool stream_by = P->state_elems * each > kCacheBytes;
-  return for_launches(P, true, [&](int t, int n, int c0, int chunks) {
+  return for_launches(P, [&](int t, int n, int c0, int chunks) {
     a.first_tensor = t;
     std::memcpy(a.param, params + t, size_t(n) * sizeof(void*));
     std::memcpy(a.grad, grads + t, size_t(n) * sizeof(void*));
-    for (int end = chunks; end > 0; end -= kChunksPerLaunch) {
-      const int from = std::max(end - kChunksPerLaunch, 0);
+    for (int from = 0; from < chunks; from += kChunksPerLaunch) {
       a.chunks = P->d_chunks + c0 + from;
-      const hipError_t e = launch_adamw(a, end - from, Elem(param_dtype), Elem(grad_dtype), bits8, stream_by,
-                                        static_cast<hipStream_t>(stream));
+      const hipError_t e = launch_adamw(a, std::min(chunks - from, kChunksPerLaunch), Elem(param_dtype),
+                                        Elem(grad_dtype), bits8, stream_by, static_cast<hipStream_t>(stream));
       if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -498,7 +496,7 @@ int cgtp_grad_norm(cgtp_params_t P, int grad_dtype, const void* const* grads, co
                                     static_cast<hipStream_t>(stream)));
     return ok();
   }
-  int rc = for_launches(P, false, [&](int t, int n, int c0, int count) {
+  int rc = for_launches(P, [&](int t, int n, int c0, int count) {
     a.chunks = P->d_chunks + c0;
     a.part = part;
     part += square_blocks(count);
