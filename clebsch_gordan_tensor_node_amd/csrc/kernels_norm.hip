@@ -169,8 +169,8 @@ __device__ inline void shift(float (&x)[C][V], float by) {
 // Where a lane's vectors of a stretch lie.
 template <int V, int G, int C>
 struct Place {
-  int lane, len, last;   // last: the chunk that holds the stretch's end (the same in all lanes)
-  __device__ Place(int n) : lane(threadIdx.x % G), len(n), last((n - 1) / (V * G)) {}
+  int lane, len, last;   // last: the chunk that holds the stretch's end (the same in all lanes; 0 of one)
+  __device__ Place(int n) : lane(threadIdx.x % G), len(n), last(C == 1 ? 0 : (n - 1) / (V * G)) {}
   __device__ int start(int c) const { return (c * G + lane) * V; }
   __device__ bool has(int c) const { return c < last || (c == last && start(c) < len); }
   __device__ int at(int c) const { return min(start(c), len - V); }   // first element of the vector
