@@ -20,8 +20,8 @@
 // it repeats are left out of the sums, and written twice with the same value.
 // A workgroup keeps its weights over all its rows (first its own number, then in strides).
 // Measured, with 4.75 TB/s for a large device copy: forward of 114688 x 1312 fp32 212 us
-// (5.7 TB/s), of 4096 x 5472 in four terms 38 us (4.7); backward with all gradients of 32768
-// x 704 in four terms 55 us (5.1), of 114688 x 128 bf16 22 + 5 us for the sums of the
+// (5.7 TB/s), of 4096 x 5472 in four terms 37 us (4.8); backward with all gradients of 32768
+// x 704 in four terms 54 us (5.1), of 114688 x 128 bf16 22 + 5 us for the sums of the
 // weight's gradient, which wait for the memory's latency (as do rows of a few lanes).
 #include "elem.hpp"
 #include "norm_layout.hpp"
@@ -169,8 +169,10 @@ __device__ inline void shift(float (&x)[C][V], float by) {
 // Where a lane's vectors of a stretch lie.
 template <int V, int G, int C>
 struct Place {
-  int lane, len, last;   // last: the chunk that holds the stretch's end (the same in all lanes; 0 of one)
-  __device__ Place(int n) : lane(threadIdx.x % G), len(n), last(C == 1 ? 0 : (n - 1) / (V * G)) {}
+  int lane, len, last;   // last: the chunk that holds the stretch's end (the same in all lanes)
+  // first: that chunk is known to be the first.  With C = 1 it always is; the backward, which
+  // waits for its loads where it tests it, is slower if told so (32768 x 704 fp32 55.5 us, 54.4).
+  __device__ Place(int n, bool first) : lane(threadIdx.x % G), len(n), last(first ? 0 : (n - 1) / (V * G)) {}
   __device__ int start(int c) const { return (c * G + lane) * V; }
   __device__ bool has(int c) const { return c < last || (c == last && start(c) < len); }
   __device__ int at(int c) const { return min(start(c), len - V); }   // first element of the vector
@@ -267,7 +269,7 @@ __device__ inline void load_weights(const Place<V, G, C>& p, const void* w, int 
 template <int B, bool Stream, typename T, int V, int G, int C>
 __device__ inline void fwd_rows(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds) {
   constexpr int kGroups = B / G;
-  const Place<V, G, C> p(t.len);
+  const Place<V, G, C> p(t.len, C == 1);
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
   float w[C][V], b[C][V], x[C][V];
@@ -309,7 +311,7 @@ template <int B, bool Stream, typename T, int V, int G, int C>
 __device__ inline void bwd_rows(const NormCall& a, const TermArgs& t, int n_terms, int index, int block, float* lds,
                                 float* sums, bool direct) {
   constexpr int kGroups = B / G;
-  const Place<V, G, C> p(t.len);
+  const Place<V, G, C> p(t.len, false);
   const bool centred = t.b_off >= 0;
   const float inv = 1.0f / float(t.len);
   float x[C][V], g[C][V], gw[C][V], gb[C][V];

@@ -257,7 +257,7 @@ __device__ inline void adamw_chunk(const AdamwArgs& a, const AdamwScalars& h, co
 
 // Bound by HBM with 32-bit states: 49.8 M elements, 28 bytes each, 201 us (6.9 TB/s of
 // algorithmic bytes, a part of the gradients still cached from their norm).  With 8-bit
-// states 37.3 M elements of 16 bytes take 106 us (5.6 TB/s) and some 85 operations each, two
+// states 37.3 M elements of 16 bytes take 109 us (5.5 TB/s) and some 85 operations each, two
 // thirds of the time that the bytes need at that rate: every operation added here costs.
 template <typename P, typename G, bool Bits8, bool Stream>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(kFinish) void grad_norm_kernel(const double* part, 
 }
 
 // Small sets, in one workgroup and launch: two chunks to each wave, read together.  24
-// tensors of 8192 elements at most 5.5 us, and a launch less for the host (3.7 us) than the
+// tensors of 8192 elements at most 5.6 us, and a launch less for the host (3.7 us) than the
 // two kernels' 3.1 + 2.0 us.
 template <typename G>
 __global__ __launch_bounds__(kFinish) void grad_norm_small_kernel(GradNormArgs a, const float* grad_scale,

@@ -14,8 +14,8 @@ enum class Elem : int { f32 = 0, bf16 = 1, f16 = 2 };
 // What the last-level cache holds.  A call that moves more has nothing of it left in the
 // caches when it ends: its accesses pass them by (non-temporal), which keeps the lines that
 // it writes from being written back during the next kernel.  Measured without and with: a
-// clipped AdamW step of 1.4 GB 302 and 245 us, layer norm of 1.2 GB 232 and 218 us; but a
-// backward of 84 MB, whose rows the caches hold, 27 and 33 us.
+// clipped AdamW step of 1.4 GB 305 and 240 us, layer norm of 1.2 GB 240 and 212 us; but a
+// backward of 84 MB, whose rows the caches hold, 23 and 31 us.
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
 
 // ---- normalisation -----------------------------------------------------------------
@@ -63,9 +63,8 @@ hipError_t launch_norm_backward(const NormCall& c, const NormShape& p, Elem type
 // ---- optimiser ---------------------------------------------------------------------
 
 constexpr int kStateBlock = 64;          // elements that share an exponent in 8-bit states
-// Most elements of one chunk.  A step of 50 M elements with 32-bit states took 207, 204 and
-// 210 us with 4096, 2048 and 1024, one of 37 M with 8-bit states 112, 106 and 103 us, the
-// gradient norm's first pass over 50 M 34, 34 and 52 us.
+// Most elements of one chunk.  A clipped step of 50 M elements with 32-bit states takes 241,
+// 238 and 244 us with 4096, 2048 and 1024, one of 37 M with 8-bit states 118, 116 and 120 us.
 constexpr int kChunk = 2048;
 constexpr int kTensorsPerLaunch = 232;   // tensors whose pointers fit the kernel arguments
 constexpr int kChunksPerLaunch = 1 << 22;   // a grid's threads stay below 2^32

@@ -76,11 +76,11 @@ inline int vectors_of(int variant) {
 // Workgroups of a launch, shared among the terms by their cost: enough to keep the
 // memory busy, which takes more of them where every access goes to HBM, and in the
 // backward no more, since each leaves a row of partial sums.  Measured: forward of 114688 x
-// 1312 fp32 217, 229 and 223 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 48, 37 and
-// 40, of 300000 x 64 (cached) 31, 32 and 32; backward and sums of 768 x 9088 (cached) 23.3,
+// 1312 fp32 231, 230 and 224 us with 1024, 2048 and 4096, of 4096 x 5472 (cached) 47, 37 and
+// 40, of 300000 x 64 (cached) 31, 32 and 31; backward and sums of 768 x 9088 (cached) 23.3,
 // 23.3, 25.0 and 27.8 us with 512, 768, 1024 and 1536, of 32768 x 704 82, 67, 60 and 56.  Past
 // the cache the forward takes more, as long as each has 28 / element bytes turns for the
-// weights that it loads: without, with 28 and with 14, 114688 x 1312 fp32 223, 212 and 209 us,
+// weights that it loads: without, with 28 and with 14, 114688 x 1312 fp32 224, 212 and 212 us,
 // 100000 x 704 113, 107 and 107; 24414 x 4096 bf16 94, 94 and 105.
 constexpr int kTurnBytes = 28;
 constexpr int kForwardBlocks = 2048, kForwardBlocksStream = 4096;
