@@ -301,8 +301,9 @@ int cgtp_layer_norm_backward_workspace_size(int64_t n_rows, int64_t width, size_
  *   grad_x = rstd (a - sum(a)/width - h sum(a h)/width)        rows ld_gx elements apart
  *   grad_weight[c] = sum over rows of grad_out h, grad_bias[c] = sum over rows of grad_out
  * Each output may be NULL to skip it, and is overwritten; it may not overlap an input.
- * grad_weight and grad_bias are of type weight_dtype (with n_rows = 0 they are 0).  workspace: 256-byte aligned, not needed
- * (NULL) when both are NULL.  No atomics: bitwise reproducible. */
+ * grad_weight and grad_bias are of type weight_dtype (with n_rows = 0 they are 0).
+ * workspace: 256-byte aligned, not needed (NULL) when both are NULL.  No atomics: bitwise
+ * reproducible. */
 int cgtp_layer_norm_backward(int dtype, int64_t n_rows, int64_t width, const void* grad_out, int64_t ld_g,
                              const void* x, int64_t ld_x, const float* stats, int weight_dtype, const void* weight,
                              void* grad_x, int64_t ld_gx, void* grad_weight, void* grad_bias, void* workspace,
