@@ -11,7 +11,8 @@ built library or a gfx950 device the calls raise.
     out = conv_forward(plan, pos, cell, row_ptr, col, shift, x, w, mask)
 
 The operators that train a network around it (layer and irreps normalisation, AdamW) are
-in train.py and exported here.
+in train.py, those of a network with several branches (group normalisation, routing, the
+gate's gradient) in branch.py; both are exported here.
 """
 from __future__ import annotations
 
@@ -22,13 +23,16 @@ import torch
 
 from . import _lib
 from ._lib import CGTP_PATHS_ALL, CGTP_PATHS_PARITY, CgtpError, check, load
+from .branch import (Route, conv_gate_backward, group_norm_backward, group_norm_forward, route_backward,
+                     route_forward)
 from .train import (NormPlan, ParamSet, adamw_moments, adamw_state, adamw_step, grad_norm, irreps_norm_backward,
                     irreps_norm_forward, layer_norm_backward, layer_norm_forward)
 
 __all__ = ["Plan", "neighbors_build", "conv_prepare", "edge_sh", "conv_forward", "conv_backward", "CgtpError",
            "CGTP_PATHS_ALL", "CGTP_PATHS_PARITY", "library_path", "version", "NormPlan", "ParamSet", "adamw_moments",
            "adamw_state", "adamw_step", "grad_norm", "irreps_norm_backward", "irreps_norm_forward",
-           "layer_norm_backward", "layer_norm_forward"]
+           "layer_norm_backward", "layer_norm_forward", "Route", "conv_gate_backward", "group_norm_backward",
+           "group_norm_forward", "route_backward", "route_forward"]
 
 
 def library_path() -> str:

@@ -25,6 +25,7 @@ CGTP_PATHS_PARITY = 1
 CGTP_PLAN_HOST_ONLY = 1
 CGTP_PLAN_FP64 = 2
 CGTP_ADAMW_SCALARS_BYTES = 24
+ACT = {None: 0, "silu": 1, "gelu": 2}   # CGTP_ACT_NONE, CGTP_ACT_SILU, CGTP_ACT_GELU
 ELEM = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # CGTP_F32, CGTP_BF16, CGTP_F16
 
 EXPORTED = [
@@ -38,6 +39,8 @@ EXPORTED = [
     "cgtp_irreps_norm_backward_workspace_size", "cgtp_irreps_norm_backward", "cgtp_params_create",
     "cgtp_params_info", "cgtp_params_destroy", "cgtp_adamw_step", "cgtp_adamw_scalars",
     "cgtp_adamw_step_8bit", "cgtp_adamw_read_8bit", "cgtp_grad_norm_workspace_size", "cgtp_grad_norm",
+    "cgtp_group_norm_workspace_size", "cgtp_group_norm_forward", "cgtp_group_norm_backward",
+    "cgtp_route_workspace_size", "cgtp_route_forward", "cgtp_route_backward", "cgtp_conv_gate_backward",
 ]
 
 
@@ -109,6 +112,15 @@ def load():
         "cgtp_adamw_read_8bit": ([P, P, P, P, P, P, P, P], I32),
         "cgtp_grad_norm_workspace_size": ([P, ctypes.POINTER(SZ)], I32),
         "cgtp_grad_norm": ([P, I32, P, P, F64, P, P, SZ, P], I32),
+        "cgtp_group_norm_workspace_size": ([I32, I32, I64, I64, I64, I64, P, I64, ctypes.POINTER(SZ)], I32),
+        "cgtp_group_norm_forward": ([I32, I64, I64, I64, I64, P, I64, P, I64, I32, P, P, I32, F64, I32, P, I64, P, P, SZ,
+                                     P], I32),
+        "cgtp_group_norm_backward": ([I32, I64, I64, I64, I64, P, I64, P, I64, P, I64, P, I32, P, P, I32, P, I64, P, P, P,
+                                      SZ, P], I32),
+        "cgtp_route_workspace_size": ([I64, I32, ctypes.POINTER(SZ)], I32),
+        "cgtp_route_forward": ([I32, I64, I32, I32, P, I64, P, I32, I32, P, P, P, P, P, P, SZ, P], I32),
+        "cgtp_route_backward": ([I32, I64, I32, I32, P, I64, I32, I32, P, P, P, P, P, I64, P], I32),
+        "cgtp_conv_gate_backward": ([I64, I64, P, P, P, P, P, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)

@@ -43,7 +43,9 @@ def _hipcc() -> str:
 def _units():
     units = [("cgtp_api.hip", [], "cgtp_api.o"), ("kernels_graph.hip", [], "kernels_graph.o"),
              ("kernels_bwd.hip", [], "kernels_bwd.o"), ("train_api.hip", [], "train_api.o"),
-             ("kernels_norm.hip", [], "kernels_norm.o"), ("kernels_optim.hip", [], "kernels_optim.o")]
+             ("kernels_norm.hip", [], "kernels_norm.o"), ("kernels_optim.hip", [], "kernels_optim.o"),
+             ("branch_api.hip", [], "branch_api.o"), ("kernels_group.hip", [], "kernels_group.o"),
+             ("kernels_route.hip", [], "kernels_route.o")]
     for c in range(N_CONV_CLASSES):
         units.append(("kernels_conv.hip", [f"-DCGTP_CONV_CLASS={c}"], f"kernels_conv_c{c}.o"))
     return units
@@ -91,7 +93,8 @@ def build(incremental: bool = False, jobs: int | None = None, verbose: bool = Tr
     t0 = time.time()
     # the slowest units (the backward's edge pass, the l >= 4 conv classes) start first
     slow = {"kernels_conv_c6.o": 0, "kernels_conv_c7.o": 1, "kernels_conv_c8.o": 2, "kernels_conv_c1.o": 3,
-            "kernels_conv_c5.o": 4, "kernels_bwd.o": 5, "kernels_conv_c4.o": 6, "kernels_norm.o": 7}
+            "kernels_conv_c5.o": 4, "kernels_bwd.o": 5, "kernels_conv_c4.o": 6, "kernels_norm.o": 7,
+            "kernels_group.o": 8, "kernels_route.o": 9}
     order = sorted(range(len(_units())), key=lambda k: slow.get(_units()[k][2], 99))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         done = dict(zip(order, ex.map(compile_one, [_units()[k] for k in order])))

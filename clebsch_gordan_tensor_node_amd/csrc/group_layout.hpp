@@ -1,0 +1,130 @@
+// How group normalisation lays rows and columns over workgroups.  Host code only, apart from
+// the constants.
+#pragma once
+
+#include <algorithm>
+
+#include "launch_branch.hpp"
+
+namespace cgtp {
+
+constexpr int kTileBlock = 256;        // threads of a tile's workgroup
+constexpr int64_t kGroupGrid = (int64_t(1) << 32) - 1;   // most threads of a launch
+
+// A chunk is the columns that a workgroup takes: whole groups, or where a group is wider than
+// a workgroup's lanes reach, a part of one.  A thread has a place of `vec` columns among its
+// chunk's `lanes` and every slices-th row.
+struct GroupLayout {
+  int whole;             // 1: a workgroup has all rows of one sample, and holds them in registers;
+                         // 0: tiles of rows, whose sums a second launch joins
+  int vec;               // columns of a place: kGroupVec, or 1 where the row has fewer
+  int block;             // threads of a workgroup
+  int held;              // whole: rows that a thread holds
+  int64_t per_chunk;     // groups of a chunk
+  int64_t split;         // parts of a group (1 unless a group is wider than a workgroup reaches)
+  int64_t part;          // columns of a part; the last of a group may have fewer
+  int64_t chunks;
+  int lanes, slices;
+  int64_t tile_rows, tiles;   // tiles only
+};
+
+// Columns of a thread's place.  Everything that a thread has per column (weights, statistics,
+// sums) is in 32 bits: of eight columns it would take the registers that 16-bit rows leave.
+constexpr int kGroupVec = 4;
+
+// Rows that a thread holds of a whole sample: 64 registers of x, or 48 of x and grad_out (64
+// of them spill in workgroups of 1024).
+constexpr int kHeldFew = 4;
+constexpr int held_most(int elem_bytes, bool backward) { return (backward ? 24 : 64) / elem_bytes; }
+
+inline void set_lanes(GroupLayout& y, int64_t columns) {
+  y.lanes = int((columns + y.vec - 1) / y.vec);
+  y.slices = y.block / y.lanes;
+}
+
+inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backward) {
+  GroupLayout y{};
+  const int64_t cg = c.width / c.groups;
+  y.vec = c.width >= kGroupVec ? kGroupVec : 1;
+  y.split = 1;
+  y.part = cg;
+  // the longest sample: as told, as equal samples have it, or eight times the mean
+  const int64_t mean = c.samples ? (c.rows + c.samples - 1) / c.samples : 0;
+  const int64_t longest = c.longest > 0 ? std::min(c.longest, c.rows) : std::min(c.rows, c.offsets ? 8 * mean : mean);
+  const int most = held_most(elem_bytes, backward);
+  // A workgroup for a whole sample: the smallest that holds one, with the widest chunk that
+  // leaves kWant workgroups, down to 32 bytes of a row.
+  constexpr int64_t kWant = 512;
+  for (const int block : {64, 256, 1024}) {
+    y.block = block;
+    int64_t take = 0;
+    for (int64_t m = std::min(c.groups, block * int64_t(y.vec) / cg); m >= 1; m = m == 1 ? 0 : (m + 1) / 2) {
+      set_lanes(y, m * cg);
+      if (int64_t(y.slices) * most < longest) continue;
+      if (take && m * cg * elem_bytes < 32) break;
+      take = m;
+      if (c.samples * ((c.groups + m - 1) / m) >= kWant) break;
+    }
+    if (!take) continue;
+    y.whole = 1;
+    y.per_chunk = take;
+    y.chunks = (c.groups + take - 1) / take;
+    set_lanes(y, take * cg);
+    y.held = int64_t(y.slices) * kHeldFew >= longest ? kHeldFew : most;
+    return y;
+  }
+  y.whole = 0;
+  y.block = kTileBlock;
+  const int64_t reach = int64_t(kTileBlock) * y.vec;
+  if (cg > reach) {
+    y.split = (cg + reach - 1) / reach;
+    y.part = ((cg + y.split - 1) / y.split + y.vec - 1) / y.vec * y.vec;
+    y.split = (cg + y.part - 1) / y.part;
+    y.per_chunk = 1;
+    y.chunks = c.groups * y.split;
+    set_lanes(y, y.part);
+  } else {
+    // the number of chunks that leaves the fewest threads idle, the smallest unless another
+    // gains 3 %
+    const int64_t least = (c.groups + reach / cg - 1) / (reach / cg);
+    double best = 0;
+    for (int64_t n = least; n < least + 8 && n <= c.groups; ++n) {
+      const int64_t m = (c.groups + n - 1) / n;
+      set_lanes(y, m * cg);
+      const double busy = double(y.slices) * double(c.width) / double((c.groups + m - 1) / m) / y.vec / kTileBlock;
+      if (busy > best * 1.03) {
+        best = busy;
+        y.per_chunk = m;
+      }
+    }
+    y.chunks = (c.groups + y.per_chunk - 1) / y.per_chunk;
+    set_lanes(y, y.per_chunk * cg);
+  }
+  // tiles of four turns at least, so many that they fill the device some times over
+  constexpr int64_t kTileBlocks = 2048;
+  y.tile_rows = std::max<int64_t>((c.rows * y.chunks + kTileBlocks - 1) / kTileBlocks, 4 * y.slices);
+  y.tile_rows = std::min((y.tile_rows + y.slices - 1) / y.slices * y.slices, std::max<int64_t>(c.rows, 1));
+  y.tiles = (c.rows + y.tile_rows - 1) / y.tile_rows;
+  return y;
+}
+
+// The workspace: sums of the pieces (a tile's part of a sample: tile t of sample s is piece
+// t + s, which no other pair is, since a walk through the pieces moves on in one of them at a
+// time), then per sample what they join to.
+struct GroupWork {
+  int64_t pieces, join, coef, total;   // floats before each, and of all
+};
+inline GroupWork group_work(const GroupCall& c, const GroupLayout& y, bool backward) {
+  GroupWork w{};
+  const int64_t pieces = y.whole ? 0 : y.tiles + c.samples;
+  const int64_t per_piece = backward ? 2 * c.width : 2 * c.groups * y.split;
+  w.pieces = 0;
+  w.join = pieces * per_piece;
+  // backward: [samples][2][width] sums per channel (of one whole sample: none), then
+  // [samples][groups][2] means; forward: the statistics, if the caller wants none
+  w.coef = w.join + (backward && !(y.whole && c.samples <= 1) ? c.samples * 2 * c.width : 0);
+  w.total = w.coef + (y.whole ? 0 : c.samples * c.groups * 2);
+  return w;
+}
+
+}  // namespace cgtp

@@ -1,0 +1,1048 @@
+// Group normalisation of rows, channels last, with an activation: forward and backward.
+//
+// Over the M values of one sample (a range of rows) and one group (a range of c columns):
+//   mu = sum(x)/M, s2 = sum((x - mu)^2)/M, rstd = 1/sqrt(s2 + eps), h = (x - mu) rstd,
+//   z = h w + b, y = act(z).
+// Backward, d = g act'(z), a = d w:  dx = rstd (a - sum(a)/M - h sum(a h)/M),
+//   dw = sum over rows of d h, db = sum over rows of d.
+// sum(a) and sum(a h) are the weighted sums of a sample's sums of d and d h per channel, so
+// the backward sums d and d h per channel only, once, and all four gradients come from them.
+//
+// Statistics are fp32, and never a difference of large sums: a thread sums x - K and its square,
+// K its first value of the channel.  As K is one of its n values, (K - mean)^2 <= M2, the sum
+// of squares about the mean, so that sum (x - K)^2 = M2 + n (K - mean)^2 <= (n + 1) M2: the
+// difference that gives M2 loses at most a factor n + 1 of the rounding, n being some ten to a
+// hundred.  Threads' and workgroups' means and M2 are joined about the first of them, then
+// about the joint mean.  A constant sample's mean is exact this way, and y = act(bias).
+//
+// Columns are a thread's own (four of them), rows are dealt out among a workgroup's
+// slices: accesses run along the rows whatever the group's width, and a place may straddle
+// groups.  A sample that the registers of one workgroup hold is read once, in one launch.
+// Longer ones are cut into tiles of rows whose sums a second launch joins and a third applies,
+// reading the rows again.
+#include "group_layout.hpp"
+#include "vec.hpp"
+
+namespace cgtp {
+namespace {
+
+// exp(x) to some 2 ulp: 2^t with t = x log2(e) rounded, times 1 + what the rounding left out.
+__device__ inline float exp_f32(float x) {
+  constexpr float kLog2e = 1.44269504f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
+  const float t = x * kLog2e;
+  const float rest = fmaf(x, kRest, fmaf(x, kLog2e, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  // where p is 0 or infinity (or x is) the rest may be NaN and has no say
+  return p > 0 && p < __builtin_inff() ? fmaf(p, rest * kLn2, p) : p;
+}
+
+__device__ inline float act_value(float z, Act act) {
+  if (act == Act::silu) return z * __builtin_amdgcn_rcpf(1.0f + exp_f32(-z));
+  if (act == Act::gelu) return z * (0.5f + 0.5f * erff(z * 0.707106781f));
+  return z;
+}
+__device__ inline float act_slope(float z, Act act) {
+  if (act == Act::silu) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + exp_f32(-z));
+    return p + z * p * (1.0f - p);
+  }
+  if (act == Act::gelu)
+    return 0.5f + 0.5f * erff(z * 0.707106781f) + z * 0.398942280f * exp_f32(-0.5f * z * z);
+  return 1.0f;
+}
+
+__device__ inline int64_t sample_begin(const GroupCall& c, int64_t s) {
+  if (!c.offsets) return c.rows / c.samples * s;
+  return min(max(int64_t(c.offsets[s]), int64_t(0)), c.rows);
+}
+// Never before the sample's begin, nor past the rows, whatever the offsets hold.
+__device__ inline int64_t sample_end(const GroupCall& c, int64_t s, int64_t begin) {
+  if (!c.offsets) return c.rows / c.samples * (s + 1);
+  return min(max(int64_t(c.offsets[s + 1]), begin), c.rows);
+}
+// The first sample that ends behind `row` (samples, if none does): 64 lanes probe at once.
+__device__ inline int64_t sample_behind(const GroupCall& c, int64_t row) {
+  if (!c.offsets) return c.samples ? row / (c.rows / c.samples) : 0;
+  const int lane = threadIdx.x % kWave;
+  int64_t lo = 0, n = c.samples;
+  while (n > 0) {
+    const int64_t step = (n + kWave - 1) / kWave;
+    const int64_t at = min((lane + 1) * step, n) - 1;
+    // as many lanes as the last probe that lies inside makes
+    const bool before = lane * step < n && int64_t(c.offsets[lo + at + 1]) <= row;
+    const int64_t passed = min(__popcll(__ballot(before)) * step, n);
+    lo += passed;
+    n = step == 1 ? 0 : min(step - 1, n - passed);   // the probed one itself ends behind
+  }
+  return lo;
+}
+
+// The columns of a chunk, and the groups (or the part of one) in it.
+struct Chunk {
+  int64_t c0;        // first column
+  int32_t cw;        // columns
+  int64_t u0;        // first unit: a group, or a part of one
+  int32_t nu, uw;    // units, and the columns of each
+};
+__device__ inline Chunk chunk_of(const GroupCall& c, const GroupLayout& y, int64_t k) {
+  const int64_t cg = c.width / c.groups;
+  Chunk q;
+  if (y.split == 1) {
+    q.u0 = k * y.per_chunk;
+    q.nu = int(min(y.per_chunk, c.groups - q.u0));
+    q.uw = int(cg);
+    q.c0 = q.u0 * cg;
+    q.cw = q.nu * q.uw;
+  } else {
+    const int64_t in = k % y.split * y.part;
+    q.u0 = k;
+    q.nu = 1;
+    q.c0 = k / y.split * cg + in;
+    q.cw = q.uw = int(min(y.part, cg - in));
+  }
+  return q;
+}
+
+// A thread's place: V columns from `at` on, of which [own, end) are its own.  The last place of
+// a chunk that V does not divide is moved back to end with the chunk (but not before the row).
+template <int V>
+struct Place {
+  int slice;
+  bool in;           // has a place
+  int64_t at;        // first column in the row
+  int rel;           // the same in the chunk (may be negative)
+  int own, end;
+  __device__ Place(const Chunk& q, const GroupLayout& y) {
+    slice = int(threadIdx.x) / y.lanes;
+    const int lane = int(threadIdx.x) - slice * y.lanes;
+    const int start = lane * V;
+    in = slice < y.slices && start < q.cw;
+    rel = min(start, q.cw - V);
+    if (q.c0 + rel < 0) rel = -int(q.c0);
+    at = q.c0 + rel;
+    own = start - rel;
+    end = min(V, q.cw - rel);
+  }
+  __device__ bool whole() const { return own == 0 && end == V; }
+  __device__ bool has(int j) const { return j >= own && j < end; }
+};
+
+template <bool Stream, typename T, int V>
+__device__ inline void store_own(const Place<V>& p, T* row, const float (&v)[V]) {
+  Vec<T, V> r;
+#pragma unroll
+  for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(v[j]);
+  if (p.whole()) {
+    store_vec<Stream, T, V>(row + p.at, r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (p.has(j)) row[p.at + j] = r.v[j];
+  }
+}
+
+// Weights (biases) at a place; `none` where there are none.
+template <typename T, int V>
+__device__ inline void place_weights(const Place<V>& p, const void* w, int f32, float none, float (&out)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) out[j] = w && p.in && p.has(j) ? load_either<T>(w, f32, p.at + j) : none;
+}
+
+__device__ inline float wave_sum(float v) { return lanes_sum<kWave>(v); }
+
+// ---- statistics --------------------------------------------------------------------
+
+// Sums of x - K and of its square over a thread's rows of a sample.
+template <int V>
+struct Shifted {
+  float k[V], s[V], q[V];
+  __device__ void clear() {
+#pragma unroll
+    for (int j = 0; j < V; ++j) k[j] = s[j] = q[j] = 0;
+  }
+  __device__ void add(const float (&x)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = x[j] - k[j];
+      s[j] += d;
+      q[j] = fmaf(d, d, q[j]);
+    }
+  }
+};
+
+// What a workgroup's threads have of one sample, in LDS: a mean and an M2 for each slice and
+// column, or, where no place straddles units, for each slice and place.
+struct Entries {
+  float* mean;
+  float* m2;
+  int stride;     // entries of a slice
+  int per_unit;   // entries of a slice and unit
+  float weight;   // values of an entry per row
+  int64_t n;      // rows of the sample here
+  float each;     // of which each slice has so many, and the first `more` one more
+  int more, slices;
+  bool merged;
+  __device__ Entries(float* lds, const Chunk& q, const GroupLayout& y, int v, int64_t rows)
+      : n(rows), slices(y.slices), merged(q.uw % v == 0) {
+    each = float(uint32_t(rows) / uint32_t(slices));
+    more = int(uint32_t(rows) % uint32_t(slices));
+    stride = merged ? q.cw / v : q.cw;
+    per_unit = merged ? q.uw / v : q.uw;
+    weight = merged ? float(v) : 1.0f;
+    mean = lds;
+    m2 = lds + int64_t(stride) * slices;
+  }
+  __device__ float rows_of(int slice) const { return slice < more ? each + 1 : each; }
+
+  template <int V>
+  __device__ void put(const Place<V>& p, const Shifted<V>& t) const {
+    if (!p.in) return;
+    const float rows = rows_of(p.slice), inv = rows > 0 ? 1.0f / rows : 0.0f;
+    float m[V], v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = t.s[j] * inv;
+      m[j] = t.k[j] + d;
+      v[j] = t.q[j] - t.s[j] * d;
+      v[j] = v[j] < 0 ? 0.0f : v[j];   // NaN stays
+    }
+    if (merged) {
+      float s = 0, u = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += m[j] - m[0];
+      const float all = m[0] + s * (1.0f / V);
+#pragma unroll
+      for (int j = 0; j < V; ++j) u += v[j] + rows * (m[j] - all) * (m[j] - all);
+      const int at = p.slice * stride + p.rel / V;
+      mean[at] = all;
+      m2[at] = u;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (p.has(j)) {
+          mean[p.slice * stride + p.rel + j] = m[j];
+          m2[p.slice * stride + p.rel + j] = v[j];
+        }
+    }
+  }
+  // One wave's: the mean and M2 of unit u, in every lane.
+  __device__ void join(int u, float& mean_out, float& m2_out) const {
+    const int total = slices * per_unit, lane = threadIdx.x % kWave;
+    const float first = mean[u * per_unit];   // slice 0 has a row
+    float s = 0, v = 0;
+    for (int e = lane; e < total; e += kWave) {
+      const int slice = e / per_unit, at = slice * stride + u * per_unit + e - slice * per_unit;
+      s += rows_of(slice) * (mean[at] - first);
+    }
+    const float all = first + wave_sum(s) / (float(n) * float(per_unit));
+    for (int e = lane; e < total; e += kWave) {
+      const int slice = e / per_unit, at = slice * stride + u * per_unit + e - slice * per_unit;
+      const float d = mean[at] - all;
+      v += m2[at] + rows_of(slice) * weight * d * d;
+    }
+    mean_out = all;
+    m2_out = wave_sum(v);
+  }
+};
+
+__device__ inline float rstd_of(float m2, float values, float eps) {
+  return 1.0f / sqrtf((values > 0 ? m2 / values : 0.0f) + eps);
+}
+
+// ---- rows --------------------------------------------------------------------------
+
+// Zeros in the workgroup's columns of rows [from, to).
+template <typename T, int V>
+__device__ inline void zero_rows(const GroupCall& c, const Place<V>& p, int slices, int64_t from, int64_t to) {
+  if (!p.in) return;
+  const float none[V] = {};
+  for (int64_t r = from + p.slice; r < to; r += slices) store_own<false>(p, static_cast<T*>(c.y) + r * c.ld_y, none);
+}
+
+template <int V>
+struct Scales {
+  float mean[V], scale[V], shift[V];   // z = (x - mean) scale + shift
+};
+
+template <typename T, int V>
+__device__ inline void activated(const Vec<T, V>& r, const Scales<V>& k, Act act, float (&z)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) z[j] = fmaf(to_f32(r.v[j]) - k.mean[j], k.scale[j], k.shift[j]);
+  // the type of activation is the same for all: one branch for the vector
+  if (act == Act::silu) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[j] = act_value(z[j], Act::silu);
+  } else if (act == Act::gelu) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[j] = act_value(z[j], Act::gelu);
+  }
+}
+
+// What the backward needs at a place: h = (x - mean) rstd, d = g act'(h w + b).
+template <int V>
+struct Slopes {
+  float mean[V], rstd[V], w[V], b[V];
+};
+template <typename T, int V>
+__device__ inline void slopes(const Vec<T, V>& x, const Vec<T, V>& g, const Slopes<V>& k, Act act, float (&h)[V],
+                              float (&d)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    h[j] = (to_f32(x.v[j]) - k.mean[j]) * k.rstd[j];
+    d[j] = to_f32(g.v[j]);
+  }
+  if (act == Act::silu) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] *= act_slope(fmaf(h[j], k.w[j], k.b[j]), Act::silu);
+  } else if (act == Act::gelu) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] *= act_slope(fmaf(h[j], k.w[j], k.b[j]), Act::gelu);
+  }
+}
+
+// The statistics of a place's columns, of sample s.
+template <int V>
+__device__ inline void place_stats(const GroupCall& c, const Place<V>& p, const float* stats, int64_t s,
+                                   float (&mean)[V], float (&rstd)[V]) {
+  const int64_t cg = c.width / c.groups;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    mean[j] = rstd[j] = 0;
+    if (p.in && p.has(j)) {
+      const int64_t at = s * c.groups + (p.at + j) / cg;
+      mean[j] = stats[at];
+      rstd[j] = stats[c.samples * c.groups + at];
+    }
+  }
+}
+
+// A thread's sums of d and d h per column, added over the slices in a fixed order: column e's
+// are lds[e] and lds[n + e] afterwards, n the returned number.
+template <int V>
+__device__ inline int column_sums(const Place<V>& p, const Chunk& q, int slices, const float (&sd)[V],
+                                  const float (&sh)[V], float* lds) {
+  const int n = slices * q.cw;
+  if (p.in) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (p.has(j)) {
+        lds[p.slice * q.cw + p.rel + j] = sd[j];
+        lds[n + p.slice * q.cw + p.rel + j] = sh[j];
+      }
+  }
+  __syncthreads();
+  // in two steps where there are more threads than columns
+  const int threads = int(blockDim.x), sub = min(threads / q.cw, slices);
+  if (sub > 1) {
+    float a = 0, b = 0;
+    const int k = int(threadIdx.x) / q.cw, e = int(threadIdx.x) - k * q.cw;
+    if (k < sub)
+      for (int i = k; i < slices; i += sub) {
+        a += lds[i * q.cw + e];
+        b += lds[n + i * q.cw + e];
+      }
+    __syncthreads();
+    if (k < sub) {
+      lds[k * q.cw + e] = a;
+      lds[n + k * q.cw + e] = b;
+    }
+    __syncthreads();
+  }
+  const int rest = sub > 1 ? sub : slices;
+  for (int e = threadIdx.x; e < q.cw; e += threads) {
+    float a = 0, b = 0;
+    for (int i = 0; i < rest; ++i) {
+      a += lds[i * q.cw + e];
+      b += lds[n + i * q.cw + e];
+    }
+    lds[e] = a;
+    lds[n + e] = b;
+  }
+  __syncthreads();
+  return n;
+}
+
+// ---- a whole sample in one workgroup -----------------------------------------------
+
+// Rows outside every sample lie before the first of them and behind the last.
+__device__ inline void outside(const GroupCall& c, int64_t& first, int64_t& last) {
+  first = last = c.rows;
+  if (c.samples == 0) return;
+  first = sample_begin(c, 0);
+  last = max(first, sample_end(c, c.samples - 1, sample_begin(c, c.samples - 1)));
+}
+// Zeros in them, by the workgroups behind the samples'.
+constexpr int kZeroBlocks = 64;
+template <typename T, int V>
+__device__ inline void zero_outside(const GroupCall& c, const GroupLayout& y, int64_t block) {
+  int64_t first, last;
+  outside(c, first, last);
+  const float none[V] = {};
+  for (int64_t k = 0; k < y.chunks; ++k) {
+    const Place<V> p(chunk_of(c, y, k), y);
+    if (!p.in) continue;
+    for (int64_t i = block * y.slices + p.slice; i < first + c.rows - last; i += int64_t(y.slices) * kZeroBlocks)
+      store_own<false>(p, static_cast<T*>(c.y) + (i < first ? i : last + i - first) * c.ld_y, none);
+  }
+}
+
+// A sample's rows among the slices: those of the thread, and the most of any.
+struct Rows {
+  int mine, most;
+  template <int V>
+  __device__ Rows(const Place<V>& p, int slices, int64_t rows) {
+    const uint32_t n = uint32_t(rows), each = n / uint32_t(slices), more = n - each * uint32_t(slices);
+    mine = p.in ? int(each + (uint32_t(p.slice) < more)) : 0;
+    most = int(each + (more > 0));
+  }
+};
+// A value that the compiler computes where it stands, instead of all rows' addresses and
+// conditions ahead, which would take the registers that hold rows.
+template <typename T>
+__device__ inline T afresh(T v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+// A row's vector as it is held: packed, so that the compiler keeps neither its elements nor
+// their values in 32 bits until they are used.
+template <int Bytes>
+struct Words {
+  typedef uint32_t Type __attribute__((ext_vector_type(Bytes / 4)));
+};
+template <>
+struct Words<4> {
+  typedef uint32_t Type;
+};
+template <>
+struct Words<2> {
+  typedef uint16_t Type;
+};
+template <typename T, int V>
+using Held = typename Words<sizeof(T) * V>::Type;
+template <typename T, int V>
+__device__ inline Held<T, V> hold(const T* p) {
+  return __builtin_bit_cast(Held<T, V>, load_vec<false, T, V>(p));
+}
+template <typename T, int V>
+__device__ inline Vec<T, V> unpack(const Held<T, V>& h) {
+  return __builtin_bit_cast(Vec<T, V>, h);
+}
+template <typename T, int V, int B, int N>
+__global__ __launch_bounds__(B) void group_fwd_kernel(GroupCall c, GroupLayout y, int64_t items) {
+  __shared__ __align__(16) float lds[2 * B * V];
+  if (int64_t(blockIdx.x) >= items) {
+    zero_outside<T, V>(c, y, blockIdx.x - items);
+    return;
+  }
+  for (int64_t item = blockIdx.x; item < c.samples * y.chunks; item += items) {
+    const int64_t s = item / y.chunks;
+    const Chunk q = chunk_of(c, y, item - s * y.chunks);
+    const Place<V> p(q, y);
+    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin), rows = end - begin;
+    const Rows own(p, y.slices, rows);
+    const T* x = static_cast<const T*>(c.x) + (begin + p.slice) * c.ld_x + p.at;
+    const int64_t step = int64_t(y.slices) * c.ld_x;
+    Held<T, V> held[N];
+    Shifted<V> sum;
+    sum.clear();
+    auto read = [&](int first) {
+      const T* at = x + first * step;
+      const int left = afresh(own.mine - first);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (i < left) held[i] = hold<T, V>(at);
+        at = afresh(at + step);
+      }
+    };
+    for (int first = 0; first < own.most; first += N) {
+      read(first);
+      const int left = afresh(own.mine - first);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) {
+          const Vec<T, V> row = unpack<T, V>(held[i]);
+          float v[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] = to_f32(row.v[j]);
+          if (i == 0 && first == 0) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum.k[j] = v[j];
+          }
+          sum.add(v);
+        }
+    }
+    const Entries e(lds, q, y, V, rows);
+    e.put(p, sum);
+    float w[V], b[V];
+    place_weights<T>(p, c.weight, c.weight_f32, 1.0f, w);
+    place_weights<T>(p, c.bias, c.weight_f32, 0.0f, b);
+    __syncthreads();
+    for (int u = threadIdx.x / kWave; u < q.nu; u += B / kWave) {
+      float mean = 0, m2 = 0;
+      if (rows > 0) e.join(u, mean, m2);
+      const float rstd = rstd_of(m2, float(rows) * float(q.uw), c.eps);
+      if (threadIdx.x % kWave == 0) {
+        e.mean[u * e.per_unit] = mean;   // in the place of an entry that only this wave reads
+        e.m2[u * e.per_unit] = rstd;
+        if (c.stats) {
+          c.stats[s * c.groups + q.u0 + u] = mean;
+          c.stats[(c.samples + s) * c.groups + q.u0 + u] = rstd;
+        }
+      }
+    }
+    __syncthreads();
+    Scales<V> k;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int u = p.in && p.has(j) ? (p.rel + j) / q.uw : 0;
+      k.mean[j] = e.mean[u * e.per_unit];
+      k.scale[j] = e.m2[u * e.per_unit] * w[j];
+      k.shift[j] = b[j];
+    }
+    T* out = static_cast<T*>(c.y) + (begin + p.slice) * c.ld_y;
+    const int64_t step_y = int64_t(y.slices) * c.ld_y;
+    for (int first = 0; first < own.most; first += N) {
+      if (own.most > N) read(first);   // else they are held
+      const int left = afresh(own.mine - first);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (i < left) {
+          float z[V];
+          activated(unpack<T, V>(held[i]), k, c.act, z);
+          store_own<false>(p, out, z);
+        }
+        out = afresh(out + step_y);
+      }
+    }
+    __syncthreads();   // before the next sample's entries
+  }
+}
+
+template <typename T, int V, int B, int N>
+__global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y, int64_t items, float* join) {
+  __shared__ __align__(16) float lds[2 * B * V];
+  if (int64_t(blockIdx.x) >= items) {
+    zero_outside<T, V>(c, y, blockIdx.x - items);
+    return;
+  }
+  for (int64_t item = blockIdx.x; item < c.samples * y.chunks; item += items) {
+    const int64_t s = item / y.chunks;
+    const Chunk q = chunk_of(c, y, item - s * y.chunks);
+    const Place<V> p(q, y);
+    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin), rows = end - begin;
+    const Rows own(p, y.slices, rows);
+    const T* x = static_cast<const T*>(c.x) + (begin + p.slice) * c.ld_x + p.at;
+    const T* g = static_cast<const T*>(c.grad_out) + (begin + p.slice) * c.ld_g + p.at;
+    const int64_t step_x = int64_t(y.slices) * c.ld_x, step_g = int64_t(y.slices) * c.ld_g;
+    Held<T, V> hx[N], hg[N];
+    Slopes<V> k;
+    place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
+    place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
+    place_stats(c, p, c.stats, s, k.mean, k.rstd);
+    float sd[V] = {}, sh[V] = {};
+    auto read = [&](int first) {
+      const T *at_x = x + first * step_x, *at_g = g + first * step_g;
+      const int left = afresh(own.mine - first);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (i < left) {
+          hx[i] = hold<T, V>(at_x);
+          hg[i] = hold<T, V>(at_g);
+        }
+        at_x = afresh(at_x + step_x);
+        at_g = afresh(at_g + step_g);
+      }
+    };
+    for (int first = 0; first < own.most; first += N) {
+      read(first);
+      const int left = afresh(own.mine - first);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) {
+          float h[V], d[V];
+          slopes(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]), k, c.act, h, d);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            sd[j] += d[j];
+            sh[j] += d[j] * h[j];
+          }
+        }
+    }
+    const int n = column_sums(p, q, y.slices, sd, sh, lds);
+    // the columns' sums, for the weights' gradients
+    for (int e = threadIdx.x; e < q.cw; e += B) {
+      if (join) {
+        join[s * 2 * c.width + q.c0 + e] = lds[e];
+        join[(s * 2 + 1) * c.width + q.c0 + e] = lds[n + e];
+      } else {
+        if (c.grad_bias) store_either<T>(c.grad_bias, c.weight_f32, q.c0 + e, lds[e]);
+        if (c.grad_weight) store_either<T>(c.grad_weight, c.weight_f32, q.c0 + e, lds[n + e]);
+      }
+    }
+    if (c.y) {
+      __syncthreads();
+      // a group's means of a and of a h
+      const float inv = rows > 0 ? 1.0f / (float(rows) * float(q.uw)) : 0.0f;
+      for (int u = threadIdx.x / kWave; u < q.nu; u += B / kWave) {
+        float a = 0, b = 0;
+        for (int e = threadIdx.x % kWave; e < q.uw; e += kWave) {
+          const int at = u * q.uw + e;
+          const float w = c.weight ? load_either<T>(c.weight, c.weight_f32, q.c0 + at) : 1.0f;
+          a += w * lds[at];
+          b += w * lds[n + at];
+        }
+        a = wave_sum(a) * inv;
+        b = wave_sum(b) * inv;
+        if (threadIdx.x % kWave == 0) {
+          lds[u * q.uw] = a;   // in the place of a column that only this wave reads
+          lds[n + u * q.uw] = b;
+        }
+      }
+      __syncthreads();
+      float ma[V], mh[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int u = p.in && p.has(j) ? (p.rel + j) / q.uw : 0;
+        ma[j] = lds[u * q.uw];
+        mh[j] = lds[n + u * q.uw];
+      }
+      T* out = static_cast<T*>(c.y) + (begin + p.slice) * c.ld_y;
+      const int64_t step_y = int64_t(y.slices) * c.ld_y;
+      for (int first = 0; first < own.most; first += N) {
+        if (own.most > N) read(first);
+        const int left = afresh(own.mine - first);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (i < left) {
+            float h[V], d[V];
+            slopes(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]), k, c.act, h, d);
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
+            store_own<false>(p, out, d);
+          }
+          out = afresh(out + step_y);
+        }
+      }
+    }
+    __syncthreads();   // before the next sample's sums
+  }
+}
+
+// ---- tiles -------------------------------------------------------------------------
+
+// Walks through the workgroup's tile: f(sample, first row, past the last, piece).
+template <typename F>
+__device__ inline void for_pieces(const GroupCall& c, int64_t tile, int64_t r0, int64_t r1, F&& f) {
+  for (int64_t s = sample_behind(c, r0); s < c.samples; ++s) {
+    const int64_t begin = sample_begin(c, s);
+    if (begin >= r1) break;
+    const int64_t lo = max(begin, r0), hi = min(sample_end(c, s, begin), r1);
+    if (lo < hi) f(s, lo, hi, tile + s);
+  }
+}
+
+constexpr int kInFlight = 8;   // rows that a thread reads at once
+
+// Rows lo + slice, + slices ... of [lo, hi): f(vector, whether it is the first) for each.
+template <typename T, int V, typename F>
+__device__ inline void for_rows(const Place<V>& p, int slices, const T* x, int64_t ld, int64_t lo, int64_t hi, F&& f) {
+  const int64_t step = int64_t(slices) * ld;
+  int64_t left = (hi - lo - p.slice + slices - 1) / slices;
+  if (!p.in || hi - lo <= p.slice) return;
+  const T* at = x + (lo + p.slice) * ld + p.at;
+  bool first = true;
+  while (left > 0) {
+    Vec<T, V> v[kInFlight];
+#pragma unroll
+    for (int i = 0; i < kInFlight; ++i) v[i] = load_vec<false, T, V>(at + (i < left ? i : left - 1) * step);
+#pragma unroll
+    for (int i = 0; i < kInFlight; ++i)
+      if (i < left) {
+        f(v[i], first);
+        first = false;
+      }
+    at += kInFlight * step;
+    left -= kInFlight;
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kTileBlock) void group_sum_kernel(GroupCall c, GroupLayout y, float* pieces) {
+  __shared__ __align__(16) float lds[2 * kTileBlock * V];
+  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
+  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
+  const Place<V> p(q, y);
+  const int64_t units = c.groups * y.split;
+  for_pieces(c, tile, r0, r1, [&](int64_t, int64_t lo, int64_t hi, int64_t piece) {
+    Shifted<V> sum;
+    sum.clear();
+    for_rows<T, V>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, lo, hi, [&](const Vec<T, V>& r, bool first) {
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = to_f32(r.v[j]);
+      if (first) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum.k[j] = v[j];
+      }
+      sum.add(v);
+    });
+    const Entries e(lds, q, y, V, hi - lo);
+    e.put(p, sum);
+    __syncthreads();
+    for (int u = threadIdx.x / kWave; u < q.nu; u += kTileBlock / kWave) {
+      float mean, m2;
+      e.join(u, mean, m2);
+      if (threadIdx.x % kWave == 0) {
+        float* at = pieces + (piece * units + q.u0 + u) * 2;
+        at[0] = mean;
+        at[1] = m2;
+      }
+    }
+    __syncthreads();
+  });
+}
+
+// A wave joins the pieces of one sample and group.
+__global__ __launch_bounds__(kTileBlock) void group_join_kernel(GroupCall c, GroupLayout y, const float* pieces,
+                                                                float* stats) {
+  const int lane = threadIdx.x % kWave;
+  const int64_t waves = int64_t(gridDim.x) * (kTileBlock / kWave), cg = c.width / c.groups, units = c.groups * y.split;
+  for (int64_t k = int64_t(blockIdx.x) * (kTileBlock / kWave) + threadIdx.x / kWave; k < c.samples * c.groups; k += waves) {
+    const int64_t s = k / c.groups, g = k - s * c.groups;
+    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin);
+    float mean = 0, m2 = 0;
+    if (begin < end) {
+      const int64_t t0 = begin / y.tile_rows, n = ((end - 1) / y.tile_rows - t0 + 1) * y.split;
+      const float* at = pieces + ((t0 + s) * units + g * y.split) * 2;
+      const float first = at[0];
+      // piece e / split, part e % split: its mean, M2 and values
+      auto place = [&](int64_t e, float& values) {
+        const int64_t t = e / y.split, part = e - t * y.split, r = (t0 + t) * y.tile_rows;
+        const int64_t rows = min(r + y.tile_rows, end) - max(r, begin);
+        values = float(rows) * float(min(y.part, cg - part * y.part));
+        return at + (t * units + part) * 2;
+      };
+      float a = 0, b = 0, values;
+      for (int64_t e = lane; e < n; e += kWave) {
+        const float* q = place(e, values);
+        a += values * (q[0] - first);
+      }
+      mean = first + wave_sum(a) / (float(end - begin) * float(cg));
+      for (int64_t e = lane; e < n; e += kWave) {
+        const float* q = place(e, values);
+        const float d = q[0] - mean;
+        b += q[1] + values * d * d;
+      }
+      m2 = wave_sum(b);
+    }
+    if (lane == 0) {
+      stats[k] = mean;
+      stats[c.samples * c.groups + k] = rstd_of(m2, float(end - begin) * float(cg), c.eps);
+    }
+  }
+}
+
+// Zeros of a tile's rows outside every sample.
+template <typename T, int V>
+__device__ inline void zero_tile(const GroupCall& c, const GroupLayout& y, const Place<V>& p, int64_t r0, int64_t r1) {
+  int64_t first, last;
+  outside(c, first, last);
+  zero_rows<T>(c, p, y.slices, r0, min(r1, first));
+  zero_rows<T>(c, p, y.slices, max(r0, last), r1);
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kTileBlock) void group_apply_kernel(GroupCall c, GroupLayout y, const float* stats) {
+  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
+  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
+  const Place<V> p(q, y);
+  float w[V], b[V];
+  place_weights<T>(p, c.weight, c.weight_f32, 1.0f, w);
+  place_weights<T>(p, c.bias, c.weight_f32, 0.0f, b);
+  for_pieces(c, tile, r0, r1, [&](int64_t s, int64_t lo, int64_t hi, int64_t) {
+    Scales<V> k;
+    place_stats(c, p, stats, s, k.mean, k.scale);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      k.scale[j] *= w[j];
+      k.shift[j] = b[j];
+    }
+    T* out = static_cast<T*>(c.y) + (lo + p.slice) * c.ld_y;
+    for_rows<T, V>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, lo, hi, [&](const Vec<T, V>& r, bool) {
+      float z[V];
+      activated(r, k, c.act, z);
+      store_own<false>(p, out, z);
+      out += int64_t(y.slices) * c.ld_y;
+    });
+  });
+  if (c.zero_outside && c.offsets) zero_tile<T>(c, y, p, r0, r1);
+}
+
+// Rows of x and of grad_out together.
+template <typename T, int V, typename F>
+__device__ inline void for_row_pairs(const GroupCall& c, const Place<V>& p, int slices, int64_t lo, int64_t hi, F&& f) {
+  const int64_t sx = int64_t(slices) * c.ld_x, sg = int64_t(slices) * c.ld_g;
+  int64_t left = (hi - lo - p.slice + slices - 1) / slices;
+  if (!p.in || hi - lo <= p.slice) return;
+  const T* x = static_cast<const T*>(c.x) + (lo + p.slice) * c.ld_x + p.at;
+  const T* g = static_cast<const T*>(c.grad_out) + (lo + p.slice) * c.ld_g + p.at;
+  constexpr int kPairs = kInFlight / 2;
+  while (left > 0) {
+    Vec<T, V> vx[kPairs], vg[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      vx[i] = load_vec<false, T, V>(x + (i < left ? i : left - 1) * sx);
+      vg[i] = load_vec<false, T, V>(g + (i < left ? i : left - 1) * sg);
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      if (i < left) f(vx[i], vg[i]);
+    x += kPairs * sx;
+    g += kPairs * sg;
+    left -= kPairs;
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kTileBlock) void group_bwd_sum_kernel(GroupCall c, GroupLayout y, float* pieces) {
+  __shared__ __align__(16) float lds[2 * kTileBlock * V];
+  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
+  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
+  const Place<V> p(q, y);
+  Slopes<V> k;
+  place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
+  place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
+  for_pieces(c, tile, r0, r1, [&](int64_t s, int64_t lo, int64_t hi, int64_t piece) {
+    place_stats(c, p, c.stats, s, k.mean, k.rstd);
+    float sd[V] = {}, sh[V] = {};
+    for_row_pairs<T, V>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
+      float h[V], d[V];
+      slopes(x, g, k, c.act, h, d);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        sd[j] += d[j];
+        sh[j] += d[j] * h[j];
+      }
+    });
+    const int n = column_sums(p, q, y.slices, sd, sh, lds);
+    float* at = pieces + piece * 2 * c.width + q.c0;
+    for (int e = threadIdx.x; e < q.cw; e += kTileBlock) {
+      at[e] = lds[e];
+      at[c.width + e] = lds[n + e];
+    }
+    __syncthreads();
+  });
+}
+
+// A workgroup joins the pieces of one sample and group: the columns' sums, and the means of
+// a and a h.
+template <typename T>
+__global__ __launch_bounds__(kTileBlock) void group_bwd_join_kernel(GroupCall c, GroupLayout y, const float* pieces,
+                                                                    float* join, float* coef) {
+  __shared__ float lds[2][kTileBlock];
+  const int64_t cg = c.width / c.groups;
+  const int lanes = int(min(cg, int64_t(kTileBlock))), subs = kTileBlock / lanes;
+  const int sub = int(threadIdx.x) / lanes, lane = int(threadIdx.x) - sub * lanes;
+  for (int64_t k = blockIdx.x; k < c.samples * c.groups; k += gridDim.x) {
+    const int64_t s = k / c.groups, g = k - s * c.groups;
+    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin);
+    const int64_t t0 = begin / y.tile_rows, n = begin < end ? (end - 1) / y.tile_rows - t0 + 1 : 0;
+    float sa = 0, sh = 0;
+    for (int64_t c0 = 0; c0 < cg; c0 += lanes) {
+      const bool in = sub < subs && c0 + lane < cg;
+      const int64_t e = g * cg + c0 + lane;
+      float a = 0, b = 0;
+      if (in) {
+        const float* at = pieces + (t0 + s) * 2 * c.width + e;
+#pragma unroll 4
+        for (int64_t t = sub; t < n; t += subs) {
+          a += at[t * 2 * c.width];
+          b += at[(t * 2 + 1) * c.width];
+        }
+      }
+      lds[0][threadIdx.x] = a;
+      lds[1][threadIdx.x] = b;
+      __syncthreads();
+      if (sub == 0 && in) {
+        for (int i = 1; i < subs; ++i) {
+          a += lds[0][i * lanes + lane];
+          b += lds[1][i * lanes + lane];
+        }
+        if (join) {
+          join[s * 2 * c.width + e] = a;
+          join[(s * 2 + 1) * c.width + e] = b;
+        } else {
+          if (c.grad_bias) store_either<T>(c.grad_bias, c.weight_f32, e, a);
+          if (c.grad_weight) store_either<T>(c.grad_weight, c.weight_f32, e, b);
+        }
+        const float w = c.weight ? load_either<T>(c.weight, c.weight_f32, e) : 1.0f;
+        sa += w * a;
+        sh += w * b;
+      }
+      __syncthreads();
+    }
+    sa = wave_sum(sa);
+    sh = wave_sum(sh);
+    if (threadIdx.x % kWave == 0) {
+      lds[0][threadIdx.x / kWave] = sa;
+      lds[1][threadIdx.x / kWave] = sh;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      float v = 0;
+      for (int i = 0; i < kTileBlock / kWave; ++i) v += lds[threadIdx.x][i];
+      coef[k * 2 + threadIdx.x] = begin < end ? v / (float(end - begin) * float(cg)) : 0.0f;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c, GroupLayout y, const float* coef) {
+  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
+  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
+  const Place<V> p(q, y);
+  const int64_t cg = c.width / c.groups;
+  Slopes<V> k;
+  place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
+  place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
+  for_pieces(c, tile, r0, r1, [&](int64_t s, int64_t lo, int64_t hi, int64_t) {
+    place_stats(c, p, c.stats, s, k.mean, k.rstd);
+    float ma[V], mh[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      ma[j] = mh[j] = 0;
+      if (p.in && p.has(j)) {
+        const float* at = coef + (s * c.groups + (p.at + j) / cg) * 2;
+        ma[j] = at[0];
+        mh[j] = at[1];
+      }
+    }
+    T* out = static_cast<T*>(c.y) + (lo + p.slice) * c.ld_y;
+    for_row_pairs<T, V>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
+      float h[V], d[V];
+      slopes(x, g, k, c.act, h, d);
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
+      store_own<false>(p, out, d);
+      out += int64_t(y.slices) * c.ld_y;
+    });
+  });
+  if (c.offsets) zero_tile<T>(c, y, p, r0, r1);
+}
+
+// The weights' gradients from the samples' sums, 16 columns a workgroup, in a fixed order.
+constexpr int kParamBlock = 1024, kParamColumns = 16;
+template <typename T>
+__global__ __launch_bounds__(kParamBlock) void group_param_kernel(GroupCall c, const float* join) {
+  constexpr int kSubs = kParamBlock / kParamColumns;
+  __shared__ float lds[2][kParamBlock];
+  const int sub = threadIdx.x / kParamColumns, lane = threadIdx.x % kParamColumns;
+  const int64_t e = int64_t(blockIdx.x) * kParamColumns + lane;
+  float a = 0, b = 0;
+  if (e < c.width) {
+#pragma unroll 4
+    for (int64_t s = sub; s < c.samples; s += kSubs) {
+      a += join[s * 2 * c.width + e];
+      b += join[(s * 2 + 1) * c.width + e];
+    }
+  }
+  lds[0][threadIdx.x] = a;
+  lds[1][threadIdx.x] = b;
+  for (int half = kSubs / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (sub < half) {
+      lds[0][threadIdx.x] += lds[0][threadIdx.x + half * kParamColumns];
+      lds[1][threadIdx.x] += lds[1][threadIdx.x + half * kParamColumns];
+    }
+  }
+  if (sub == 0 && e < c.width) {
+    if (c.grad_bias) store_either<T>(c.grad_bias, c.weight_f32, e, lds[0][lane]);
+    if (c.grad_weight) store_either<T>(c.grad_weight, c.weight_f32, e, lds[1][lane]);
+  }
+}
+
+// ---- launches ----------------------------------------------------------------------
+
+// Workgroups of one item each, as many as a launch takes.
+unsigned blocks_of(int64_t items, int threads) { return unsigned(std::min(items, kGroupGrid / threads - kZeroBlocks)); }
+
+template <typename T, int V, int B>
+void whole(const GroupCall& c, const GroupLayout& y, bool backward, float* join, hipStream_t s) {
+  const int64_t items = blocks_of(c.samples * y.chunks, B);
+  const bool zeros = c.offsets && c.rows > 0 && (backward ? c.y != nullptr : c.zero_outside != 0);
+  const dim3 grid{unsigned(items + (zeros ? kZeroBlocks : 0))}, block{B};
+  if (grid.x == 0) return;
+  constexpr int kForward = held_most(int(sizeof(T)), false), kBackward = held_most(int(sizeof(T)), true);
+  if (!backward) {
+    if (y.held == kHeldFew)
+      hipLaunchKernelGGL((group_fwd_kernel<T, V, B, kHeldFew>), grid, block, 0, s, c, y, items);
+    else
+      hipLaunchKernelGGL((group_fwd_kernel<T, V, B, kForward>), grid, block, 0, s, c, y, items);
+  } else {
+    if (y.held == kHeldFew)
+      hipLaunchKernelGGL((group_bwd_kernel<T, V, B, kHeldFew>), grid, block, 0, s, c, y, items, join);
+    else
+      hipLaunchKernelGGL((group_bwd_kernel<T, V, B, kBackward>), grid, block, 0, s, c, y, items, join);
+  }
+}
+
+template <typename T, int V>
+hipError_t run(const GroupCall& c, const GroupLayout& y, bool backward, hipStream_t s) {
+  const GroupWork at = group_work(c, y, backward);
+  float* pieces = c.work + at.pieces;
+  const bool params = backward && (c.grad_weight || c.grad_bias);
+  // the sums per sample and channel, unless one sample's are the gradients themselves
+  float* join = params && c.samples != 1 ? c.work + at.join : nullptr;
+  if (y.whole) {
+    // a null join makes the kernel write the gradients
+    if (y.block == 64)
+      whole<T, V, 64>(c, y, backward, join, s);
+    else if (y.block == 256)
+      whole<T, V, 256>(c, y, backward, join, s);
+    else
+      whole<T, V, 1024>(c, y, backward, join, s);
+  } else {
+    float* coef = c.work + at.coef;
+    const dim3 grid{unsigned(y.tiles * y.chunks)}, block{kTileBlock};
+    const int64_t joins = c.samples * c.groups;
+    if (!backward) {
+      float* stats = c.stats ? c.stats : coef;
+      if (grid.x) hipLaunchKernelGGL((group_sum_kernel<T, V>), grid, block, 0, s, c, y, pieces);
+      if (joins)
+        hipLaunchKernelGGL(group_join_kernel, dim3(blocks_of((joins + 3) / 4, kTileBlock)), block, 0, s, c, y, pieces, stats);
+      if (grid.x) hipLaunchKernelGGL((group_apply_kernel<T, V>), grid, block, 0, s, c, y, stats);
+    } else {
+      if (grid.x) hipLaunchKernelGGL((group_bwd_sum_kernel<T, V>), grid, block, 0, s, c, y, pieces);
+      if (joins)
+        hipLaunchKernelGGL(group_bwd_join_kernel<T>, dim3(blocks_of(joins, kTileBlock)), block, 0, s, c, y, pieces, join,
+                           coef);
+      if (grid.x && c.y) hipLaunchKernelGGL((group_bwd_apply_kernel<T, V>), grid, block, 0, s, c, y, coef);
+    }
+  }
+  if (params && c.samples != 1)
+    hipLaunchKernelGGL(group_param_kernel<T>, dim3(unsigned((c.width + kParamColumns - 1) / kParamColumns)),
+                       dim3(kParamBlock), 0, s, c, join);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run(const GroupCall& c, bool backward, hipStream_t s) {
+  const GroupLayout y = lay_out_group(c, int(sizeof(T)), backward);
+  return y.vec == 1 ? run<T, 1>(c, y, backward, s) : run<T, kGroupVec>(c, y, backward, s);
+}
+hipError_t run(const GroupCall& c, Elem type, bool backward, hipStream_t s) {
+  return type == Elem::f32 ? run<float>(c, backward, s)
+         : type == Elem::bf16 ? run<Bf16>(c, backward, s) : run<F16>(c, backward, s);
+}
+
+}  // namespace
+
+size_t group_norm_floats(const GroupCall& c, Elem type, bool backward) {
+  return size_t(group_work(c, lay_out_group(c, type == Elem::f32 ? 4 : 2, backward), backward).total);
+}
+
+hipError_t launch_group_norm_forward(const GroupCall& c, Elem type, hipStream_t s) { return run(c, type, false, s); }
+hipError_t launch_group_norm_backward(const GroupCall& c, Elem type, hipStream_t s) { return run(c, type, true, s); }
+
+}  // namespace cgtp

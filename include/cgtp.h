@@ -408,6 +408,98 @@ int cgtp_grad_norm_workspace_size(cgtp_params_t set, size_t* bytes);
 int cgtp_grad_norm(cgtp_params_t set, int grad_dtype, const void* const* grads, const float* grad_scale,
                    double max_norm, float* out, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Operators for branching networks --------------------------------------------
+ *
+ * What a network needs that sends its edges through several branches, each a convolution of
+ * its own that takes its edges' gates (cgtp_conv_forward_gated; BranchIP, Method: zero-gated
+ * features are omitted): group normalisation with an activation over each structure's rows
+ * (the hidden rows that gates and weights come from), the routing that makes the gates, its
+ * balance loss, and the way back from the convolution's weight gradient to the gates.  The
+ * interface is this library's own.  Types, ownership, asynchrony and errors as for the
+ * training operators above. */
+
+/* Activations of cgtp_group_norm_forward: z, z sigmoid(z), z (1 + erf(z / sqrt 2)) / 2. */
+enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1, CGTP_ACT_GELU = 2 };
+
+/* Group normalisation of rows, channels last, with an activation.  The rows of x [n_rows,
+ * width] belong to n_samples samples (structures): sample s has rows offsets[s] to
+ * offsets[s + 1] - 1, or, where offsets is NULL, n_rows / n_samples of them (which has to be
+ * a whole number).  The columns are n_groups groups of width / n_groups (a whole number).
+ * Over the M values of one sample and group:
+ *   mu = sum(x)/M, s2 = sum((x - mu)^2)/M, rstd = 1/sqrt(s2 + eps),
+ *   z = (x - mu) rstd weight + bias,  y = act(z)
+ * weight and bias [width] (each may be NULL: 1, 0) are of type weight_dtype, CGTP_F32 or
+ * dtype; x and y as cgtp_layer_norm_forward's (rows any stride apart, one element's
+ * alignment, y may be x itself).  stats [2, n_samples, n_groups] fp32 (may be NULL) receives
+ * mu and rstd, 0 and 1/sqrt(eps) for a sample without rows.  offsets [n_samples + 1] are on
+ * the device and ascend; the library reads no row outside 0 to n_rows - 1, whatever they
+ * hold.  Rows before offsets[0] and from offsets[n_samples] on belong to no sample: they are
+ * not read, and their y is left as it is, or 0 with zero_outside != 0.
+ * longest: rows of the longest sample, as far as the caller knows (0: not known).  It chooses
+ * between launches, nothing else: a call with another value is as right, and slower where a
+ * sample much longer than told falls to one workgroup.
+ * workspace: 256-byte aligned, cgtp_group_norm_workspace_size bytes (0: NULL).  Rows of at
+ * most 2^24 values.  No atomics: bitwise reproducible. */
+int cgtp_group_norm_workspace_size(int backward, int dtype, int64_t n_rows, int64_t width, int64_t n_groups,
+                                   int64_t n_samples, const int32_t* offsets, int64_t longest, size_t* bytes);
+int cgtp_group_norm_forward(int dtype, int64_t n_rows, int64_t width, int64_t n_groups, int64_t n_samples,
+                            const int32_t* offsets, int64_t longest, const void* x, int64_t ld_x, int weight_dtype,
+                            const void* weight, const void* bias, int activation, double eps, int zero_outside, void* y,
+                            int64_t ld_y, float* stats, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients of a scalar L of that output, given grad_out = dL/dy and the forward's x, stats,
+ * weight and bias.  With h = (x - mu) rstd, d = grad_out act'(h weight + bias), a = d weight:
+ *   grad_x = rstd (a - sum(a)/M - h sum(a h)/M)               0 for rows outside every sample
+ *   grad_weight[c] = sum over rows of d h, grad_bias[c] = sum over rows of d
+ * Each output may be NULL to skip it, and is overwritten; it may not overlap an input.
+ * grad_weight and grad_bias are of type weight_dtype. */
+int cgtp_group_norm_backward(int dtype, int64_t n_rows, int64_t width, int64_t n_groups, int64_t n_samples,
+                             const int32_t* offsets, int64_t longest, const void* grad_out, int64_t ld_g,
+                             const void* x, int64_t ld_x, const float* stats, int weight_dtype, const void* weight,
+                             const void* bias, int activation, void* grad_x, int64_t ld_gx, void* grad_weight,
+                             void* grad_bias, void* workspace, size_t ws_bytes, void* stream);
+
+/* Routing of rows (edges) to k of n branches by their logits [n_rows, n] (type dtype, rows
+ * ld elements apart).  With p = softmax(logits) of a row, the k branches of the largest
+ * logits are chosen; equal ones go to the lowest index, NaN counts as larger than every
+ * number, and a branch whose logit is -infinity is never chosen.  A row whose mask (may be
+ * NULL) is 0, or whose logits are all -infinity, takes no part.  Outputs:
+ *   ids [n_rows, k]: the chosen, largest first, -1 where there is none (further);
+ *   gates: p of the chosen; with renormalise != 0 divided by their sum.  [n_rows, k] beside
+ *     the ids (0 where there is none), or with dense != 0 [n, n_rows], 0 for what a row did
+ *     not choose: row b is the gate argument of branch b's convolution;
+ *   counts [n]: the rows that chose each branch;
+ *   balance [1] and slope [n]: with C the sum of the counts and R the rows that take part,
+ *     slope[e] = n counts[e] / (C R), balance = sum over e and rows of slope[e] p[e]: 1 where
+ *     choices and probabilities are even, n where one branch has all (0 if R = 0).
+ * A row whose logits hold NaN or +infinity has NaN gates and makes balance NaN.
+ * 1 <= n <= 1024, 1 <= k <= min(n, 64).  Sums over rows in a fixed order, joined in fp64; no
+ * atomics: bitwise reproducible.  workspace: 256-byte aligned, cgtp_route_workspace_size
+ * bytes (0: NULL). */
+int cgtp_route_workspace_size(int64_t n_rows, int n, size_t* bytes);
+int cgtp_route_forward(int dtype, int64_t n_rows, int n, int k, const void* logits, int64_t ld, const uint8_t* mask,
+                       int renormalise, int dense, int32_t* ids, float* gates, int32_t* counts, float* balance,
+                       float* slope, void* workspace, size_t ws_bytes, void* stream);
+
+/* The logits' gradient [n_rows, n] (type dtype, rows ld_g elements apart), of a scalar L of
+ * the gates and the balance loss: grad_gates = dL/dgates (as the forward's gates are laid
+ * out; only the entries of chosen branches are read; NULL: 0), grad_balance [1] =
+ * dL/dbalance (NULL: 0).  ids and slope are the forward's: choices and counts are held
+ * fixed.  Rows without part receive 0.  Ids outside -1 to n - 1 count as -1. */
+int cgtp_route_backward(int dtype, int64_t n_rows, int n, int k, const void* logits, int64_t ld, int renormalise,
+                        int dense, const int32_t* ids, const float* slope, const float* grad_gates,
+                        const float* grad_balance, void* grad_logits, int64_t ld_g, void* stream);
+
+/* The gradient of the convolution with respect to its gate, from the gradient with respect
+ * to its weights that cgtp_conv_backward wrote with that gate.  An edge's message is linear
+ * in gate[e] w[e], so that
+ *   grad_gate[e] = sum over c of w[e, c] grad_w[e, c] / gate[e]
+ * and 0 for inactive edges (mask 0, may be NULL, or gate 0), whose w and grad_w are not read.
+ * w and grad_w [n_edges, w_per_edge], gate and grad_gate [n_edges], fp32 (grad_w carries the
+ * gate: one so small that their product leaves the normal range of fp32 costs digits). */
+int cgtp_conv_gate_backward(int64_t n_edges, int64_t w_per_edge, const float* w, const float* grad_w,
+                            const uint8_t* mask, const float* gate, float* grad_gate, void* stream);
+
 /* Frees the plan's device tables, streams and events (interface bookkeeping; the pages
  * define no such call).  NULL is ignored. */
 void cgtp_plan_destroy(cgtp_plan_t plan);
