@@ -20,12 +20,14 @@ struct GroupLayout {
   int vec;               // columns of a place: kGroupVec, or 1 where the row has fewer
   int block;             // threads of a workgroup
   int held;              // whole: rows that a thread holds
-  int64_t per_chunk;     // groups of a chunk
-  int64_t split;         // parts of a group (1 unless a group is wider than a workgroup reaches)
-  int64_t part;          // columns of a part; the last of a group may have fewer
-  int64_t chunks;
+  int per_group;         // columns of a group
+  int per_chunk;         // groups of a chunk
+  int split;             // parts of a group (1 unless a group is wider than a workgroup reaches)
+  int part;              // columns of a part; the last of a group may have fewer
+  int chunks;
   int lanes, slices;
-  int64_t tile_rows, tiles;   // tiles only
+  int tile_rows, tiles;  // tiles only
+  int equal;             // rows of each sample, where there are no offsets
 };
 
 // Columns of a thread's place.  Everything that a thread has per column (weights, statistics,
@@ -45,30 +47,34 @@ inline void set_lanes(GroupLayout& y, int64_t columns) {
 inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backward) {
   GroupLayout y{};
   const int64_t cg = c.width / c.groups;
+  y.per_group = int(cg);
+  y.equal = c.offsets || c.samples == 0 ? 0 : int(c.rows / c.samples);
   y.vec = c.width >= kGroupVec ? kGroupVec : 1;
   y.split = 1;
-  y.part = cg;
+  y.part = int(cg);
   // the longest sample: as told, as equal samples have it, or eight times the mean
   const int64_t mean = c.samples ? (c.rows + c.samples - 1) / c.samples : 0;
   const int64_t longest = c.longest > 0 ? std::min(c.longest, c.rows) : std::min(c.rows, c.offsets ? 8 * mean : mean);
   const int most = held_most(elem_bytes, backward);
-  // A workgroup for a whole sample: the smallest that holds one, with the widest chunk that
-  // leaves kWant workgroups, down to 32 bytes of a row.
+  // A workgroup for a whole sample: the smallest that holds one, with the widest chunk, if that
+  // leaves kWant workgroups; else 256 or 1024 threads that do, with chunks down to 32 bytes of a
+  // row.
   constexpr int64_t kWant = 512;
   for (const int block : {64, 256, 1024}) {
     y.block = block;
-    int64_t take = 0;
+    int64_t take = 0, items = 0;
     for (int64_t m = std::min(c.groups, block * int64_t(y.vec) / cg); m >= 1; m = m == 1 ? 0 : (m + 1) / 2) {
       set_lanes(y, m * cg);
       if (int64_t(y.slices) * most < longest) continue;
       if (take && m * cg * elem_bytes < 32) break;
       take = m;
-      if (c.samples * ((c.groups + m - 1) / m) >= kWant) break;
+      items = c.samples * ((c.groups + m - 1) / m);
+      if (items >= kWant) break;
     }
-    if (!take) continue;
+    if (!take || (block == 64 && items < kWant)) continue;
     y.whole = 1;
-    y.per_chunk = take;
-    y.chunks = (c.groups + take - 1) / take;
+    y.per_chunk = int(take);
+    y.chunks = int((c.groups + take - 1) / take);
     set_lanes(y, take * cg);
     y.held = int64_t(y.slices) * kHeldFew >= longest ? kHeldFew : most;
     return y;
@@ -77,11 +83,11 @@ inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backwa
   y.block = kTileBlock;
   const int64_t reach = int64_t(kTileBlock) * y.vec;
   if (cg > reach) {
-    y.split = (cg + reach - 1) / reach;
-    y.part = ((cg + y.split - 1) / y.split + y.vec - 1) / y.vec * y.vec;
-    y.split = (cg + y.part - 1) / y.part;
+    const int64_t parts = (cg + reach - 1) / reach;
+    y.part = int(((cg + parts - 1) / parts + y.vec - 1) / y.vec * y.vec);
+    y.split = int((cg + y.part - 1) / y.part);
     y.per_chunk = 1;
-    y.chunks = c.groups * y.split;
+    y.chunks = int(c.groups * y.split);
     set_lanes(y, y.part);
   } else {
     // the number of chunks that leaves the fewest threads idle, the smallest unless another
@@ -94,17 +100,18 @@ inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backwa
       const double busy = double(y.slices) * double(c.width) / double((c.groups + m - 1) / m) / y.vec / kTileBlock;
       if (busy > best * 1.03) {
         best = busy;
-        y.per_chunk = m;
+        y.per_chunk = int(m);
       }
     }
-    y.chunks = (c.groups + y.per_chunk - 1) / y.per_chunk;
+    y.chunks = int((c.groups + y.per_chunk - 1) / y.per_chunk);
     set_lanes(y, y.per_chunk * cg);
   }
   // tiles of four turns at least, so many that they fill the device some times over
   constexpr int64_t kTileBlocks = 2048;
-  y.tile_rows = std::max<int64_t>((c.rows * y.chunks + kTileBlocks - 1) / kTileBlocks, 4 * y.slices);
-  y.tile_rows = std::min((y.tile_rows + y.slices - 1) / y.slices * y.slices, std::max<int64_t>(c.rows, 1));
-  y.tiles = (c.rows + y.tile_rows - 1) / y.tile_rows;
+  int64_t rows = std::max<int64_t>((c.rows * y.chunks + kTileBlocks - 1) / kTileBlocks, 4 * y.slices);
+  rows = std::max<int64_t>(std::min((rows + y.slices - 1) / y.slices * y.slices, c.rows), 1);
+  y.tile_rows = int(rows);
+  y.tiles = int((c.rows + rows - 1) / rows);
   return y;
 }
 

@@ -20,56 +20,91 @@
 // groups.  A sample that the registers of one workgroup hold is read once, in one launch.
 // Longer ones are cut into tiles of rows whose sums a second launch joins and a third applies,
 // reading the rows again.
+#include <type_traits>
+
 #include "group_layout.hpp"
 #include "vec.hpp"
 
 namespace cgtp {
 namespace {
 
-// exp(x) to some 2 ulp: 2^t with t = x log2(e) rounded, times 1 + what the rounding left out.
-__device__ inline float exp_f32(float x) {
+// exp(x): 2^t with t = x log2(e) rounded, and in fp32 times 1 + what the rounding left out
+// (some 2 ulp; in 16 bits an error of |x| 2^-24 of it is nothing).
+template <bool Exact>
+__device__ inline float exp_of(float x) {
   constexpr float kLog2e = 1.44269504f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
-  const float t = x * kLog2e;
+  const float t = x * kLog2e, p = __builtin_amdgcn_exp2f(t);
+  if constexpr (!Exact) return p;
   const float rest = fmaf(x, kRest, fmaf(x, kLog2e, -t));
-  const float p = __builtin_amdgcn_exp2f(t);
   // where p is 0 or infinity (or x is) the rest may be NaN and has no say
   return p > 0 && p < __builtin_inff() ? fmaf(p, rest * kLn2, p) : p;
 }
+// (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2).  Of x = |z| / sqrt 2, 1 - erf(x) = exp(-x^2) times a
+// polynomial in 1 / (1 + 0.3275911 x) to 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26), some 2.5 of fp32's roundings of 1.
+template <bool Exact>
+__device__ inline float normal_cdf(float z, float& density) {
+  density = exp_of<Exact>(-0.5f * z * z);
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.707106781f, 1.0f));
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  q *= 0.5f * t * density;
+  return z < 0 ? q : 1.0f - q;
+}
 
-__device__ inline float act_value(float z, Act act) {
-  if (act == Act::silu) return z * __builtin_amdgcn_rcpf(1.0f + exp_f32(-z));
-  if (act == Act::gelu) return z * (0.5f + 0.5f * erff(z * 0.707106781f));
+template <Act A, bool Exact>
+__device__ inline float act_value(float z) {
+  if constexpr (A == Act::silu) return z * __builtin_amdgcn_rcpf(1.0f + exp_of<Exact>(-z));
+  if constexpr (A == Act::gelu) {
+    float density;
+    return z * normal_cdf<Exact>(z, density);
+  }
   return z;
 }
-__device__ inline float act_slope(float z, Act act) {
-  if (act == Act::silu) {
-    const float p = __builtin_amdgcn_rcpf(1.0f + exp_f32(-z));
-    return p + z * p * (1.0f - p);
+template <Act A, bool Exact>
+__device__ inline float act_slope(float z) {
+  if constexpr (A == Act::silu) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + exp_of<Exact>(-z));
+    return fmaf(z * p, 1.0f - p, p);
   }
-  if (act == Act::gelu)
-    return 0.5f + 0.5f * erff(z * 0.707106781f) + z * 0.398942280f * exp_f32(-0.5f * z * z);
+  if constexpr (A == Act::gelu) {
+    float density;
+    const float p = normal_cdf<Exact>(z, density);
+    return fmaf(z * 0.398942280f, density, p);
+  }
   return 1.0f;
 }
+// f with the activation as a constant: one branch for what f does, the same for all lanes.
+template <typename F>
+__device__ inline void with_act(Act act, F&& f) {
+  if (act == Act::silu)
+    f(std::integral_constant<Act, Act::silu>{});
+  else if (act == Act::gelu)
+    f(std::integral_constant<Act, Act::gelu>{});
+  else
+    f(std::integral_constant<Act, Act::none>{});
+}
 
-__device__ inline int64_t sample_begin(const GroupCall& c, int64_t s) {
-  if (!c.offsets) return c.rows / c.samples * s;
-  return min(max(int64_t(c.offsets[s]), int64_t(0)), c.rows);
+__device__ inline int sample_begin(const GroupCall& c, const GroupLayout& y, int64_t s) {
+  if (!c.offsets) return int(s * y.equal);
+  return min(max(c.offsets[s], 0), int(c.rows));
 }
 // Never before the sample's begin, nor past the rows, whatever the offsets hold.
-__device__ inline int64_t sample_end(const GroupCall& c, int64_t s, int64_t begin) {
-  if (!c.offsets) return c.rows / c.samples * (s + 1);
-  return min(max(int64_t(c.offsets[s + 1]), begin), c.rows);
+__device__ inline int sample_end(const GroupCall& c, const GroupLayout& y, int64_t s, int begin) {
+  if (!c.offsets) return int((s + 1) * y.equal);
+  return min(max(c.offsets[s + 1], begin), int(c.rows));
 }
 // The first sample that ends behind `row` (samples, if none does): 64 lanes probe at once.
-__device__ inline int64_t sample_behind(const GroupCall& c, int64_t row) {
-  if (!c.offsets) return c.samples ? row / (c.rows / c.samples) : 0;
-  const int lane = threadIdx.x % kWave;
+__device__ inline int64_t sample_behind(const GroupCall& c, const GroupLayout& y, int row) {
+  if (!c.offsets) return y.equal ? row / y.equal : 0;
+  const int64_t lane = threadIdx.x % kWave;
   int64_t lo = 0, n = c.samples;
   while (n > 0) {
     const int64_t step = (n + kWave - 1) / kWave;
     const int64_t at = min((lane + 1) * step, n) - 1;
-    // as many lanes as the last probe that lies inside makes
-    const bool before = lane * step < n && int64_t(c.offsets[lo + at + 1]) <= row;
+    const bool before = lane * step < n && c.offsets[lo + at + 1] <= row;
     const int64_t passed = min(__popcll(__ballot(before)) * step, n);
     lo += passed;
     n = step == 1 ? 0 : min(step - 1, n - passed);   // the probed one itself ends behind
@@ -79,26 +114,24 @@ __device__ inline int64_t sample_behind(const GroupCall& c, int64_t row) {
 
 // The columns of a chunk, and the groups (or the part of one) in it.
 struct Chunk {
-  int64_t c0;        // first column
-  int32_t cw;        // columns
-  int64_t u0;        // first unit: a group, or a part of one
-  int32_t nu, uw;    // units, and the columns of each
+  int c0, cw;        // first column, columns
+  int u0;            // first unit: a group, or a part of one
+  int nu, uw;        // units, and the columns of each
 };
-__device__ inline Chunk chunk_of(const GroupCall& c, const GroupLayout& y, int64_t k) {
-  const int64_t cg = c.width / c.groups;
+__device__ inline Chunk chunk_of(const GroupCall& c, const GroupLayout& y, int k) {
   Chunk q;
   if (y.split == 1) {
     q.u0 = k * y.per_chunk;
-    q.nu = int(min(y.per_chunk, c.groups - q.u0));
-    q.uw = int(cg);
-    q.c0 = q.u0 * cg;
+    q.nu = min(y.per_chunk, int(c.groups) - q.u0);
+    q.uw = y.per_group;
+    q.c0 = q.u0 * y.per_group;
     q.cw = q.nu * q.uw;
   } else {
-    const int64_t in = k % y.split * y.part;
+    const int g = k / y.split, in = (k - g * y.split) * y.part;
     q.u0 = k;
     q.nu = 1;
-    q.c0 = k / y.split * cg + in;
-    q.cw = q.uw = int(min(y.part, cg - in));
+    q.c0 = g * y.per_group + in;
+    q.cw = q.uw = min(y.part, y.per_group - in);
   }
   return q;
 }
@@ -109,7 +142,7 @@ template <int V>
 struct Place {
   int slice;
   bool in;           // has a place
-  int64_t at;        // first column in the row
+  int at;            // first column in the row
   int rel;           // the same in the chunk (may be negative)
   int own, end;
   __device__ Place(const Chunk& q, const GroupLayout& y) {
@@ -118,7 +151,7 @@ struct Place {
     const int start = lane * V;
     in = slice < y.slices && start < q.cw;
     rel = min(start, q.cw - V);
-    if (q.c0 + rel < 0) rel = -int(q.c0);
+    if (q.c0 + rel < 0) rel = -q.c0;
     at = q.c0 + rel;
     own = start - rel;
     end = min(V, q.cw - rel);
@@ -178,11 +211,11 @@ struct Entries {
   int stride;     // entries of a slice
   int per_unit;   // entries of a slice and unit
   float weight;   // values of an entry per row
-  int64_t n;      // rows of the sample here
+  int n;          // rows of the sample here
   float each;     // of which each slice has so many, and the first `more` one more
   int more, slices;
   bool merged;
-  __device__ Entries(float* lds, const Chunk& q, const GroupLayout& y, int v, int64_t rows)
+  __device__ Entries(float* lds, const Chunk& q, const GroupLayout& y, int v, int rows)
       : n(rows), slices(y.slices), merged(q.uw % v == 0) {
     each = float(uint32_t(rows) / uint32_t(slices));
     more = int(uint32_t(rows) % uint32_t(slices));
@@ -190,7 +223,7 @@ struct Entries {
     per_unit = merged ? q.uw / v : q.uw;
     weight = merged ? float(v) : 1.0f;
     mean = lds;
-    m2 = lds + int64_t(stride) * slices;
+    m2 = lds + stride * slices;
   }
   __device__ float rows_of(int slice) const { return slice < more ? each + 1 : each; }
 
@@ -225,23 +258,40 @@ struct Entries {
         }
     }
   }
-  // One wave's: the mean and M2 of unit u, in every lane.
+  // The mean and M2 of unit u, in each of the G neighbouring lanes that join its entries.
+  template <int G>
   __device__ void join(int u, float& mean_out, float& m2_out) const {
-    const int total = slices * per_unit, lane = threadIdx.x % kWave;
+    const int total = slices * per_unit, lane = threadIdx.x % G;
     const float first = mean[u * per_unit];   // slice 0 has a row
     float s = 0, v = 0;
-    for (int e = lane; e < total; e += kWave) {
+    for (int e = lane; e < total; e += G) {
       const int slice = e / per_unit, at = slice * stride + u * per_unit + e - slice * per_unit;
       s += rows_of(slice) * (mean[at] - first);
     }
-    const float all = first + wave_sum(s) / (float(n) * float(per_unit));
-    for (int e = lane; e < total; e += kWave) {
+    const float all = first + lanes_sum<G>(s) / (float(n) * float(per_unit));
+    for (int e = lane; e < total; e += G) {
       const int slice = e / per_unit, at = slice * stride + u * per_unit + e - slice * per_unit;
       const float d = mean[at] - all;
       v += m2[at] + rows_of(slice) * weight * d * d;
     }
     mean_out = all;
-    m2_out = wave_sum(v);
+    m2_out = lanes_sum<G>(v);
+  }
+  // f(unit, mean, M2, whether the lane is to write) for every unit, by the whole workgroup of B.
+  template <int B, typename F>
+  __device__ void for_units(const Chunk& q, F&& f) const {
+    float mu, ss;
+    if (q.nu > B / kWave) {
+      for (int u = threadIdx.x / 16; u < q.nu; u += B / 16) {
+        join<16>(u, mu, ss);
+        f(u, mu, ss, threadIdx.x % 16 == 0);
+      }
+    } else {
+      for (int u = threadIdx.x / kWave; u < q.nu; u += B / kWave) {
+        join<kWave>(u, mu, ss);
+        f(u, mu, ss, threadIdx.x % kWave == 0);
+      }
+    }
   }
 };
 
@@ -268,14 +318,10 @@ template <typename T, int V>
 __device__ inline void activated(const Vec<T, V>& r, const Scales<V>& k, Act act, float (&z)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) z[j] = fmaf(to_f32(r.v[j]) - k.mean[j], k.scale[j], k.shift[j]);
-  // the type of activation is the same for all: one branch for the vector
-  if (act == Act::silu) {
+  with_act(act, [&](auto a) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) z[j] = act_value(z[j], Act::silu);
-  } else if (act == Act::gelu) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) z[j] = act_value(z[j], Act::gelu);
-  }
+    for (int j = 0; j < V; ++j) z[j] = act_value<a(), sizeof(T) == 4>(z[j]);
+  });
 }
 
 // What the backward needs at a place: h = (x - mean) rstd, d = g act'(h w + b).
@@ -291,28 +337,33 @@ __device__ inline void slopes(const Vec<T, V>& x, const Vec<T, V>& g, const Slop
     h[j] = (to_f32(x.v[j]) - k.mean[j]) * k.rstd[j];
     d[j] = to_f32(g.v[j]);
   }
-  if (act == Act::silu) {
+  with_act(act, [&](auto a) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) d[j] *= act_slope(fmaf(h[j], k.w[j], k.b[j]), Act::silu);
-  } else if (act == Act::gelu) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] *= act_slope(fmaf(h[j], k.w[j], k.b[j]), Act::gelu);
-  }
+    for (int j = 0; j < V; ++j) d[j] *= act_slope<a(), sizeof(T) == 4>(fmaf(h[j], k.w[j], k.b[j]));
+  });
 }
 
 // The statistics of a place's columns, of sample s.
 template <int V>
-__device__ inline void place_stats(const GroupCall& c, const Place<V>& p, const float* stats, int64_t s,
+__device__ inline void place_stats(const GroupCall& c, const int (&group)[V], const float* stats, int64_t s,
                                    float (&mean)[V], float (&rstd)[V]) {
-  const int64_t cg = c.width / c.groups;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    mean[j] = rstd[j] = 0;
-    if (p.in && p.has(j)) {
-      const int64_t at = s * c.groups + (p.at + j) / cg;
-      mean[j] = stats[at];
-      rstd[j] = stats[c.samples * c.groups + at];
-    }
+    const float* at = stats + s * c.groups + group[j];
+    mean[j] = at[0];
+    rstd[j] = at[c.samples * c.groups];
+  }
+}
+// The groups of a place's columns (the first group for columns that it has not).
+template <int V>
+__device__ inline void place_groups(const GroupLayout& y, const Place<V>& p, int (&group)[V]) {
+  if (y.per_group % V == 0 && y.part % V == 0) {   // places do not straddle groups
+    const int g = p.in ? p.at / y.per_group : 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) group[j] = g;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) group[j] = p.in && p.has(j) ? (p.at + j) / y.per_group : 0;
   }
 }
 
@@ -365,20 +416,20 @@ __device__ inline int column_sums(const Place<V>& p, const Chunk& q, int slices,
 // ---- a whole sample in one workgroup -----------------------------------------------
 
 // Rows outside every sample lie before the first of them and behind the last.
-__device__ inline void outside(const GroupCall& c, int64_t& first, int64_t& last) {
-  first = last = c.rows;
+__device__ inline void outside(const GroupCall& c, const GroupLayout& y, int& first, int& last) {
+  first = last = int(c.rows);
   if (c.samples == 0) return;
-  first = sample_begin(c, 0);
-  last = max(first, sample_end(c, c.samples - 1, sample_begin(c, c.samples - 1)));
+  first = sample_begin(c, y, 0);
+  last = max(first, sample_end(c, y, c.samples - 1, sample_begin(c, y, c.samples - 1)));
 }
 // Zeros in them, by the workgroups behind the samples'.
 constexpr int kZeroBlocks = 64;
 template <typename T, int V>
 __device__ inline void zero_outside(const GroupCall& c, const GroupLayout& y, int64_t block) {
-  int64_t first, last;
-  outside(c, first, last);
+  int first, last;
+  outside(c, y, first, last);
   const float none[V] = {};
-  for (int64_t k = 0; k < y.chunks; ++k) {
+  for (int k = 0; k < y.chunks; ++k) {
     const Place<V> p(chunk_of(c, y, k), y);
     if (!p.in) continue;
     for (int64_t i = block * y.slices + p.slice; i < first + c.rows - last; i += int64_t(y.slices) * kZeroBlocks)
@@ -390,7 +441,7 @@ __device__ inline void zero_outside(const GroupCall& c, const GroupLayout& y, in
 struct Rows {
   int mine, most;
   template <int V>
-  __device__ Rows(const Place<V>& p, int slices, int64_t rows) {
+  __device__ Rows(const Place<V>& p, int slices, int rows) {
     const uint32_t n = uint32_t(rows), each = n / uint32_t(slices), more = n - each * uint32_t(slices);
     mine = p.in ? int(each + (uint32_t(p.slice) < more)) : 0;
     most = int(each + (more > 0));
@@ -403,6 +454,54 @@ __device__ inline T afresh(T v) {
   asm volatile("" : "+v"(v));
   return v;
 }
+// Rows that a thread reads at once, in tiles; a workgroup that holds rows has few registers left.
+constexpr int kInFlight = 8, kBeside = 2;
+
+// Rows lo + slice, + slices ... of [lo, hi): f(vector, whether it is the first) for each.
+template <typename T, int V, int Q, typename F>
+__device__ inline void for_rows(const Place<V>& p, int slices, const T* x, int64_t ld, int lo, int hi, F&& f) {
+  const int64_t step = int64_t(slices) * ld;
+  int left = Rows(p, slices, hi - lo).mine;
+  const T* at = x + int64_t(lo + p.slice) * ld + p.at;
+  bool first = true;
+  while (left > 0) {
+    Vec<T, V> v[Q];
+#pragma unroll
+    for (int i = 0; i < Q; ++i) v[i] = load_vec<false, T, V>(at + (i < left ? i : left - 1) * step);
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+      if (i < left) {
+        f(v[i], first);
+        first = false;
+      }
+    at += Q * step;
+    left -= Q;
+  }
+}
+
+// Rows of x and of grad_out together.
+template <typename T, int V, int Q, typename F>
+__device__ inline void for_row_pairs(const GroupCall& c, const Place<V>& p, int slices, int lo, int hi, F&& f) {
+  const int64_t sx = int64_t(slices) * c.ld_x, sg = int64_t(slices) * c.ld_g;
+  int left = Rows(p, slices, hi - lo).mine;
+  const T* x = static_cast<const T*>(c.x) + int64_t(lo + p.slice) * c.ld_x + p.at;
+  const T* g = static_cast<const T*>(c.grad_out) + int64_t(lo + p.slice) * c.ld_g + p.at;
+  while (left > 0) {
+    Vec<T, V> vx[Q], vg[Q];
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      vx[i] = load_vec<false, T, V>(x + (i < left ? i : left - 1) * sx);
+      vg[i] = load_vec<false, T, V>(g + (i < left ? i : left - 1) * sg);
+    }
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+      if (i < left) f(vx[i], vg[i]);
+    x += Q * sx;
+    g += Q * sg;
+    left -= Q;
+  }
+}
+
 // A row's vector as it is held: packed, so that the compiler keeps neither its elements nor
 // their values in 32 bits until they are used.
 template <int Bytes>
@@ -427,6 +526,15 @@ template <typename T, int V>
 __device__ inline Vec<T, V> unpack(const Held<T, V>& h) {
   return __builtin_bit_cast(Vec<T, V>, h);
 }
+// An item's sample and chunk.
+__device__ inline int64_t sample_of(int64_t item, int chunks, int& chunk) {
+  const int64_t s = item >> 32 ? item / chunks : int64_t(uint32_t(item) / uint32_t(chunks));
+  chunk = int(item - s * chunks);
+  return s;
+}
+
+// N rows of a thread are held from the sums to the output; a sample of more has the others read
+// again, while the caches may still hold them.
 template <typename T, int V, int B, int N>
 __global__ __launch_bounds__(B) void group_fwd_kernel(GroupCall c, GroupLayout y, int64_t items) {
   __shared__ __align__(16) float lds[2 * B * V];
@@ -435,85 +543,92 @@ __global__ __launch_bounds__(B) void group_fwd_kernel(GroupCall c, GroupLayout y
     return;
   }
   for (int64_t item = blockIdx.x; item < c.samples * y.chunks; item += items) {
-    const int64_t s = item / y.chunks;
-    const Chunk q = chunk_of(c, y, item - s * y.chunks);
+    int chunk;
+    const int64_t s = sample_of(item, y.chunks, chunk);
+    const Chunk q = chunk_of(c, y, chunk);
     const Place<V> p(q, y);
-    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin), rows = end - begin;
+    const int begin = sample_begin(c, y, s), end = sample_end(c, y, s, begin), rows = end - begin;
     const Rows own(p, y.slices, rows);
-    const T* x = static_cast<const T*>(c.x) + (begin + p.slice) * c.ld_x + p.at;
+    const T* x = static_cast<const T*>(c.x) + int64_t(begin + p.slice) * c.ld_x + p.at;
     const int64_t step = int64_t(y.slices) * c.ld_x;
-    Held<T, V> held[N];
+    const int rest = begin + N * y.slices;   // the first row that is not held
     Shifted<V> sum;
     sum.clear();
-    auto read = [&](int first) {
-      const T* at = x + first * step;
-      const int left = afresh(own.mine - first);
+    auto add = [&](const Vec<T, V>& row, bool first) {
+      float v[V];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (i < left) held[i] = hold<T, V>(at);
-        at = afresh(at + step);
+      for (int j = 0; j < V; ++j) v[j] = to_f32(row.v[j]);
+      if (first) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum.k[j] = v[j];
       }
+      sum.add(v);
     };
-    for (int first = 0; first < own.most; first += N) {
-      read(first);
-      const int left = afresh(own.mine - first);
+    if (own.most > N) for_rows<T, V, kBeside>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, rest, end, add);
+    Held<T, V> held[N];
+    const T* at = x;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < left) {
-          const Vec<T, V> row = unpack<T, V>(held[i]);
-          float v[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) v[j] = to_f32(row.v[j]);
-          if (i == 0 && first == 0) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum.k[j] = v[j];
-          }
-          sum.add(v);
-        }
+    for (int i = 0; i < N; ++i) {
+      if (i < own.mine) held[i] = hold<T, V>(at);
+      at = afresh(at + step);
     }
-    const Entries e(lds, q, y, V, rows);
-    e.put(p, sum);
+    const int left = afresh(own.mine);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < left) add(unpack<T, V>(held[i]), i == 0 && left <= N);
     float w[V], b[V];
     place_weights<T>(p, c.weight, c.weight_f32, 1.0f, w);
     place_weights<T>(p, c.bias, c.weight_f32, 0.0f, b);
+    const Entries e(lds, q, y, V, rows);
+    e.put(p, sum);
     __syncthreads();
-    for (int u = threadIdx.x / kWave; u < q.nu; u += B / kWave) {
-      float mean = 0, m2 = 0;
-      if (rows > 0) e.join(u, mean, m2);
-      const float rstd = rstd_of(m2, float(rows) * float(q.uw), c.eps);
-      if (threadIdx.x % kWave == 0) {
-        e.mean[u * e.per_unit] = mean;   // in the place of an entry that only this wave reads
-        e.m2[u * e.per_unit] = rstd;
-        if (c.stats) {
-          c.stats[s * c.groups + q.u0 + u] = mean;
-          c.stats[(c.samples + s) * c.groups + q.u0 + u] = rstd;
-        }
+    if (rows == 0) {
+      for (int u = threadIdx.x; c.stats && u < q.nu; u += B) {
+        c.stats[s * c.groups + q.u0 + u] = 0;
+        c.stats[(c.samples + s) * c.groups + q.u0 + u] = rstd_of(0, 0, c.eps);
       }
+      continue;
     }
+    e.template for_units<B>(q, [&](int u, float mean, float m2, bool first) {
+      if (!first) return;
+      const float rstd = rstd_of(m2, float(rows) * float(q.uw), c.eps);
+      e.mean[u * e.per_unit] = mean;   // in the place of an entry that only these lanes read
+      e.m2[u * e.per_unit] = rstd;
+      if (c.stats) {
+        c.stats[s * c.groups + q.u0 + u] = mean;
+        c.stats[(c.samples + s) * c.groups + q.u0 + u] = rstd;
+      }
+    });
     __syncthreads();
+    int group[V];
+    place_groups(y, p, group);
     Scales<V> k;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int u = p.in && p.has(j) ? (p.rel + j) / q.uw : 0;
+      const int u = p.in ? max(group[j] - q.u0, 0) : 0;
       k.mean[j] = e.mean[u * e.per_unit];
       k.scale[j] = e.m2[u * e.per_unit] * w[j];
       k.shift[j] = b[j];
     }
-    T* out = static_cast<T*>(c.y) + (begin + p.slice) * c.ld_y;
+    T* out = static_cast<T*>(c.y) + int64_t(begin + p.slice) * c.ld_y;
     const int64_t step_y = int64_t(y.slices) * c.ld_y;
-    for (int first = 0; first < own.most; first += N) {
-      if (own.most > N) read(first);   // else they are held
-      const int left = afresh(own.mine - first);
+    const int again = afresh(own.mine);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (i < left) {
-          float z[V];
-          activated(unpack<T, V>(held[i]), k, c.act, z);
-          store_own<false>(p, out, z);
-        }
-        out = afresh(out + step_y);
+    for (int i = 0; i < N; ++i) {
+      if (i < again) {
+        float z[V];
+        activated(unpack<T, V>(held[i]), k, c.act, z);
+        store_own<false>(p, out, z);
       }
+      out = afresh(out + step_y);
     }
+    if (own.most > N)
+      for_rows<T, V, kBeside>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, rest, end, [&](const Vec<T, V>& row, bool) {
+        float z[V];
+        activated(row, k, c.act, z);
+        store_own<false>(p, out, z);
+        out += step_y;
+      });
     __syncthreads();   // before the next sample's entries
   }
 }
@@ -526,48 +641,48 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
     return;
   }
   for (int64_t item = blockIdx.x; item < c.samples * y.chunks; item += items) {
-    const int64_t s = item / y.chunks;
-    const Chunk q = chunk_of(c, y, item - s * y.chunks);
+    int chunk;
+    const int64_t s = sample_of(item, y.chunks, chunk);
+    const Chunk q = chunk_of(c, y, chunk);
     const Place<V> p(q, y);
-    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin), rows = end - begin;
+    const int begin = sample_begin(c, y, s), end = sample_end(c, y, s, begin), rows = end - begin;
     const Rows own(p, y.slices, rows);
-    const T* x = static_cast<const T*>(c.x) + (begin + p.slice) * c.ld_x + p.at;
-    const T* g = static_cast<const T*>(c.grad_out) + (begin + p.slice) * c.ld_g + p.at;
+    const int rest = begin + N * y.slices;
+    const T* x = static_cast<const T*>(c.x) + int64_t(begin + p.slice) * c.ld_x + p.at;
+    const T* g = static_cast<const T*>(c.grad_out) + int64_t(begin + p.slice) * c.ld_g + p.at;
     const int64_t step_x = int64_t(y.slices) * c.ld_x, step_g = int64_t(y.slices) * c.ld_g;
-    Held<T, V> hx[N], hg[N];
+    int group[V];
+    place_groups(y, p, group);
     Slopes<V> k;
     place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
     place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
-    place_stats(c, p, c.stats, s, k.mean, k.rstd);
+    place_stats(c, group, c.stats, s, k.mean, k.rstd);
     float sd[V] = {}, sh[V] = {};
-    auto read = [&](int first) {
-      const T *at_x = x + first * step_x, *at_g = g + first * step_g;
-      const int left = afresh(own.mine - first);
+    auto add = [&](const Vec<T, V>& vx, const Vec<T, V>& vg) {
+      float h[V], d[V];
+      slopes(vx, vg, k, c.act, h, d);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (i < left) {
-          hx[i] = hold<T, V>(at_x);
-          hg[i] = hold<T, V>(at_g);
-        }
-        at_x = afresh(at_x + step_x);
-        at_g = afresh(at_g + step_g);
+      for (int j = 0; j < V; ++j) {
+        sd[j] += d[j];
+        sh[j] += d[j] * h[j];
       }
     };
-    for (int first = 0; first < own.most; first += N) {
-      read(first);
-      const int left = afresh(own.mine - first);
+    if (own.most > N) for_row_pairs<T, V, kBeside>(c, p, y.slices, rest, end, add);
+    Held<T, V> hx[N], hg[N];
+    const T *at_x = x, *at_g = g;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < left) {
-          float h[V], d[V];
-          slopes(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]), k, c.act, h, d);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            sd[j] += d[j];
-            sh[j] += d[j] * h[j];
-          }
-        }
+    for (int i = 0; i < N; ++i) {
+      if (i < own.mine) {
+        hx[i] = hold<T, V>(at_x);
+        hg[i] = hold<T, V>(at_g);
+      }
+      at_x = afresh(at_x + step_x);
+      at_g = afresh(at_g + step_g);
     }
+    const int left = afresh(own.mine);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < left) add(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]));
     const int n = column_sums(p, q, y.slices, sd, sh, lds);
     // the columns' sums, for the weights' gradients
     for (int e = threadIdx.x; e < q.cw; e += B) {
@@ -579,10 +694,10 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
         if (c.grad_weight) store_either<T>(c.grad_weight, c.weight_f32, q.c0 + e, lds[n + e]);
       }
     }
-    if (c.y) {
+    if (c.y && rows > 0) {
       __syncthreads();
       // a group's means of a and of a h
-      const float inv = rows > 0 ? 1.0f / (float(rows) * float(q.uw)) : 0.0f;
+      const float inv = 1.0f / (float(rows) * float(q.uw));
       for (int u = threadIdx.x / kWave; u < q.nu; u += B / kWave) {
         float a = 0, b = 0;
         for (int e = threadIdx.x % kWave; e < q.uw; e += kWave) {
@@ -602,27 +717,30 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
       float ma[V], mh[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int u = p.in && p.has(j) ? (p.rel + j) / q.uw : 0;
+        const int u = p.in ? max(group[j] - q.u0, 0) : 0;
         ma[j] = lds[u * q.uw];
         mh[j] = lds[n + u * q.uw];
       }
-      T* out = static_cast<T*>(c.y) + (begin + p.slice) * c.ld_y;
+      T* out = static_cast<T*>(c.y) + int64_t(begin + p.slice) * c.ld_y;
       const int64_t step_y = int64_t(y.slices) * c.ld_y;
-      for (int first = 0; first < own.most; first += N) {
-        if (own.most > N) read(first);
-        const int left = afresh(own.mine - first);
+      auto apply = [&](const Vec<T, V>& vx, const Vec<T, V>& vg) {
+        float h[V], d[V];
+        slopes(vx, vg, k, c.act, h, d);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (i < left) {
-            float h[V], d[V];
-            slopes(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]), k, c.act, h, d);
+        for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
+        store_own<false>(p, out, d);
+      };
+      const int again = afresh(own.mine);
 #pragma unroll
-            for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
-            store_own<false>(p, out, d);
-          }
-          out = afresh(out + step_y);
-        }
+      for (int i = 0; i < N; ++i) {
+        if (i < again) apply(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]));
+        out = afresh(out + step_y);
       }
+      if (own.most > N)
+        for_row_pairs<T, V, kBeside>(c, p, y.slices, rest, end, [&](const Vec<T, V>& vx, const Vec<T, V>& vg) {
+          apply(vx, vg);
+          out += step_y;
+        });
     }
     __syncthreads();   // before the next sample's sums
   }
@@ -630,53 +748,46 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
 
 // ---- tiles -------------------------------------------------------------------------
 
-// Walks through the workgroup's tile: f(sample, first row, past the last, piece).
+// A workgroup's tile and chunk.  Workgroups go to the eight dies (XCDs) by turns, and each has an
+// L2 of its own: the second reading's workgroup of a tile has the first's place among eight.  It
+// comes last first, as what was read last is what the caches still hold.
+struct Tile {
+  int tile, chunk, r0, r1;
+  __device__ Tile(const GroupCall& c, const GroupLayout& y, int block) {
+    tile = int(uint32_t(block) / uint32_t(y.chunks));
+    chunk = block - tile * y.chunks;
+    r0 = int(int64_t(tile) * y.tile_rows);
+    r1 = int(min(int64_t(tile + 1) * y.tile_rows, c.rows));
+  }
+};
+constexpr int kDies = 8;
+__device__ inline int from_behind(int block, int blocks) {
+  return ((blocks + kDies - 1) / kDies - 1 - block / kDies) * kDies + block % kDies;
+}
+
+// Walks through a tile: f(sample, first row, past the last).
 template <typename F>
-__device__ inline void for_pieces(const GroupCall& c, int64_t tile, int64_t r0, int64_t r1, F&& f) {
-  for (int64_t s = sample_behind(c, r0); s < c.samples; ++s) {
-    const int64_t begin = sample_begin(c, s);
-    if (begin >= r1) break;
-    const int64_t lo = max(begin, r0), hi = min(sample_end(c, s, begin), r1);
-    if (lo < hi) f(s, lo, hi, tile + s);
+__device__ inline void for_pieces(const GroupCall& c, const GroupLayout& y, const Tile& t, F&& f) {
+  for (int64_t s = sample_behind(c, y, t.r0); s < c.samples; ++s) {
+    const int begin = sample_begin(c, y, s);
+    if (begin >= t.r1) break;
+    const int lo = max(begin, t.r0), hi = min(sample_end(c, y, s, begin), t.r1);
+    if (lo < hi) f(s, lo, hi);
   }
 }
 
-constexpr int kInFlight = 8;   // rows that a thread reads at once
-
-// Rows lo + slice, + slices ... of [lo, hi): f(vector, whether it is the first) for each.
-template <typename T, int V, typename F>
-__device__ inline void for_rows(const Place<V>& p, int slices, const T* x, int64_t ld, int64_t lo, int64_t hi, F&& f) {
-  const int64_t step = int64_t(slices) * ld;
-  int64_t left = (hi - lo - p.slice + slices - 1) / slices;
-  if (!p.in || hi - lo <= p.slice) return;
-  const T* at = x + (lo + p.slice) * ld + p.at;
-  bool first = true;
-  while (left > 0) {
-    Vec<T, V> v[kInFlight];
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) v[i] = load_vec<false, T, V>(at + (i < left ? i : left - 1) * step);
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i)
-      if (i < left) {
-        f(v[i], first);
-        first = false;
-      }
-    at += kInFlight * step;
-    left -= kInFlight;
-  }
-}
-
+// The pieces' means and M2, [units][tiles + samples][2].
 template <typename T, int V>
 __global__ __launch_bounds__(kTileBlock) void group_sum_kernel(GroupCall c, GroupLayout y, float* pieces) {
   __shared__ __align__(16) float lds[2 * kTileBlock * V];
-  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
-  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
+  const Tile t(c, y, blockIdx.x);
+  const Chunk q = chunk_of(c, y, t.chunk);
   const Place<V> p(q, y);
-  const int64_t units = c.groups * y.split;
-  for_pieces(c, tile, r0, r1, [&](int64_t, int64_t lo, int64_t hi, int64_t piece) {
+  const int64_t n_pieces = y.tiles + c.samples;
+  for_pieces(c, y, t, [&](int64_t s, int lo, int hi) {
     Shifted<V> sum;
     sum.clear();
-    for_rows<T, V>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, lo, hi, [&](const Vec<T, V>& r, bool first) {
+    for_rows<T, V, kInFlight>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, lo, hi, [&](const Vec<T, V>& r, bool first) {
       float v[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = to_f32(r.v[j]);
@@ -689,133 +800,134 @@ __global__ __launch_bounds__(kTileBlock) void group_sum_kernel(GroupCall c, Grou
     const Entries e(lds, q, y, V, hi - lo);
     e.put(p, sum);
     __syncthreads();
-    for (int u = threadIdx.x / kWave; u < q.nu; u += kTileBlock / kWave) {
-      float mean, m2;
-      e.join(u, mean, m2);
-      if (threadIdx.x % kWave == 0) {
-        float* at = pieces + (piece * units + q.u0 + u) * 2;
-        at[0] = mean;
-        at[1] = m2;
-      }
-    }
+    e.template for_units<kTileBlock>(q, [&](int u, float mean, float m2, bool first) {
+      if (!first) return;
+      float* at = pieces + ((q.u0 + u) * n_pieces + t.tile + s) * 2;
+      at[0] = mean;
+      at[1] = m2;
+    });
     __syncthreads();
   });
 }
 
-// A wave joins the pieces of one sample and group.
+// Sum over a group of G lanes, the workgroup's threads for G = kTileBlock.
+template <int G>
+__device__ inline float many_sum(float v, float* lds) {
+  v = wave_sum(v);
+  if constexpr (G > kWave) {
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < G / kWave; ++i) v += lds[i];
+  }
+  return v;
+}
+
+// G lanes join the pieces of one sample and group.
+template <int G>
 __global__ __launch_bounds__(kTileBlock) void group_join_kernel(GroupCall c, GroupLayout y, const float* pieces,
                                                                 float* stats) {
-  const int lane = threadIdx.x % kWave;
-  const int64_t waves = int64_t(gridDim.x) * (kTileBlock / kWave), cg = c.width / c.groups, units = c.groups * y.split;
-  for (int64_t k = int64_t(blockIdx.x) * (kTileBlock / kWave) + threadIdx.x / kWave; k < c.samples * c.groups; k += waves) {
-    const int64_t s = k / c.groups, g = k - s * c.groups;
-    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin);
+  __shared__ float lds[kTileBlock / kWave];
+  const int lane = threadIdx.x % G;
+  const int64_t n_pieces = y.tiles + c.samples;
+  for (int64_t k = int64_t(blockIdx.x) * (kTileBlock / G) + threadIdx.x / G; k < c.samples * c.groups;
+       k += int64_t(gridDim.x) * (kTileBlock / G)) {
+    int g;
+    const int64_t s = sample_of(k, int(c.groups), g);
+    const int begin = sample_begin(c, y, s), end = sample_end(c, y, s, begin);
     float mean = 0, m2 = 0;
     if (begin < end) {
-      const int64_t t0 = begin / y.tile_rows, n = ((end - 1) / y.tile_rows - t0 + 1) * y.split;
-      const float* at = pieces + ((t0 + s) * units + g * y.split) * 2;
-      const float first = at[0];
-      // piece e / split, part e % split: its mean, M2 and values
-      auto place = [&](int64_t e, float& values) {
-        const int64_t t = e / y.split, part = e - t * y.split, r = (t0 + t) * y.tile_rows;
-        const int64_t rows = min(r + y.tile_rows, end) - max(r, begin);
-        values = float(rows) * float(min(y.part, cg - part * y.part));
-        return at + (t * units + part) * 2;
-      };
-      float a = 0, b = 0, values;
-      for (int64_t e = lane; e < n; e += kWave) {
-        const float* q = place(e, values);
-        a += values * (q[0] - first);
+      const int t0 = begin / y.tile_rows, n = (end - 1) / y.tile_rows - t0 + 1;
+      const float values = float(end - begin) * float(y.per_group);
+      const float first = pieces[(int64_t(g) * y.split * n_pieces + t0 + s) * 2];
+      float a = 0, b = 0;
+      for (int part = 0; part < y.split; ++part) {
+        const float* at = pieces + ((int64_t(g) * y.split + part) * n_pieces + t0 + s) * 2;
+        const float columns = float(min(y.part, y.per_group - part * y.part));
+#pragma unroll 4
+        for (int t = lane; t < n; t += G) {
+          const int64_t r = int64_t(t0 + t) * y.tile_rows;
+          a += float(min(r + y.tile_rows, int64_t(end)) - max(r, int64_t(begin))) * columns * (at[2 * t] - first);
+        }
       }
-      mean = first + wave_sum(a) / (float(end - begin) * float(cg));
-      for (int64_t e = lane; e < n; e += kWave) {
-        const float* q = place(e, values);
-        const float d = q[0] - mean;
-        b += q[1] + values * d * d;
+      mean = first + many_sum<G>(a, lds) / values;
+      for (int part = 0; part < y.split; ++part) {
+        const float* at = pieces + ((int64_t(g) * y.split + part) * n_pieces + t0 + s) * 2;
+        const float columns = float(min(y.part, y.per_group - part * y.part));
+#pragma unroll 4
+        for (int t = lane; t < n; t += G) {
+          const int64_t r = int64_t(t0 + t) * y.tile_rows;
+          const float d = at[2 * t] - mean;
+          b += at[2 * t + 1] + float(min(r + y.tile_rows, int64_t(end)) - max(r, int64_t(begin))) * columns * d * d;
+        }
       }
-      m2 = wave_sum(b);
+      m2 = many_sum<G>(b, lds);
     }
     if (lane == 0) {
       stats[k] = mean;
-      stats[c.samples * c.groups + k] = rstd_of(m2, float(end - begin) * float(cg), c.eps);
+      stats[c.samples * c.groups + k] = rstd_of(m2, float(end - begin) * float(y.per_group), c.eps);
     }
   }
 }
 
 // Zeros of a tile's rows outside every sample.
 template <typename T, int V>
-__device__ inline void zero_tile(const GroupCall& c, const GroupLayout& y, const Place<V>& p, int64_t r0, int64_t r1) {
-  int64_t first, last;
-  outside(c, first, last);
-  zero_rows<T>(c, p, y.slices, r0, min(r1, first));
-  zero_rows<T>(c, p, y.slices, max(r0, last), r1);
+__device__ inline void zero_tile(const GroupCall& c, const GroupLayout& y, const Place<V>& p, const Tile& t) {
+  int first, last;
+  outside(c, y, first, last);
+  zero_rows<T>(c, p, y.slices, t.r0, min(t.r1, first));
+  zero_rows<T>(c, p, y.slices, max(t.r0, last), t.r1);
 }
 
 template <typename T, int V>
 __global__ __launch_bounds__(kTileBlock) void group_apply_kernel(GroupCall c, GroupLayout y, const float* stats) {
-  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
-  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
+  const int block = from_behind(blockIdx.x, y.tiles * y.chunks);
+  if (block >= y.tiles * y.chunks) return;
+  const Tile t(c, y, block);
+  const Chunk q = chunk_of(c, y, t.chunk);
   const Place<V> p(q, y);
+  int group[V];
+  place_groups(y, p, group);
   float w[V], b[V];
   place_weights<T>(p, c.weight, c.weight_f32, 1.0f, w);
   place_weights<T>(p, c.bias, c.weight_f32, 0.0f, b);
-  for_pieces(c, tile, r0, r1, [&](int64_t s, int64_t lo, int64_t hi, int64_t) {
+  for_pieces(c, y, t, [&](int64_t s, int lo, int hi) {
     Scales<V> k;
-    place_stats(c, p, stats, s, k.mean, k.scale);
+    place_stats(c, group, stats, s, k.mean, k.scale);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       k.scale[j] *= w[j];
       k.shift[j] = b[j];
     }
-    T* out = static_cast<T*>(c.y) + (lo + p.slice) * c.ld_y;
-    for_rows<T, V>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, lo, hi, [&](const Vec<T, V>& r, bool) {
+    T* out = static_cast<T*>(c.y) + int64_t(lo + p.slice) * c.ld_y;
+    for_rows<T, V, kInFlight>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, lo, hi, [&](const Vec<T, V>& r, bool) {
       float z[V];
       activated(r, k, c.act, z);
       store_own<false>(p, out, z);
       out += int64_t(y.slices) * c.ld_y;
     });
   });
-  if (c.zero_outside && c.offsets) zero_tile<T>(c, y, p, r0, r1);
+  if (c.zero_outside && c.offsets) zero_tile<T>(c, y, p, t);
 }
 
-// Rows of x and of grad_out together.
-template <typename T, int V, typename F>
-__device__ inline void for_row_pairs(const GroupCall& c, const Place<V>& p, int slices, int64_t lo, int64_t hi, F&& f) {
-  const int64_t sx = int64_t(slices) * c.ld_x, sg = int64_t(slices) * c.ld_g;
-  int64_t left = (hi - lo - p.slice + slices - 1) / slices;
-  if (!p.in || hi - lo <= p.slice) return;
-  const T* x = static_cast<const T*>(c.x) + (lo + p.slice) * c.ld_x + p.at;
-  const T* g = static_cast<const T*>(c.grad_out) + (lo + p.slice) * c.ld_g + p.at;
-  constexpr int kPairs = kInFlight / 2;
-  while (left > 0) {
-    Vec<T, V> vx[kPairs], vg[kPairs];
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      vx[i] = load_vec<false, T, V>(x + (i < left ? i : left - 1) * sx);
-      vg[i] = load_vec<false, T, V>(g + (i < left ? i : left - 1) * sg);
-    }
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      if (i < left) f(vx[i], vg[i]);
-    x += kPairs * sx;
-    g += kPairs * sg;
-    left -= kPairs;
-  }
-}
-
+// The pieces' sums of d and d h, [tiles + samples][2][width].
 template <typename T, int V>
 __global__ __launch_bounds__(kTileBlock) void group_bwd_sum_kernel(GroupCall c, GroupLayout y, float* pieces) {
   __shared__ __align__(16) float lds[2 * kTileBlock * V];
-  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
-  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
+  const Tile t(c, y, blockIdx.x);
+  const Chunk q = chunk_of(c, y, t.chunk);
   const Place<V> p(q, y);
+  int group[V];
+  place_groups(y, p, group);
   Slopes<V> k;
   place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
   place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
-  for_pieces(c, tile, r0, r1, [&](int64_t s, int64_t lo, int64_t hi, int64_t piece) {
-    place_stats(c, p, c.stats, s, k.mean, k.rstd);
+  for_pieces(c, y, t, [&](int64_t s, int lo, int hi) {
+    place_stats(c, group, c.stats, s, k.mean, k.rstd);
     float sd[V] = {}, sh[V] = {};
-    for_row_pairs<T, V>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
+    for_row_pairs<T, V, kInFlight / 2>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
       float h[V], d[V];
       slopes(x, g, k, c.act, h, d);
 #pragma unroll
@@ -825,7 +937,7 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_sum_kernel(GroupCall c, 
       }
     });
     const int n = column_sums(p, q, y.slices, sd, sh, lds);
-    float* at = pieces + piece * 2 * c.width + q.c0;
+    float* at = pieces + (t.tile + s) * 2 * c.width + q.c0;
     for (int e = threadIdx.x; e < q.cw; e += kTileBlock) {
       at[e] = lds[e];
       at[c.width + e] = lds[n + e];
@@ -834,43 +946,52 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_sum_kernel(GroupCall c, 
   });
 }
 
-// A workgroup joins the pieces of one sample and group: the columns' sums, and the means of
-// a and a h.
-template <typename T>
-__global__ __launch_bounds__(kTileBlock) void group_bwd_join_kernel(GroupCall c, GroupLayout y, const float* pieces,
-                                                                    float* join, float* coef) {
-  __shared__ float lds[2][kTileBlock];
-  const int64_t cg = c.width / c.groups;
-  const int lanes = int(min(cg, int64_t(kTileBlock))), subs = kTileBlock / lanes;
+// A workgroup of B joins the pieces of one sample and group: the columns' sums, and the means
+// of a and a h.
+template <typename T, int B>
+__global__ __launch_bounds__(B) void group_bwd_join_kernel(GroupCall c, GroupLayout y, const float* pieces, float* join,
+                                                           float* coef) {
+  __shared__ float lds[2][B];
+  const int cg = y.per_group, lanes = min(cg, B), subs = B / lanes;
   const int sub = int(threadIdx.x) / lanes, lane = int(threadIdx.x) - sub * lanes;
+  const int64_t ld = 2 * c.width;
   for (int64_t k = blockIdx.x; k < c.samples * c.groups; k += gridDim.x) {
-    const int64_t s = k / c.groups, g = k - s * c.groups;
-    const int64_t begin = sample_begin(c, s), end = sample_end(c, s, begin);
-    const int64_t t0 = begin / y.tile_rows, n = begin < end ? (end - 1) / y.tile_rows - t0 + 1 : 0;
+    int g;
+    const int64_t s = sample_of(k, int(c.groups), g);
+    const int begin = sample_begin(c, y, s), end = sample_end(c, y, s, begin);
+    const int t0 = begin / y.tile_rows, n = begin < end ? (end - 1) / y.tile_rows - t0 + 1 : 0;
     float sa = 0, sh = 0;
-    for (int64_t c0 = 0; c0 < cg; c0 += lanes) {
+    for (int c0 = 0; c0 < cg; c0 += lanes) {
       const bool in = sub < subs && c0 + lane < cg;
-      const int64_t e = g * cg + c0 + lane;
+      const int64_t e = int64_t(g) * cg + c0 + lane;
       float a = 0, b = 0;
       if (in) {
-        const float* at = pieces + (t0 + s) * 2 * c.width + e;
-#pragma unroll 4
-        for (int64_t t = sub; t < n; t += subs) {
-          a += at[t * 2 * c.width];
-          b += at[(t * 2 + 1) * c.width];
+        const float* at = pieces + (t0 + s) * ld + e;
+#pragma unroll 8
+        for (int t = sub; t < n; t += subs) {
+          a += at[t * ld];
+          b += at[t * ld + c.width];
         }
       }
       lds[0][threadIdx.x] = a;
       lds[1][threadIdx.x] = b;
       __syncthreads();
-      if (sub == 0 && in) {
-        for (int i = 1; i < subs; ++i) {
-          a += lds[0][i * lanes + lane];
-          b += lds[1][i * lanes + lane];
+      // a tree over the subs, of which there may be any number
+      for (int m = subs; m > 1;) {
+        const int half = (m + 1) / 2;
+        if (sub < m - half) {
+          lds[0][threadIdx.x] += lds[0][threadIdx.x + half * lanes];
+          lds[1][threadIdx.x] += lds[1][threadIdx.x + half * lanes];
         }
+        m = half;
+        __syncthreads();
+      }
+      if (sub == 0 && in) {
+        a = lds[0][lane];
+        b = lds[1][lane];
         if (join) {
-          join[s * 2 * c.width + e] = a;
-          join[(s * 2 + 1) * c.width + e] = b;
+          join[s * ld + e] = a;
+          join[s * ld + c.width + e] = b;
         } else {
           if (c.grad_bias) store_either<T>(c.grad_bias, c.weight_f32, e, a);
           if (c.grad_weight) store_either<T>(c.grad_weight, c.weight_f32, e, b);
@@ -890,61 +1011,29 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_join_kernel(GroupCall c,
     __syncthreads();
     if (threadIdx.x < 2) {
       float v = 0;
-      for (int i = 0; i < kTileBlock / kWave; ++i) v += lds[threadIdx.x][i];
+#pragma unroll
+      for (int i = 0; i < B / kWave; ++i) v += lds[threadIdx.x][i];
       coef[k * 2 + threadIdx.x] = begin < end ? v / (float(end - begin) * float(cg)) : 0.0f;
     }
     __syncthreads();
   }
 }
 
-template <typename T, int V>
-__global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c, GroupLayout y, const float* coef) {
-  const int64_t tile = blockIdx.x / y.chunks, r0 = tile * y.tile_rows, r1 = min(r0 + y.tile_rows, c.rows);
-  const Chunk q = chunk_of(c, y, blockIdx.x - tile * y.chunks);
-  const Place<V> p(q, y);
-  const int64_t cg = c.width / c.groups;
-  Slopes<V> k;
-  place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
-  place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
-  for_pieces(c, tile, r0, r1, [&](int64_t s, int64_t lo, int64_t hi, int64_t) {
-    place_stats(c, p, c.stats, s, k.mean, k.rstd);
-    float ma[V], mh[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      ma[j] = mh[j] = 0;
-      if (p.in && p.has(j)) {
-        const float* at = coef + (s * c.groups + (p.at + j) / cg) * 2;
-        ma[j] = at[0];
-        mh[j] = at[1];
-      }
-    }
-    T* out = static_cast<T*>(c.y) + (lo + p.slice) * c.ld_y;
-    for_row_pairs<T, V>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
-      float h[V], d[V];
-      slopes(x, g, k, c.act, h, d);
-#pragma unroll
-      for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
-      store_own<false>(p, out, d);
-      out += int64_t(y.slices) * c.ld_y;
-    });
-  });
-  if (c.offsets) zero_tile<T>(c, y, p, r0, r1);
-}
-
-// The weights' gradients from the samples' sums, 16 columns a workgroup, in a fixed order.
-constexpr int kParamBlock = 1024, kParamColumns = 16;
-template <typename T>
-__global__ __launch_bounds__(kParamBlock) void group_param_kernel(GroupCall c, const float* join) {
-  constexpr int kSubs = kParamBlock / kParamColumns;
-  __shared__ float lds[2][kParamBlock];
+// The weights' gradients of kParamColumns columns from the samples' sums, by a workgroup of B,
+// in a fixed order.
+constexpr int kParamColumns = 16;
+template <typename T, int B>
+__device__ inline void sum_params(const GroupCall& c, const float* join, int block) {
+  constexpr int kSubs = B / kParamColumns;
+  __shared__ float lds[2][B];
   const int sub = threadIdx.x / kParamColumns, lane = threadIdx.x % kParamColumns;
-  const int64_t e = int64_t(blockIdx.x) * kParamColumns + lane;
+  const int64_t e = int64_t(block) * kParamColumns + lane, ld = 2 * c.width;
   float a = 0, b = 0;
   if (e < c.width) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t s = sub; s < c.samples; s += kSubs) {
-      a += join[s * 2 * c.width + e];
-      b += join[(s * 2 + 1) * c.width + e];
+      a += join[s * ld + e];
+      b += join[s * ld + c.width + e];
     }
   }
   lds[0][threadIdx.x] = a;
@@ -960,6 +1049,53 @@ __global__ __launch_bounds__(kParamBlock) void group_param_kernel(GroupCall c, c
     if (c.grad_bias) store_either<T>(c.grad_bias, c.weight_f32, e, lds[0][lane]);
     if (c.grad_weight) store_either<T>(c.grad_weight, c.weight_f32, e, lds[1][lane]);
   }
+}
+
+// The first `params` workgroups sum the weights' gradients, the others have a tile each.
+template <typename T, int V>
+__global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c, GroupLayout y, const float* coef,
+                                                                     const float* join, int params) {
+  if (int(blockIdx.x) < params) {
+    sum_params<T, kTileBlock>(c, join, blockIdx.x);
+    return;
+  }
+  const int block = from_behind(blockIdx.x - params, y.tiles * y.chunks);
+  if (block >= y.tiles * y.chunks) return;
+  const Tile t(c, y, block);
+  const Chunk q = chunk_of(c, y, t.chunk);
+  const Place<V> p(q, y);
+  int group[V];
+  place_groups(y, p, group);
+  Slopes<V> k;
+  place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
+  place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
+  for_pieces(c, y, t, [&](int64_t s, int lo, int hi) {
+    place_stats(c, group, c.stats, s, k.mean, k.rstd);
+    float ma[V], mh[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float* at = coef + (s * c.groups + group[j]) * 2;
+      ma[j] = at[0];
+      mh[j] = at[1];
+    }
+    T* out = static_cast<T*>(c.y) + int64_t(lo + p.slice) * c.ld_y;
+    for_row_pairs<T, V, kInFlight / 2>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
+      float h[V], d[V];
+      slopes(x, g, k, c.act, h, d);
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
+      store_own<false>(p, out, d);
+      out += int64_t(y.slices) * c.ld_y;
+    });
+  });
+  if (c.offsets) zero_tile<T>(c, y, p, t);
+}
+
+// The weights' gradients by themselves, behind whole samples.
+constexpr int kParamBlock = 1024;
+template <typename T>
+__global__ __launch_bounds__(kParamBlock) void group_param_kernel(GroupCall c, const float* join) {
+  sum_params<T, kParamBlock>(c, join, blockIdx.x);
 }
 
 // ---- launches ----------------------------------------------------------------------
@@ -988,39 +1124,57 @@ void whole(const GroupCall& c, const GroupLayout& y, bool backward, float* join,
 }
 
 template <typename T, int V>
-hipError_t run(const GroupCall& c, const GroupLayout& y, bool backward, hipStream_t s) {
+void tiles(const GroupCall& c, const GroupLayout& y, bool backward, bool sums, float* join, hipStream_t s) {
   const GroupWork at = group_work(c, y, backward);
-  float* pieces = c.work + at.pieces;
-  const bool params = backward && (c.grad_weight || c.grad_bias);
-  // the sums per sample and channel, unless one sample's are the gradients themselves
-  float* join = params && c.samples != 1 ? c.work + at.join : nullptr;
-  if (y.whole) {
-    // a null join makes the kernel write the gradients
-    if (y.block == 64)
-      whole<T, V, 64>(c, y, backward, join, s);
-    else if (y.block == 256)
-      whole<T, V, 256>(c, y, backward, join, s);
-    else
-      whole<T, V, 1024>(c, y, backward, join, s);
-  } else {
-    float* coef = c.work + at.coef;
-    const dim3 grid{unsigned(y.tiles * y.chunks)}, block{kTileBlock};
-    const int64_t joins = c.samples * c.groups;
-    if (!backward) {
-      float* stats = c.stats ? c.stats : coef;
-      if (grid.x) hipLaunchKernelGGL((group_sum_kernel<T, V>), grid, block, 0, s, c, y, pieces);
-      if (joins)
-        hipLaunchKernelGGL(group_join_kernel, dim3(blocks_of((joins + 3) / 4, kTileBlock)), block, 0, s, c, y, pieces, stats);
-      if (grid.x) hipLaunchKernelGGL((group_apply_kernel<T, V>), grid, block, 0, s, c, y, stats);
-    } else {
-      if (grid.x) hipLaunchKernelGGL((group_bwd_sum_kernel<T, V>), grid, block, 0, s, c, y, pieces);
-      if (joins)
-        hipLaunchKernelGGL(group_bwd_join_kernel<T>, dim3(blocks_of(joins, kTileBlock)), block, 0, s, c, y, pieces, join,
-                           coef);
-      if (grid.x && c.y) hipLaunchKernelGGL((group_bwd_apply_kernel<T, V>), grid, block, 0, s, c, y, coef);
-    }
+  float *pieces = c.work + at.pieces, *coef = c.work + at.coef;
+  const unsigned blocks = unsigned(y.tiles * y.chunks), back = (blocks + kDies - 1) / kDies * kDies;
+  const dim3 block{kTileBlock};
+  // lanes for one sample and group: as many as its tiles keep busy
+  const int64_t joins = c.samples * c.groups, mean = joins ? y.tiles / c.samples : 0;
+  if (!backward) {
+    float* stats = c.stats ? c.stats : coef;
+    if (blocks) hipLaunchKernelGGL((group_sum_kernel<T, V>), dim3(blocks), block, 0, s, c, y, pieces);
+    if (joins && mean > 2 * kWave)
+      hipLaunchKernelGGL(group_join_kernel<kTileBlock>, dim3(blocks_of(joins, kTileBlock)), block, 0, s, c, y, pieces, stats);
+    else if (joins)
+      hipLaunchKernelGGL(group_join_kernel<kWave>, dim3(blocks_of((joins + 3) / 4, kTileBlock)), block, 0, s, c, y, pieces,
+                         stats);
+    if (blocks) hipLaunchKernelGGL((group_apply_kernel<T, V>), dim3(back), block, 0, s, c, y, stats);
+    return;
   }
-  if (params && c.samples != 1)
+  if (blocks) hipLaunchKernelGGL((group_bwd_sum_kernel<T, V>), dim3(blocks), block, 0, s, c, y, pieces);
+  const int64_t work = mean * y.per_group;   // sums that a workgroup joins
+  if (joins && work > 2048)
+    hipLaunchKernelGGL((group_bwd_join_kernel<T, 1024>), dim3(blocks_of(joins, 1024)), dim3(1024), 0, s, c, y, pieces, join,
+                       coef);
+  else if (joins && work > 256)
+    hipLaunchKernelGGL((group_bwd_join_kernel<T, 256>), dim3(blocks_of(joins, 256)), dim3(256), 0, s, c, y, pieces, join,
+                       coef);
+  else if (joins)
+    hipLaunchKernelGGL((group_bwd_join_kernel<T, 64>), dim3(blocks_of(joins, 64)), dim3(64), 0, s, c, y, pieces, join, coef);
+  const unsigned params = sums ? unsigned((c.width + kParamColumns - 1) / kParamColumns) : 0u;
+  if (params + (c.y ? back : 0))
+    hipLaunchKernelGGL((group_bwd_apply_kernel<T, V>), dim3(params + (c.y ? back : 0)), block, 0, s, c, y, coef, join,
+                       int(params));
+}
+
+template <typename T, int V>
+hipError_t run(const GroupCall& c, const GroupLayout& y, bool backward, hipStream_t s) {
+  // the sums per sample and channel, unless one sample's are the gradients themselves, which a
+  // null join has written (of no sample there are none, and nothing to hold them)
+  const bool sums = backward && (c.grad_weight || c.grad_bias) && c.samples != 1;
+  float* join = sums ? c.work + group_work(c, y, backward).join : nullptr;
+  if (!y.whole) {
+    tiles<T, V>(c, y, backward, sums, join, s);
+    return hipGetLastError();
+  }
+  if (y.block == 64)
+    whole<T, V, 64>(c, y, backward, join, s);
+  else if (y.block == 256)
+    whole<T, V, 256>(c, y, backward, join, s);
+  else
+    whole<T, V, 1024>(c, y, backward, join, s);
+  if (sums)
     hipLaunchKernelGGL(group_param_kernel<T>, dim3(unsigned((c.width + kParamColumns - 1) / kParamColumns)),
                        dim3(kParamBlock), 0, s, c, join);
   return hipGetLastError();
