@@ -28,6 +28,7 @@ struct GroupLayout {
   int lanes, slices;
   int tile_rows, tiles;  // tiles only
   int equal;             // rows of each sample, where there are no offsets
+  int stream;            // the output passes by the caches: the call moves more than they hold
 };
 
 // Columns of a thread's place.  Everything that a thread has per column (weights, statistics,
@@ -38,6 +39,14 @@ constexpr int kGroupVec = 4;
 // of them spill in workgroups of 1024).
 constexpr int kHeldFew = 4;
 constexpr int held_most(int elem_bytes, bool backward) { return (backward ? 24 : 64) / elem_bytes; }
+
+// Workgroups with a tile each: one for every place that the device has for them (some 1000), or,
+// past the caches, as many as keep the addresses that are read at one time together.  Measured
+// with 512, 1024 and 2048: forward of 114688 x 128 bf16 28, 25 and 28 us, backward of 20060 x 481
+// fp32 in 48 samples 48, 49 and 54; with 1024, 2048, 4096 and 6144: forward of 114688 x 1312 fp32
+// 391, 373, 350 and 351 us, backward of 400000 x 128 in 20 samples 207, 196, 190 and 189.
+constexpr int64_t kTiles = 1024, kTilesStream = 4096;
+constexpr int kTileTurn = 8;   // rows that a thread reads at once
 
 inline void set_lanes(GroupLayout& y, int64_t columns) {
   y.lanes = int((columns + y.vec - 1) / y.vec);
@@ -51,27 +60,29 @@ inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backwa
   y.equal = c.offsets || c.samples == 0 ? 0 : int(c.rows / c.samples);
   y.vec = c.width >= kGroupVec ? kGroupVec : 1;
   y.split = 1;
+  y.stream = double(c.rows) * double(c.width) * elem_bytes * (backward ? 3 : 2) > double(kCacheBytes);
   y.part = int(cg);
   // the longest sample: as told, as equal samples have it, or eight times the mean
   const int64_t mean = c.samples ? (c.rows + c.samples - 1) / c.samples : 0;
   const int64_t longest = c.longest > 0 ? std::min(c.longest, c.rows) : std::min(c.rows, c.offsets ? 8 * mean : mean);
   const int most = held_most(elem_bytes, backward);
-  // A workgroup for a whole sample: the smallest that holds one, with the widest chunk, if that
-  // leaves kWant workgroups; else 256 or 1024 threads that do, with chunks down to 32 bytes of a
-  // row.
-  constexpr int64_t kWant = 512;
+  // A workgroup for a whole sample: 64 threads with the widest chunk that leaves kWant
+  // workgroups, else 256 with chunks down to 32 bytes of a row; both hold half of the longest
+  // sample at least, and read the rest again.  1024 threads that hold it whole, one workgroup to
+  // a compute unit, only where there are no more of them than units.  Else tiles.
+  constexpr int64_t kWant = 512, kUnits = 256;
   for (const int block : {64, 256, 1024}) {
     y.block = block;
     int64_t take = 0, items = 0;
     for (int64_t m = std::min(c.groups, block * int64_t(y.vec) / cg); m >= 1; m = m == 1 ? 0 : (m + 1) / 2) {
       set_lanes(y, m * cg);
-      if (int64_t(y.slices) * most < longest) continue;
+      if (int64_t(y.slices) * most * (block < 1024 ? 2 : 1) < longest) continue;
       if (take && m * cg * elem_bytes < 32) break;
       take = m;
       items = c.samples * ((c.groups + m - 1) / m);
       if (items >= kWant) break;
     }
-    if (!take || (block == 64 && items < kWant)) continue;
+    if (!take || (block == 64 && items < kWant) || (block == 1024 && items > kUnits)) continue;
     y.whole = 1;
     y.per_chunk = int(take);
     y.chunks = int((c.groups + take - 1) / take);
@@ -106,10 +117,11 @@ inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backwa
     y.chunks = int((c.groups + y.per_chunk - 1) / y.per_chunk);
     set_lanes(y, y.per_chunk * cg);
   }
-  // tiles of four turns at least, so many that they fill the device some times over
-  constexpr int64_t kTileBlocks = 2048;
-  int64_t rows = std::max<int64_t>((c.rows * y.chunks + kTileBlocks - 1) / kTileBlocks, 4 * y.slices);
-  rows = std::max<int64_t>(std::min((rows + y.slices - 1) / y.slices * y.slices, c.rows), 1);
+  // whole turns of kTileTurn rows a thread, four rows at least
+  const int64_t most_tiles = y.stream ? kTilesStream : kTiles, turn = int64_t(kTileTurn) * y.slices;
+  int64_t rows = std::max<int64_t>((c.rows * y.chunks + most_tiles - 1) / most_tiles, 4 * y.slices);
+  if (rows > turn / 2) rows = (rows + turn - 1) / turn * turn;
+  rows = std::max<int64_t>(std::min(rows, c.rows), 1);
   y.tile_rows = int(rows);
   y.tiles = int((c.rows + rows - 1) / rows);
   return y;

@@ -160,13 +160,21 @@ struct Place {
   __device__ bool has(int j) const { return j >= own && j < end; }
 };
 
-template <bool Stream, typename T, int V>
-__device__ inline void store_own(const Place<V>& p, T* row, const float (&v)[V]) {
+// stream: past the caches (the same for all lanes).
+template <typename T, int V>
+__device__ inline void store_own(const Place<V>& p, T* row, const float (&v)[V], int stream) {
   Vec<T, V> r;
 #pragma unroll
   for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(v[j]);
   if (p.whole()) {
-    store_vec<Stream, T, V>(row + p.at, r);
+    if (stream) {
+      // the marks keep the compiler from making one ordinary store of the two
+      asm volatile("");
+      store_vec<true, T, V>(row + p.at, r);
+      asm volatile("");
+    } else {
+      store_vec<false, T, V>(row + p.at, r);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -303,10 +311,10 @@ __device__ inline float rstd_of(float m2, float values, float eps) {
 
 // Zeros in the workgroup's columns of rows [from, to).
 template <typename T, int V>
-__device__ inline void zero_rows(const GroupCall& c, const Place<V>& p, int slices, int64_t from, int64_t to) {
+__device__ inline void zero_rows(const GroupCall& c, const GroupLayout& y, const Place<V>& p, int64_t from, int64_t to) {
   if (!p.in) return;
   const float none[V] = {};
-  for (int64_t r = from + p.slice; r < to; r += slices) store_own<false>(p, static_cast<T*>(c.y) + r * c.ld_y, none);
+  for (int64_t r = from + p.slice; r < to; r += y.slices) store_own(p, static_cast<T*>(c.y) + r * c.ld_y, none, y.stream);
 }
 
 template <int V>
@@ -433,7 +441,7 @@ __device__ inline void zero_outside(const GroupCall& c, const GroupLayout& y, in
     const Place<V> p(chunk_of(c, y, k), y);
     if (!p.in) continue;
     for (int64_t i = block * y.slices + p.slice; i < first + c.rows - last; i += int64_t(y.slices) * kZeroBlocks)
-      store_own<false>(p, static_cast<T*>(c.y) + (i < first ? i : last + i - first) * c.ld_y, none);
+      store_own(p, static_cast<T*>(c.y) + (i < first ? i : last + i - first) * c.ld_y, none, y.stream);
   }
 }
 
@@ -455,13 +463,14 @@ __device__ inline T afresh(T v) {
   return v;
 }
 // Rows that a thread reads at once, in tiles; a workgroup that holds rows has few registers left.
-constexpr int kInFlight = 8, kBeside = 2;
+constexpr int kInFlight = kTileTurn, kBeside = 2;
 
 // Rows lo + slice, + slices ... of [lo, hi): f(vector, whether it is the first) for each.
 template <typename T, int V, int Q, typename F>
 __device__ inline void for_rows(const Place<V>& p, int slices, const T* x, int64_t ld, int lo, int hi, F&& f) {
   const int64_t step = int64_t(slices) * ld;
   int left = Rows(p, slices, hi - lo).mine;
+  if (left <= 0) return;
   const T* at = x + int64_t(lo + p.slice) * ld + p.at;
   bool first = true;
   while (left > 0) {
@@ -484,6 +493,7 @@ template <typename T, int V, int Q, typename F>
 __device__ inline void for_row_pairs(const GroupCall& c, const Place<V>& p, int slices, int lo, int hi, F&& f) {
   const int64_t sx = int64_t(slices) * c.ld_x, sg = int64_t(slices) * c.ld_g;
   int left = Rows(p, slices, hi - lo).mine;
+  if (left <= 0) return;
   const T* x = static_cast<const T*>(c.x) + int64_t(lo + p.slice) * c.ld_x + p.at;
   const T* g = static_cast<const T*>(c.grad_out) + int64_t(lo + p.slice) * c.ld_g + p.at;
   while (left > 0) {
@@ -618,7 +628,7 @@ __global__ __launch_bounds__(B) void group_fwd_kernel(GroupCall c, GroupLayout y
       if (i < again) {
         float z[V];
         activated(unpack<T, V>(held[i]), k, c.act, z);
-        store_own<false>(p, out, z);
+        store_own(p, out, z, y.stream);
       }
       out = afresh(out + step_y);
     }
@@ -626,7 +636,7 @@ __global__ __launch_bounds__(B) void group_fwd_kernel(GroupCall c, GroupLayout y
       for_rows<T, V, kBeside>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, rest, end, [&](const Vec<T, V>& row, bool) {
         float z[V];
         activated(row, k, c.act, z);
-        store_own<false>(p, out, z);
+        store_own(p, out, z, y.stream);
         out += step_y;
       });
     __syncthreads();   // before the next sample's entries
@@ -728,7 +738,7 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
         slopes(vx, vg, k, c.act, h, d);
 #pragma unroll
         for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
-        store_own<false>(p, out, d);
+        store_own(p, out, d, y.stream);
       };
       const int again = afresh(own.mine);
 #pragma unroll
@@ -877,8 +887,8 @@ template <typename T, int V>
 __device__ inline void zero_tile(const GroupCall& c, const GroupLayout& y, const Place<V>& p, const Tile& t) {
   int first, last;
   outside(c, y, first, last);
-  zero_rows<T>(c, p, y.slices, t.r0, min(t.r1, first));
-  zero_rows<T>(c, p, y.slices, max(t.r0, last), t.r1);
+  zero_rows<T>(c, y, p, t.r0, min(t.r1, first));
+  zero_rows<T>(c, y, p, max(t.r0, last), t.r1);
 }
 
 template <typename T, int V>
@@ -905,7 +915,7 @@ __global__ __launch_bounds__(kTileBlock) void group_apply_kernel(GroupCall c, Gr
     for_rows<T, V, kInFlight>(p, y.slices, static_cast<const T*>(c.x), c.ld_x, lo, hi, [&](const Vec<T, V>& r, bool) {
       float z[V];
       activated(r, k, c.act, z);
-      store_own<false>(p, out, z);
+      store_own(p, out, z, y.stream);
       out += int64_t(y.slices) * c.ld_y;
     });
   });
@@ -1084,7 +1094,7 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c
       slopes(x, g, k, c.act, h, d);
 #pragma unroll
       for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
-      store_own<false>(p, out, d);
+      store_own(p, out, d, y.stream);
       out += int64_t(y.slices) * c.ld_y;
     });
   });
