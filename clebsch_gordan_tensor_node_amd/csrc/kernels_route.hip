@@ -37,19 +37,30 @@ __device__ inline uint32_t lanes_max(uint32_t v) {
   }
   return v;
 }
+// Sum over the lanes of a wave whose numbers leave the same rest by L, to each of them.
+template <int L>
+__device__ inline float same_sum(float v) {
+  if constexpr (L <= 1) v += dpp<0x121>(v);   // row_ror 1, 2, 4, 8
+  if constexpr (L <= 2) v += dpp<0x122>(v);
+  if constexpr (L <= 4) v += dpp<0x124>(v);
+  if constexpr (L <= 8) v += dpp<0x128>(v);
+  if constexpr (L <= 16) v += __shfl_xor(v, 16);
+  if constexpr (L <= 32) v += __shfl_xor(v, 32);
+  return v;
+}
 template <int L>
 __device__ inline float group_sum(float v) {
   if constexpr (L >= 4) v = lanes_sum<L>(v);
   return v;
 }
 
-// exp(x), x <= 0, to some 2 ulp: 2^t with t = x log2(e) rounded, times 1 + what that left out.
+// exp(x), x <= 0, to some 2 ulp: 2^t e^(x - t ln 2) with t = x log2(e) rounded, the second factor
+// 1 + its small exponent.  From -200 on it is 0; NaN stays.
 __device__ inline float exp_f32(float x) {
-  constexpr float kLog2e = 1.44269504f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
-  const float t = x * kLog2e;
-  const float rest = fmaf(x, kRest, fmaf(x, kLog2e, -t));
+  x = x < -200.0f ? -200.0f : x;
+  const float t = x * 1.44269504f;
   const float p = __builtin_amdgcn_exp2f(t);
-  return p > 0 ? fmaf(p, rest * kLn2, p) : p;   // -infinity leaves NaN in the rest; NaN stays
+  return fmaf(p, fmaf(t, -0.693147181f, x), p);
 }
 
 // Keys in the order of the logits: -infinity is kNone, NaN the largest, -0 is 0.
@@ -102,70 +113,142 @@ __device__ inline void write_logits(T* row, int first, int n, const float (&z)[E
 
 constexpr int kRouteBlock = 256;
 
-// Where the workgroups' sums stand: [blocks][n] of p, [blocks][n] choices, [blocks] rows.
+// Where the workgroups' sums stand: [blocks][n] of p, [blocks][n] choices, [blocks] rows and
+// [blocks] choices of all branches; and the shares of the balance loss of kJoinColumns branches
+// each.
 struct RouteWork {
+  double* shares;
   float* p;
   int32_t* chosen;
   int32_t* rows;
+  int32_t* picks;
   int blocks;
 };
+constexpr int kJoinColumns = 16;
+
+// Sum over a wave of a double, to every lane.
+__device__ inline double wave_sum(double v) {
+#pragma unroll
+  for (int x = 1; x < kWave; x *= 2) v += __shfl_xor(v, x);
+  return v;
+}
 
 // Counts, slopes and the balance loss from the workgroups' sums, in a fixed order.  By one
-// whole workgroup; lds: 2 * blockDim.x doubles.
+// whole workgroup of B.  Cols branches at once, by B / Cols threads each; lds: 2 (B + 64) doubles.
+template <int B, int Cols>
 __device__ inline void finish(const RouteCall& c, const RouteWork& w, double* lds) {
-  const int threads = int(blockDim.x), t = threadIdx.x;
+  constexpr int kSubs = B / Cols, kWaves = B / kWave;
+  const int t = threadIdx.x, sub = t / Cols, lane = t % Cols;
+  double* head = lds + 2 * B;   // of each wave: rows, then choices and their p
   int r = 0;
-  for (int b = t; b < w.blocks; b += threads) r += w.rows[b];
-  int* whole = reinterpret_cast<int*>(lds);
-  whole[t] = r;
-  __syncthreads();
-  for (int half = threads / 2; half > 0; half /= 2) {
-    if (t < half) whole[t] += whole[t + half];
-    __syncthreads();
-  }
-  const double rows = whole[0];
-  __syncthreads();
-  // `subs` threads for each of `cols` branches at once
-  const int cols = min(threads, c.n <= 4 ? 4 : c.n <= 16 ? 16 : c.n <= 64 ? 64 : c.n <= 256 ? 256 : 1024);
-  const int subs = threads / cols, sub = t / cols, lane = t % cols;
+  for (int b = t; b < w.blocks; b += B) r += w.rows[b];
+  double rows = wave_sum(double(r));
+  if (t % kWave == 0) head[t / kWave] = rows;
   double all = 0, weighted = 0;   // C, and the sum of counts[e] (sum of p[e])
-  for (int e0 = 0; e0 < c.n; e0 += cols) {
+  for (int e0 = 0; e0 < c.n; e0 += Cols) {
     const int e = e0 + lane;
-    double p = 0, count = 0;
+    double p = 0;
+    int64_t count = 0;
     if (e < c.n) {
-#pragma unroll 4
-      for (int b = sub; b < w.blocks; b += subs) {
+#pragma unroll 8
+      for (int b = sub; b < w.blocks; b += kSubs) {
         p += w.p[int64_t(b) * c.n + e];
         count += w.chosen[int64_t(b) * c.n + e];
       }
     }
-    lds[2 * t] = p;
-    lds[2 * t + 1] = count;
+    double n = double(count);
+    // lanes of one wave that have the same branch, then waves
+#pragma unroll
+    for (int x = Cols; x < kWave; x *= 2) {
+      p += __shfl_xor(p, x);
+      n += __shfl_xor(n, x);
+    }
     __syncthreads();
-    if (sub == 0 && e < c.n) {
-      for (int i = 1; i < subs; ++i) {
-        p += lds[2 * (i * cols + lane)];
-        count += lds[2 * (i * cols + lane) + 1];
+    if (t % kWave < Cols) {
+      lds[2 * t] = p;
+      lds[2 * t + 1] = n;
+    }
+    __syncthreads();
+    if (t < Cols && e < c.n) {
+      constexpr int kStep = Cols < kWave ? kWave : Cols;   // from one that holds a branch to the next
+      p = n = 0;
+      for (int i = t; i < B; i += kStep) {
+        p += lds[2 * i];
+        n += lds[2 * i + 1];
       }
-      c.counts[e] = int32_t(count);
-      all += count;
-      weighted += count * p;
+      c.counts[e] = int32_t(n);
+      all += n;
+      weighted += n * p;
+    }
+  }
+  all = wave_sum(all);
+  weighted = wave_sum(weighted);
+  if (t % kWave == 0) {
+    head[kWaves + t / kWave] = all;
+    head[2 * kWaves + t / kWave] = weighted;
+  }
+  __syncthreads();   // the counts, too
+  rows = all = weighted = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    rows += head[i];
+    all += head[kWaves + i];
+    weighted += head[2 * kWaves + i];
+  }
+  const double factor = all * rows > 0 ? double(c.n) / (all * rows) : 0.0;
+  if (t == 0) c.balance[0] = float(factor > 0 ? factor * weighted : 0.0);
+  for (int e = t; e < c.n; e += B) c.slope[e] = float(factor * double(c.counts[e]));
+}
+template <int B>
+__device__ inline void finish(const RouteCall& c, const RouteWork& w, double* lds) {
+  if (c.n <= 4)
+    finish<B, 4>(c, w, lds);
+  else if (c.n <= 16)
+    finish<B, 16>(c, w, lds);
+  else if (c.n <= 64)
+    finish<B, 64>(c, w, lds);
+  else
+    finish<B, 256>(c, w, lds);
+}
+
+// A workgroup's sums from its threads': lanes of a wave that hold the same branches, then
+// waves.  lds: B / kWave * L * E floats.
+template <int B, int E, int L>
+__device__ inline void write_sums(const RouteCall& c, const RouteWork& w, const float (&p_sum)[E], const int (&n_of)[E],
+                                  int n_rows, int n_picks, float* lds, int32_t* lds_rows) {
+  constexpr int kWaves = B / kWave;
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  for (int what = 0; what < 2; ++what) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float v = same_sum<L>(what ? float(n_of[j]) : p_sum[j]);   // counts below 2^24: exact
+      if (lane < L) lds[wave * L * E + lane * E + j] = v;
+    }
+    if (what == 0) {
+      const float rows = lanes_sum<kWave>(float(n_rows)), picks = lanes_sum<kWave>(float(n_picks));
+      if (lane == 0) {
+        lds_rows[wave] = int(rows);
+        lds_rows[kWaves + wave] = int(picks);
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < c.n; e += B) {
+      float v = 0;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) v += lds[q * L * E + e];
+      if (what)
+        w.chosen[int64_t(blockIdx.x) * c.n + e] = int32_t(v);
+      else
+        w.p[int64_t(blockIdx.x) * c.n + e] = v;
+    }
+    if (what == 0 && threadIdx.x < 2) {
+      int s = 0;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) s += lds_rows[threadIdx.x * kWaves + q];
+      (threadIdx.x ? w.picks : w.rows)[blockIdx.x] = s;
     }
     __syncthreads();
   }
-  lds[2 * t] = all;
-  lds[2 * t + 1] = weighted;
-  __syncthreads();
-  for (int half = threads / 2; half > 0; half /= 2) {
-    if (t < half) {
-      lds[2 * t] += lds[2 * (t + half)];
-      lds[2 * t + 1] += lds[2 * (t + half) + 1];
-    }
-    __syncthreads();
-  }
-  const double factor = lds[0] * rows > 0 ? double(c.n) / (lds[0] * rows) : 0.0;
-  if (t == 0) c.balance[0] = float(factor > 0 ? factor * lds[1] : 0.0);
-  for (int e = t; e < c.n; e += threads) c.slope[e] = float(factor * double(c.counts[e]));
 }
 
 template <typename T, int E, int L>
@@ -174,8 +257,8 @@ __global__ __launch_bounds__(kRouteBlock) void route_fwd_kernel(RouteCall c, Rou
   constexpr int kMost = L * E < kMaxChosen ? L * E : kMaxChosen;
   constexpr int kSums = kRows * L * E, kPicks = kRows * kMost;
   __shared__ __align__(16) float lds[kSums > 2 * kPicks ? kSums : 2 * kPicks];
-  __shared__ double room[2 * kRouteBlock];
-  __shared__ int32_t lds_rows[kRouteBlock / kWave];
+  __shared__ double room[2 * (kRouteBlock + kWave)];
+  __shared__ int32_t lds_rows[2 * kRouteBlock / kWave];
   const int lane = threadIdx.x % L, first = lane * E, group = threadIdx.x / L;
   float* picked = lds + group * kMost;                                     // exp(z - top) of the choices
   int32_t* picked_id = reinterpret_cast<int32_t*>(lds) + kPicks + group * kMost;
@@ -234,7 +317,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_fwd_kernel(RouteCall c, Rou
         picked_id[i] = some ? int(at) : -1;
       }
     }
-    const float inv = 1.0f / sum, scale = c.renormalise ? 1.0f / kept : inv;
+    const float inv = __builtin_amdgcn_rcpf(sum), scale = c.renormalise ? __builtin_amdgcn_rcpf(kept) : inv;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       if (part) p_sum[j] += z[j] * inv;
@@ -254,43 +337,270 @@ __global__ __launch_bounds__(kRouteBlock) void route_fwd_kernel(RouteCall c, Rou
     __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
-  // the workgroup's sums: its row groups' in a fixed order
-  for (int what = 0; what < 2; ++what) {
+  write_sums<kRouteBlock, E, L>(c, w, p_sum, n_of, n_rows, 0, lds, lds_rows);   // (the last step adds the choices itself)
+  if (w.blocks == 1) finish<kRouteBlock>(c, w, room);   // the workgroup sees its own sums
+}
+
+// A row to a wave, n > 64.  Each lane sorts its E keys once; then the largest of the lanes'
+// first keys is chosen k times, a ballot tells whose it was (of equal ones the lowest lane's,
+// which has the lowest branches), and that lane's keys move up by one.  What the whole wave
+// finds is held in scalar registers.  Lane i keeps the i-th choice's key and lane, and looks
+// its branch up in the end.
+constexpr int kLowest = int(0x80000000u);    // below every number's key
+template <int Ctrl, int Rows>
+__device__ inline int max_dpp(int v) {
+  // the lowest number where a lane has no source: the form that fuses into one instruction
+  if constexpr (Rows == 0xf) return max(v, __builtin_amdgcn_mov_dpp(v, Ctrl, 0xf, 0xf, true));
+  return max(v, __builtin_amdgcn_update_dpp(kLowest, v, Ctrl, Rows, 0xf, false));
+}
+// To a scalar.
+__device__ inline int wave_max(int v) {
+  v = max_dpp<0xB1, 0xf>(v);    // quad_perm 1 0 3 2
+  v = max_dpp<0x4E, 0xf>(v);    // quad_perm 2 3 0 1
+  v = max_dpp<0x141, 0xf>(v);   // row_half_mirror
+  v = max_dpp<0x140, 0xf>(v);   // row_mirror
+  v = max_dpp<0x142, 0xa>(v);   // row_bcast 15: rows 1 and 3
+  v = max_dpp<0x143, 0xc>(v);   // row_bcast 31: rows 2 and 3
+  return __builtin_amdgcn_readlane(v, kWave - 1);
+}
+__device__ inline float scalar(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+__device__ inline int wide_key(float z) {
+  const int b = __builtin_bit_cast(int, z + 0.0f);
+  return b ^ int(uint32_t(b >> 31) >> 1);
+}
+__device__ inline float of_wide_key(int k) { return __builtin_bit_cast(float, k ^ int(uint32_t(k >> 31) >> 1)); }
+constexpr int kMinusInf = int(0x807fffffu);  // -infinity's
+
+// Largest first, by Batcher's odd-even merging network.
+template <int E>
+__device__ inline void sort_keys(int (&s)[E]) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) lds[group * L * E + first + j] = what ? float(n_of[j]) : p_sum[j];   // below 2^24: exact
-    for (int half = kRows / 2; half > 0; half /= 2) {
-      __syncthreads();
-      for (int e = threadIdx.x; e < half * L * E; e += kRouteBlock) lds[e] += lds[e + half * L * E];
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < c.n; e += kRouteBlock) {
-      if (what)
-        w.chosen[int64_t(blockIdx.x) * c.n + e] = int32_t(lds[e]);
-      else
-        w.p[int64_t(blockIdx.x) * c.n + e] = lds[e];
-    }
-    __syncthreads();
-  }
+  for (int p = 1; p < E; p *= 2)
 #pragma unroll
-  for (int x = 1; x < kWave; x *= 2) n_rows += __shfl_xor(n_rows, x);
-  if (threadIdx.x % kWave == 0) lds_rows[threadIdx.x / kWave] = n_rows;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int s = 0;
-    for (int q = 0; q < kRouteBlock / kWave; ++q) s += lds_rows[q];
-    w.rows[blockIdx.x] = s;
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < E; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < E && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const int u = s[i + j], v = s[i + j + k];
+            s[i + j] = max(u, v);
+            s[i + j + k] = min(u, v);
+          }
+}
+
+// Waves of a workgroup, and of a SIMD: eight of them hide the chain of each one's choices (131072
+// rows to 8 of 256: 79 us, 93 with four), where the registers allow.
+constexpr int wide_block(int e) { return e <= 8 ? 1024 : 512; }
+template <typename T, int E>
+__global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void route_fwd_wide_kernel(RouteCall c,
+                                                                                                 RouteWork w) {
+  constexpr int B = wide_block(E), kWaves = B / kWave;
+  __shared__ __align__(16) float lds[kWaves * kWave * E];
+  __shared__ double room[2 * (B + kWave)];
+  __shared__ int32_t lds_rows[2 * kWaves];
+  const int lane = threadIdx.x % kWave, first = lane * E;
+  float p_sum[E];
+  int n_of[E], n_rows = 0, n_picks = 0;
+#pragma unroll
+  for (int j = 0; j < E; ++j) p_sum[j] = 0, n_of[j] = 0;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
+  // the next row's logits are on their way while a row is routed
+  const int64_t r0 = int64_t(blockIdx.x) * kWaves + wave, step = int64_t(gridDim.x) * kWaves;
+  float next[E];
+  bool next_in = false;
+  auto read = [&](int64_t r) {
+    next_in = r < c.rows && (!c.mask || c.mask[r] != 0);
+    if (next_in) read_logits(static_cast<const T*>(c.logits) + r * c.ld, first, c.n, next);
+  };
+  read(r0);
+  for (int64_t r = r0; r < c.rows; r += step) {
+    int id = -1;
+    float gate = 0;
+    float z[E];            // then exp(z - top), of the chosen; 0 of the others
+    bool part = next_in;   // the row takes part
+#pragma unroll
+    for (int j = 0; j < E; ++j) z[j] = next[j];
+    read(r + step);
+    if (part) {
+      int key[E], s[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) s[j] = key[j] = wide_key(z[j]);
+      sort_keys(s);
+      int m = wave_max(s[0]);
+      const float top = of_wide_key(m);
+      float e[E], sum = 0;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        e[j] = exp_f32(z[j] - top);
+        sum += e[j];
+      }
+      sum = scalar(lanes_sum<kWave>(sum));
+      if (!(sum < __builtin_inff())) {
+        // no number on top: NaN above infinity above the others, or all -infinity
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          s[j] = key[j] = z[j] != z[j] ? 0x7fffffff : wide_key(z[j]);
+          e[j] = sum;   // NaN
+        }
+        sort_keys(s);
+        m = wave_max(s[0]);
+      }
+      part = m > kMinusInf;
+      if (part) {
+        int got = kMinusInf, from = 0;   // lane i's: the i-th choice's key and lane
+        int found = 0, last = m;
+        do {
+          const int at = __builtin_ctzll(__ballot(s[0] == m));
+          const bool mine = lane == at;
+#pragma unroll
+          for (int j = 0; j + 1 < E; ++j) {
+            const int above = s[j], below = s[j + 1];   // values: of two elements it would select the index
+            s[j] = mine ? below : above;
+          }
+          if (mine) s[E - 1] = kLowest;
+          if (lane == found) got = m, from = at;
+          last = m;
+          if (++found == c.k) break;
+          m = wave_max(s[0]);
+        } while (m > kMinusInf);
+        // A lane's chosen keys are above the first that is left.  One that is left may equal the
+        // last choice's: of equal ones the lane's first are chosen then, as many as it gave.
+        uint32_t chosen = 0;
+        if (__ballot(s[0] == last)) {
+          int taken = 0, above = 0;
+          for (int i = 0; i < found; ++i) taken += __builtin_amdgcn_readlane(from, i) == lane;
+#pragma unroll
+          for (int j = 0; j < E; ++j) above += key[j] > s[0];
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            const bool more = key[j] == s[0] && above < taken;
+            above += more;
+            chosen |= key[j] > s[0] || more ? 1u << j : 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < E; ++j) n_of[j] += chosen >> j & 1;
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j) n_of[j] += key[j] > s[0];
+          if (c.dense) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) chosen |= key[j] > s[0] ? 1u << j : 0u;
+          }
+        }
+        // a choice's branch is the first of its lane's that has the key, or the one behind where
+        // the choice before was of the same lane and key
+        const int got_before = __builtin_amdgcn_update_dpp(kLowest, got, 0x138, 0xf, 0xf, false);   // wave_shr 1
+        const int from_before = __builtin_amdgcn_update_dpp(-1, from, 0x138, 0xf, 0xf, false);
+        int skip = 0;
+        if (__ballot(lane < found && got == got_before && from == from_before)) {
+          for (int i = 0; i < found; ++i) {
+            const int g = __builtin_amdgcn_readlane(got, i), f = __builtin_amdgcn_readlane(from, i);
+            skip += i < lane && g == got && f == from;
+          }
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            const bool same = __builtin_amdgcn_ds_bpermute(from * 4, key[j]) == got;
+            if (same && skip-- == 0) id = from * E + j;
+          }
+        } else {
+#pragma unroll
+          for (int j = E - 1; j >= 0; --j)
+            if (__builtin_amdgcn_ds_bpermute(from * 4, key[j]) == got) id = from * E + j;
+        }
+        id = lane < found ? id : -1;
+        const float inv = __builtin_amdgcn_rcpf(sum);
+        float mine = exp_f32(of_wide_key(got) - top);
+        mine = sum != sum ? sum : mine;   // a NaN key's value is none
+        mine = lane < found ? mine : 0.0f;
+        const float scale = c.renormalise ? __builtin_amdgcn_rcpf(lanes_sum<kWave>(mine)) : inv;
+        gate = mine * scale;
+#pragma unroll
+        for (int j = 0; j < E; ++j) p_sum[j] += e[j] * inv;
+        if (c.dense) {
+#pragma unroll
+          for (int j = 0; j < E; ++j) z[j] = chosen >> j & 1 ? e[j] * scale : 0.0f;
+        }
+        ++n_rows;
+        n_picks += found;
+      }
+    }
+    if (lane < c.k) {
+      c.ids[r * c.k + lane] = id;
+      if (!c.dense) c.gates[r * c.k + lane] = gate;
+    }
+    if (c.dense) {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (first + j < c.n) c.gates[int64_t(first + j) * c.rows + r] = part ? z[j] : 0.0f;
+    }
   }
-  if (w.blocks == 1) {
-    __syncthreads();   // the workgroup sees its own sums
-    finish(c, w, room);
-  }
+  // rows were counted by every lane
+  write_sums<B, E, kWave>(c, w, p_sum, n_of, lane == 0 ? n_rows : 0, lane == 0 ? n_picks : 0, lds, lds_rows);
+  if (w.blocks == 1) finish<B>(c, w, room);
 }
 
 constexpr int kFinishBlock = 1024;
 __global__ __launch_bounds__(kFinishBlock) void route_finish_kernel(RouteCall c, RouteWork w) {
-  __shared__ double room[2 * kFinishBlock];
-  finish(c, w, room);
+  __shared__ double room[2 * (kFinishBlock + kWave)];
+  finish<kFinishBlock>(c, w, room);
 }
+
+// The same in many workgroups, kJoinColumns branches each, where there are many sums: counts,
+// slopes and the branches' share of the balance loss, which a last wave adds.
+constexpr int kJoinBlock = 1024;
+__global__ __launch_bounds__(kJoinBlock) void route_join_kernel(RouteCall c, RouteWork w) {
+  constexpr int kWaves = kJoinBlock / kWave, kSubs = kJoinBlock / kJoinColumns;
+  __shared__ double head[2][kWaves], lds[2][kWaves][kJoinColumns];
+  const int t = threadIdx.x, wave = t / kWave, sub = t / kJoinColumns, lane = t % kJoinColumns;
+  const int e = int(blockIdx.x) * kJoinColumns + lane;
+  double rows = 0, picks = 0, p = 0, n = 0;
+  for (int b = t; b < w.blocks; b += kJoinBlock) {
+    rows += w.rows[b];
+    picks += w.picks[b];
+  }
+  if (e < c.n) {
+#pragma unroll 8
+    for (int b = sub; b < w.blocks; b += kSubs) {
+      p += w.p[int64_t(b) * c.n + e];
+      n += w.chosen[int64_t(b) * c.n + e];
+    }
+  }
+  rows = wave_sum(rows);
+  picks = wave_sum(picks);
+#pragma unroll
+  for (int x = kJoinColumns; x < kWave; x *= 2) {
+    p += __shfl_xor(p, x);
+    n += __shfl_xor(n, x);
+  }
+  if (t % kWave == 0) head[0][wave] = rows, head[1][wave] = picks;
+  if (t % kWave < kJoinColumns) lds[0][wave][lane] = p, lds[1][wave][lane] = n;
+  __syncthreads();
+  if (t >= kWave) return;
+  rows = picks = p = n = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    rows += head[0][i];
+    picks += head[1][i];
+    p += lds[0][i][lane];
+    n += lds[1][i][lane];
+  }
+  const double factor = rows * picks > 0 ? double(c.n) / (rows * picks) : 0.0;
+  const bool mine = t < kJoinColumns && e < c.n;
+  if (mine) {
+    c.counts[e] = int32_t(n);
+    c.slope[e] = float(factor * n);
+  }
+  const double share = wave_sum(mine && factor > 0 ? factor * n * p : 0.0);
+  if (t == 0) w.shares[blockIdx.x] = share;
+}
+__global__ __launch_bounds__(kWave) void route_balance_kernel(RouteCall c, RouteWork w, int shares) {
+  const double all = wave_sum(int(threadIdx.x) < shares ? w.shares[threadIdx.x] : 0.0);
+  if (threadIdx.x == 0) c.balance[0] = float(all);
+}
+static_assert(kMaxBranches <= kWave * kJoinColumns, "a wave adds the shares");
 
 // ---- backward ----------------------------------------------------------------------
 
@@ -371,30 +681,56 @@ __global__ __launch_bounds__(kRouteBlock) void route_bwd_kernel(RouteCall c) {
 
 // ---- launches ----------------------------------------------------------------------
 
-// The forward's workgroups: one where they would take four turns at most; else no more than
-// leave 2^16 sums of a kind to join (256 at least, 1024 at most).
+// The forward's workgroups: one where it would take four turns at most; else no more than fill
+// the device.
 int route_blocks(int64_t rows, int n) {
-  const int lanes = n <= 16 ? 1 : n <= 64 ? 4 : n <= 256 ? 16 : 64;
-  const int64_t turns = (rows * lanes + kRouteBlock - 1) / kRouteBlock;
-  if (turns <= 4) return 1;
-  return int(std::min<int64_t>(turns, std::max(256, std::min(1024, 65536 / n))));
+  const int at_once = n <= 16 ? kRouteBlock : n <= 64 ? kRouteBlock / 4 : wide_block(n <= 512 ? 8 : 16) / kWave;
+  const int64_t turns = (rows + at_once - 1) / at_once;
+  return turns <= 4 ? 1 : int(std::min<int64_t>(turns, n <= 64 ? 1024 : n <= 256 ? 512 : 256));
+}
+RouteWork route_work(const RouteCall& c) {
+  RouteWork w;
+  w.blocks = route_blocks(c.rows, c.n);
+  w.shares = reinterpret_cast<double*>(c.work);
+  w.p = c.work + 2 * kWave;
+  w.chosen = reinterpret_cast<int32_t*>(w.p + int64_t(w.blocks) * c.n);
+  w.rows = w.chosen + int64_t(w.blocks) * c.n;
+  w.picks = w.rows + w.blocks;
+  return w;
+}
+// One workgroup joins up to 2^14 sums; measured with 256 blocks of 256 branches (2^16) it takes
+// 9.4 us, the two launches of many 7.
+void finish(const RouteCall& c, const RouteWork& w, hipStream_t s) {
+  if (w.blocks == 1) return;
+  if (c.n <= 64) {
+    hipLaunchKernelGGL(route_finish_kernel, dim3(1), dim3(kFinishBlock), 0, s, c, w);
+    return;
+  }
+  const int shares = (c.n + kJoinColumns - 1) / kJoinColumns;
+  hipLaunchKernelGGL(route_join_kernel, dim3(unsigned(shares)), dim3(kJoinBlock), 0, s, c, w);
+  hipLaunchKernelGGL(route_balance_kernel, dim3(1), dim3(kWave), 0, s, c, w, shares);
 }
 
 template <typename T, int E, int L>
-void run(const RouteCall& c, bool backward, hipStream_t s) {
-  if (backward) {
-    constexpr int64_t kMost = 4096;
-    const int64_t blocks = std::min((c.rows * L + kRouteBlock - 1) / kRouteBlock, kMost);
-    hipLaunchKernelGGL((route_bwd_kernel<T, E, L>), dim3(unsigned(blocks)), dim3(kRouteBlock), 0, s, c);
-    return;
-  }
-  RouteWork w;
-  w.blocks = route_blocks(c.rows, c.n);
-  w.p = c.work;
-  w.chosen = reinterpret_cast<int32_t*>(c.work + int64_t(w.blocks) * c.n);
-  w.rows = w.chosen + int64_t(w.blocks) * c.n;
+void backward(const RouteCall& c, hipStream_t s) {
+  constexpr int64_t kMost = 4096;
+  const int64_t blocks = std::min((c.rows * L + kRouteBlock - 1) / kRouteBlock, kMost);
+  hipLaunchKernelGGL((route_bwd_kernel<T, E, L>), dim3(unsigned(blocks)), dim3(kRouteBlock), 0, s, c);
+}
+template <typename T, int E, int L>
+void run(const RouteCall& c, bool back, hipStream_t s) {
+  if (back) return backward<T, E, L>(c, s);
+  const RouteWork w = route_work(c);
   hipLaunchKernelGGL((route_fwd_kernel<T, E, L>), dim3(unsigned(w.blocks)), dim3(kRouteBlock), 0, s, c, w);
-  if (w.blocks > 1) hipLaunchKernelGGL(route_finish_kernel, dim3(1), dim3(kFinishBlock), 0, s, c, w);
+  finish(c, w, s);
+}
+// n > 64: a wave to a row in the forward; Eb branches a lane and Lb lanes in the backward.
+template <typename T, int E, int Eb, int Lb>
+void run_wide(const RouteCall& c, bool back, hipStream_t s) {
+  if (back) return backward<T, Eb, Lb>(c, s);
+  const RouteWork w = route_work(c);
+  hipLaunchKernelGGL((route_fwd_wide_kernel<T, E>), dim3(unsigned(w.blocks)), dim3(wide_block(E)), 0, s, c, w);
+  finish(c, w, s);
 }
 template <typename T>
 hipError_t run(const RouteCall& c, bool backward, hipStream_t s) {
@@ -409,13 +745,13 @@ hipError_t run(const RouteCall& c, bool backward, hipStream_t s) {
   else if (c.n <= 64)
     run<T, 16, 4>(c, backward, s);
   else if (c.n <= 128)
-    run<T, 8, 16>(c, backward, s);
+    run_wide<T, 2, 8, 16>(c, backward, s);
   else if (c.n <= 256)
-    run<T, 16, 16>(c, backward, s);
+    run_wide<T, 4, 16, 16>(c, backward, s);
   else if (c.n <= 512)
-    run<T, 8, 64>(c, backward, s);
+    run_wide<T, 8, 8, 64>(c, backward, s);
   else
-    run<T, 16, 64>(c, backward, s);
+    run_wide<T, 16, 16, 64>(c, backward, s);
   return hipGetLastError();
 }
 hipError_t run(const RouteCall& c, Elem type, bool backward, hipStream_t s) {
@@ -467,7 +803,7 @@ __global__ __launch_bounds__(kGateBlock) void gate_bwd_kernel(GateCall c) {
 
 }  // namespace
 
-size_t route_floats(int64_t rows, int n) { return size_t(route_blocks(rows, n)) * (2 * size_t(n) + 1); }
+size_t route_floats(int64_t rows, int n) { return 2 * kWave + size_t(route_blocks(rows, n)) * (2 * size_t(n) + 2); }
 hipError_t launch_route_forward(const RouteCall& c, Elem type, hipStream_t s) { return run(c, type, false, s); }
 hipError_t launch_route_backward(const RouteCall& c, Elem type, hipStream_t s) { return run(c, type, true, s); }
 
