@@ -173,8 +173,7 @@ def route_forward(logits, k: int, mask=None, renormalise: bool = False, dense: b
     ids = logits.new_empty((rows, k), dtype=torch.int32)
     gates = logits.new_empty((n, rows) if dense else (rows, k), dtype=torch.float32)
     counts = logits.new_empty(n, dtype=torch.int32)
-    loss = logits.new_empty(1 + n, dtype=torch.float32)
-    balance, slope = loss[:1], loss[1:]
+    balance, slope = logits.new_empty(1, dtype=torch.float32), logits.new_empty(n, dtype=torch.float32)
     check(lib.cgtp_route_forward(ELEM[logits.dtype], rows, n, k, logits.data_ptr(), ld, at_mask, renormalise, dense,
                                  ids.data_ptr(), gates.data_ptr(), counts.data_ptr(), balance.data_ptr(),
                                  slope.data_ptr(), *_room(workspace, dev), _raw_stream(dev)))
