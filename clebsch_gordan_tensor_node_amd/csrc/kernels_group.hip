@@ -28,29 +28,32 @@
 namespace cgtp {
 namespace {
 
-// exp(x): 2^t with t = x log2(e) rounded, and in fp32 times 1 + what the rounding left out
-// (some 2 ulp; in 16 bits an error of |x| 2^-24 of it is nothing).
+// exp(x): 2^t with t = x log2(e) rounded, in fp32 times e^(x - t ln 2), of which 1 and the small
+// exponent are enough (some 2 ulp; in 16 bits an error of |x| 2^-24 of it is nothing).  Beyond
+// 200 it is 0 or infinity either way.
 template <bool Exact>
 __device__ inline float exp_of(float x) {
-  constexpr float kLog2e = 1.44269504f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
-  const float t = x * kLog2e, p = __builtin_amdgcn_exp2f(t);
-  if constexpr (!Exact) return p;
-  const float rest = fmaf(x, kRest, fmaf(x, kLog2e, -t));
-  // where p is 0 or infinity (or x is) the rest may be NaN and has no say
-  return p > 0 && p < __builtin_inff() ? fmaf(p, rest * kLn2, p) : p;
+  constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+  if constexpr (!Exact) return __builtin_amdgcn_exp2f(x * kLog2e);
+  x = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);
+  const float t = x * kLog2e;
+  return __builtin_amdgcn_exp2f(t) * (1.0f + fmaf(t, -kLn2, x));
 }
 // (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2).  Of x = |z| / sqrt 2, 1 - erf(x) = exp(-x^2) times a
 // polynomial in 1 / (1 + 0.3275911 x) to 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical
 // Functions, 7.1.26), some 2.5 of fp32's roundings of 1.
 template <bool Exact>
 __device__ inline float normal_cdf(float z, float& density) {
-  density = exp_of<Exact>(-0.5f * z * z);
+  if constexpr (Exact)
+    density = exp_of<true>(-0.5f * z * z);
+  else
+    density = __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.44269504f));
   const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.707106781f, 1.0f));
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  q *= 0.5f * t * density;
+  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  q = fmaf(t, q, 0.5f * 1.421413741f);
+  q = fmaf(t, q, 0.5f * -0.284496736f);
+  q = fmaf(t, q, 0.5f * 0.254829592f);
+  q *= t * density;
   return z < 0 ? q : 1.0f - q;
 }
 
@@ -332,25 +335,6 @@ __device__ inline void activated(const Vec<T, V>& r, const Scales<V>& k, Act act
   });
 }
 
-// What the backward needs at a place: h = (x - mean) rstd, d = g act'(h w + b).
-template <int V>
-struct Slopes {
-  float mean[V], rstd[V], w[V], b[V];
-};
-template <typename T, int V>
-__device__ inline void slopes(const Vec<T, V>& x, const Vec<T, V>& g, const Slopes<V>& k, Act act, float (&h)[V],
-                              float (&d)[V]) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    h[j] = (to_f32(x.v[j]) - k.mean[j]) * k.rstd[j];
-    d[j] = to_f32(g.v[j]);
-  }
-  with_act(act, [&](auto a) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) d[j] *= act_slope<a(), sizeof(T) == 4>(fmaf(h[j], k.w[j], k.b[j]));
-  });
-}
-
 // The statistics of a place's columns, of sample s.
 template <int V>
 __device__ inline void place_stats(const GroupCall& c, const int (&group)[V], const float* stats, int64_t s,
@@ -374,6 +358,74 @@ __device__ inline void place_groups(const GroupLayout& y, const Place<V>& p, int
     for (int j = 0; j < V; ++j) group[j] = p.in && p.has(j) ? (p.at + j) / y.per_group : 0;
   }
 }
+
+// What the backward needs at a place: of x - mean its slope d = g act'(z), z = (x - mean) scale
+// + shift; h stands as (x - mean) rstd in the sums and means that it is part of.
+template <typename T, int V>
+__device__ inline void slopes(const Vec<T, V>& x, const Vec<T, V>& g, const Scales<V>& k, Act act, float (&xm)[V],
+                              float (&d)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    xm[j] = to_f32(x.v[j]) - k.mean[j];
+    d[j] = to_f32(g.v[j]);
+  }
+  with_act(act, [&](auto a) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] *= act_slope<a(), sizeof(T) == 4>(fmaf(xm[j], k.scale[j], k.shift[j]));
+  });
+}
+// The backward's constants of a sample: mean, rstd w and b, with w and b given, and rstd.
+template <typename T, int V>
+struct Back {
+  Scales<V> k;
+  float rstd[V], w[V];
+  __device__ Back(const GroupCall& c, const Place<V>& p) {
+    place_weights<T>(p, c.weight, c.weight_f32, 1.0f, w);
+    place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.shift);
+  }
+  __device__ void sample(const GroupCall& c, const int (&group)[V], int64_t s) {
+    place_stats(c, group, c.stats, s, k.mean, rstd);
+#pragma unroll
+    for (int j = 0; j < V; ++j) k.scale[j] = rstd[j] * w[j];
+  }
+};
+// dx = rstd (d w - ma - h mh), ma and mh the means of a and of a h: d (rstd w) less
+// (x - mean) (rstd^2 mh) and rstd ma.
+template <typename T, int V>
+struct Means {
+  float along[V], all[V];
+  __device__ void set(const Back<T, V>& k, const float (&ma)[V], const float (&mh)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      along[j] = -k.rstd[j] * k.rstd[j] * mh[j];
+      all[j] = -k.rstd[j] * ma[j];
+    }
+  }
+  __device__ void apply(const Back<T, V>& k, Act act, const Vec<T, V>& x, const Vec<T, V>& g, float (&out)[V]) const {
+    float xm[V];
+    slopes(x, g, k.k, act, xm, out);
+#pragma unroll
+    for (int j = 0; j < V; ++j) out[j] = fmaf(out[j], k.k.scale[j], fmaf(xm[j], along[j], all[j]));
+  }
+};
+// A thread's sums of d and d h per column.
+template <typename T, int V>
+struct Sums {
+  float d[V] = {}, h[V] = {};   // h: of d (x - mean), until done
+  __device__ void add(const Back<T, V>& k, Act act, const Vec<T, V>& x, const Vec<T, V>& g) {
+    float xm[V], v[V];
+    slopes(x, g, k.k, act, xm, v);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      d[j] += v[j];
+      h[j] = fmaf(v[j], xm[j], h[j]);
+    }
+  }
+  __device__ void done(const Back<T, V>& k) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) h[j] *= k.rstd[j];
+  }
+};
 
 // A thread's sums of d and d h per column, added over the slices in a fixed order: column e's
 // are lds[e] and lds[n + e] afterwards, n the returned number.
@@ -663,20 +715,10 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
     const int64_t step_x = int64_t(y.slices) * c.ld_x, step_g = int64_t(y.slices) * c.ld_g;
     int group[V];
     place_groups(y, p, group);
-    Slopes<V> k;
-    place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
-    place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
-    place_stats(c, group, c.stats, s, k.mean, k.rstd);
-    float sd[V] = {}, sh[V] = {};
-    auto add = [&](const Vec<T, V>& vx, const Vec<T, V>& vg) {
-      float h[V], d[V];
-      slopes(vx, vg, k, c.act, h, d);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        sd[j] += d[j];
-        sh[j] += d[j] * h[j];
-      }
-    };
+    Back<T, V> k(c, p);
+    k.sample(c, group, s);
+    Sums<T, V> sum;
+    auto add = [&](const Vec<T, V>& vx, const Vec<T, V>& vg) { sum.add(k, c.act, vx, vg); };
     if (own.most > N) for_row_pairs<T, V, kBeside>(c, p, y.slices, rest, end, add);
     Held<T, V> hx[N], hg[N];
     const T *at_x = x, *at_g = g;
@@ -693,7 +735,8 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (i < left) add(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]));
-    const int n = column_sums(p, q, y.slices, sd, sh, lds);
+    sum.done(k);
+    const int n = column_sums(p, q, y.slices, sum.d, sum.h, lds);
     // the columns' sums, for the weights' gradients
     for (int e = threadIdx.x; e < q.cw; e += B) {
       if (join) {
@@ -733,11 +776,11 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
       }
       T* out = static_cast<T*>(c.y) + int64_t(begin + p.slice) * c.ld_y;
       const int64_t step_y = int64_t(y.slices) * c.ld_y;
+      Means<T, V> means;
+      means.set(k, ma, mh);
       auto apply = [&](const Vec<T, V>& vx, const Vec<T, V>& vg) {
-        float h[V], d[V];
-        slopes(vx, vg, k, c.act, h, d);
-#pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
+        float d[V];
+        means.apply(k, c.act, vx, vg, d);
         store_own(p, out, d, y.stream);
       };
       const int again = afresh(own.mine);
@@ -931,22 +974,14 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_sum_kernel(GroupCall c, 
   const Place<V> p(q, y);
   int group[V];
   place_groups(y, p, group);
-  Slopes<V> k;
-  place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
-  place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
+  Back<T, V> k(c, p);
   for_pieces(c, y, t, [&](int64_t s, int lo, int hi) {
-    place_stats(c, group, c.stats, s, k.mean, k.rstd);
-    float sd[V] = {}, sh[V] = {};
-    for_row_pairs<T, V, kInFlight / 2>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
-      float h[V], d[V];
-      slopes(x, g, k, c.act, h, d);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        sd[j] += d[j];
-        sh[j] += d[j] * h[j];
-      }
-    });
-    const int n = column_sums(p, q, y.slices, sd, sh, lds);
+    k.sample(c, group, s);
+    Sums<T, V> sum;
+    for_row_pairs<T, V, kInFlight / 2>(c, p, y.slices, lo, hi,
+                                       [&](const Vec<T, V>& x, const Vec<T, V>& g) { sum.add(k, c.act, x, g); });
+    sum.done(k);
+    const int n = column_sums(p, q, y.slices, sum.d, sum.h, lds);
     float* at = pieces + (t.tile + s) * 2 * c.width + q.c0;
     for (int e = threadIdx.x; e < q.cw; e += kTileBlock) {
       at[e] = lds[e];
@@ -1076,11 +1111,9 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c
   const Place<V> p(q, y);
   int group[V];
   place_groups(y, p, group);
-  Slopes<V> k;
-  place_weights<T>(p, c.weight, c.weight_f32, 1.0f, k.w);
-  place_weights<T>(p, c.bias, c.weight_f32, 0.0f, k.b);
+  Back<T, V> k(c, p);
   for_pieces(c, y, t, [&](int64_t s, int lo, int hi) {
-    place_stats(c, group, c.stats, s, k.mean, k.rstd);
+    k.sample(c, group, s);
     float ma[V], mh[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -1088,12 +1121,12 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c
       ma[j] = at[0];
       mh[j] = at[1];
     }
+    Means<T, V> means;
+    means.set(k, ma, mh);
     T* out = static_cast<T*>(c.y) + int64_t(lo + p.slice) * c.ld_y;
     for_row_pairs<T, V, kInFlight / 2>(c, p, y.slices, lo, hi, [&](const Vec<T, V>& x, const Vec<T, V>& g) {
-      float h[V], d[V];
-      slopes(x, g, k, c.act, h, d);
-#pragma unroll
-      for (int j = 0; j < V; ++j) d[j] = (d[j] * k.w[j] - ma[j] - h[j] * mh[j]) * k.rstd[j];
+      float d[V];
+      means.apply(k, c.act, x, g, d);
       store_own(p, out, d, y.stream);
       out += int64_t(y.slices) * c.ld_y;
     });
