@@ -389,23 +389,22 @@ struct Back {
     for (int j = 0; j < V; ++j) k.scale[j] = rstd[j] * w[j];
   }
 };
-// dx = rstd (d w - ma - h mh), ma and mh the means of a and of a h: d (rstd w) less
-// (x - mean) (rstd^2 mh) and rstd ma.
+// dx = rstd (d w - ma - h mh), ma and mh the means of a and of a h.
 template <typename T, int V>
 struct Means {
-  float along[V], all[V];
+  float along[V], all[V];   // rstd mh, ma
   __device__ void set(const Back<T, V>& k, const float (&ma)[V], const float (&mh)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      along[j] = -k.rstd[j] * k.rstd[j] * mh[j];
-      all[j] = -k.rstd[j] * ma[j];
+      along[j] = k.rstd[j] * mh[j];
+      all[j] = ma[j];
     }
   }
   __device__ void apply(const Back<T, V>& k, Act act, const Vec<T, V>& x, const Vec<T, V>& g, float (&out)[V]) const {
     float xm[V];
     slopes(x, g, k.k, act, xm, out);
 #pragma unroll
-    for (int j = 0; j < V; ++j) out[j] = fmaf(out[j], k.k.scale[j], fmaf(xm[j], along[j], all[j]));
+    for (int j = 0; j < V; ++j) out[j] = fmaf(out[j], k.w[j], -fmaf(xm[j], along[j], all[j])) * k.rstd[j];
   }
 };
 // A thread's sums of d and d h per column.

@@ -1,7 +1,7 @@
 """Trains a one-layer equivariant potential with the library's kernels: the whole path that
 a network around the convolution takes, on synthetic energies.
 
-    python examples/train_potential.py [--steps 200] [--bits 8] [--workload tiny]
+    python examples/train_potential.py [--steps 200] [--bits 8] [--workload tiny] [--branches 3]
 
 Every edge's convolution weights come from a radial network (layer norm inside), the
 convolution's output is normalised term by term (irreps norm), its scalars give the
@@ -9,6 +9,10 @@ energy, and the gradients pass back through the same operators into AdamW, clipp
 their norm on the device.  Dense products and pointwise functions are torch's.  The
 operators have first derivatives only: a second one (create_graph=True, forces in the loss)
 raises.
+
+With --branches the edges are routed: a group norm with its activation over all edges' hidden
+rows, logits from them, and two of the branches for each edge, every branch a convolution
+with weights of its own that takes its edges' gates.  A balance loss keeps the branches busy.
 """
 import argparse
 import math
@@ -81,10 +85,60 @@ class Conv(torch.autograd.Function):
                                                                               need=("x", "w"))[:2], grad.contiguous(), x, w))
 
 
+class GroupNorm(torch.autograd.Function):
+    """Group norm with its activation, all rows one sample."""
+
+    @staticmethod
+    def forward(ctx, x, groups, weight, bias):
+        y, stats = C.group_norm_forward(x, groups, weight, bias, activation="silu")
+        ctx.groups = groups
+        ctx.save_for_backward(x, stats, weight, bias)
+        return y
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, stats, weight, bias = ctx.saved_tensors
+        gx, gw, gb = Derivative.apply(lambda g, x, w, b: C.group_norm_backward(g, x, stats, ctx.groups, w, b, activation="silu"),
+                                      grad.contiguous(), x, weight, bias)
+        return gx, None, gw, gb
+
+
+class Routing(torch.autograd.Function):
+    """Gates [branches, edges] and balance loss [1] of the edges' logits."""
+
+    @staticmethod
+    def forward(ctx, logits, k):
+        ctx.route = C.route_forward(logits, k, renormalise=True, dense=True)
+        ctx.save_for_backward(logits)
+        return ctx.route.gates, ctx.route.balance
+
+    @staticmethod
+    def backward(ctx, grad_gates, grad_balance):
+        logits, = ctx.saved_tensors
+        return Derivative.apply(lambda g, b, z: C.route_backward(z, ctx.route, g, b), grad_gates.contiguous(),
+                                grad_balance.contiguous(), logits), None
+
+
+class GatedConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, graph, x, w, gate):
+        ctx.plan, ctx.graph = plan, graph
+        ctx.save_for_backward(x, w, gate)
+        return C.conv_forward(plan, *graph, x, w, gate=gate)
+
+    @staticmethod
+    def backward(ctx, grad):
+        def call(g, x, w, gate):
+            gx, gw, _ = C.conv_backward(ctx.plan, *ctx.graph, x, w, g, gate=gate, need=("x", "w"))
+            return gx, gw, C.conv_gate_backward(w, gw, gate)
+        return (None, None, *Derivative.apply(call, grad.contiguous(), *ctx.saved_tensors))
+
+
 class Potential:
     """Parameters and energy of the network on a fixed neighbour list."""
 
-    def __init__(self, wl, device, n_radial=16, hidden=64, seed=0):
+    def __init__(self, wl, device, n_radial=16, hidden=64, seed=0, branches=0):
+        self.branches, self.groups = branches, 8
         gen = torch.Generator().manual_seed(seed)
         pos, box, cell, _ = WL.positions(wl)
         self.pos = torch.from_numpy(pos).to(device)
@@ -110,30 +164,48 @@ class Potential:
              "norm_weight": (torch.ones(self.norm.n_weights, device=device), 0.0),
              "norm_bias": (torch.zeros(self.norm.n_biases, device=device), 0.0),
              "readout": (normal(self.norm.n_biases, 1, scale=1 / math.sqrt(self.norm.n_biases)), 0.01)}
+        if branches:
+            p["router"] = (normal(hidden, branches, scale=1 / math.sqrt(hidden)), 0.0)
+            p["radial_out"] = (normal(branches, hidden, w, scale=1 / math.sqrt(hidden)), 0.01)
         self.names = list(p)
         self.values = [v.requires_grad_() for v, _ in p.values()]
         self.decay = [d for _, d in p.values()]
 
     def energies(self):
         """One energy per atom [n]: the normalised scalars of the convolution, read out."""
+        return self.energies_and_balance()[0]
+
+    def energies_and_balance(self):
+        """The energies, and the routing's balance loss (0 without branches)."""
         q = dict(zip(self.names, self.values))
-        hidden = LayerNorm.apply(self.basis @ q["radial_in"], q["ln_weight"], q["ln_bias"])
+        rows, balance = self.basis @ q["radial_in"], 0.0
+        if self.branches:
+            hidden = GroupNorm.apply(rows, self.groups, q["ln_weight"], q["ln_bias"])
+            gates, balance = Routing.apply(hidden @ q["router"], min(2, self.branches))
+            conv = sum(GatedConv.apply(self.plan, self.graph, q["x"], hidden @ q["radial_out"][b], gates[b])
+                       for b in range(self.branches))
+            return self.read_out(conv, q), balance.squeeze(0)
+        hidden = LayerNorm.apply(rows, q["ln_weight"], q["ln_bias"])
         w = torch.nn.functional.silu(hidden) @ q["radial_out"]
-        out = IrrepsNorm.apply(self.norm, Conv.apply(self.plan, self.graph, q["x"], w), q["norm_weight"], q["norm_bias"])
+        return self.read_out(Conv.apply(self.plan, self.graph, q["x"], w), q), balance
+
+    def read_out(self, conv, q):
+        out = IrrepsNorm.apply(self.norm, conv, q["norm_weight"], q["norm_bias"])
         return (out[:, :self.norm.n_biases] @ q["readout"]).squeeze(1)   # 0e terms lead the output irreps
 
 
-def train(workload="tiny", steps=200, bits=32, lr=1e-2, device="cuda:0", report=None):
-    """The losses of `steps` steps towards random target energies."""
-    net = Potential(WL.WORKLOADS[workload], torch.device(device))
+def train(workload="tiny", steps=200, bits=32, lr=1e-2, device="cuda:0", report=None, branches=0):
+    """The losses of `steps` steps towards random target energies (the balance loss apart)."""
+    net = Potential(WL.WORKLOADS[workload], torch.device(device), branches=branches)
     target = torch.randn(net.pos.shape[0], generator=torch.Generator().manual_seed(1)).to(device)
     params = C.ParamSet(net.values, net.decay)
     values = params.pointers([v.detach() for v in net.values])   # the same storage
     state = C.adamw_state(params, bits)
     losses = []
     for t in range(1, steps + 1):
-        loss = (net.energies() - target).square().mean()
-        grads = params.pointers([g.contiguous() for g in torch.autograd.grad(loss, net.values)])
+        energies, balance = net.energies_and_balance()
+        loss = (energies - target).square().mean()
+        grads = params.pointers([g.contiguous() for g in torch.autograd.grad(loss + 0.01 * balance, net.values)])
         factor = C.grad_norm(params, grads, max_norm=1.0)[1:]
         C.adamw_step(params, values, grads, state, lr=lr, step=t, grad_scale=factor, seed=t)
         losses.append(loss.detach())
@@ -147,6 +219,7 @@ if __name__ == "__main__":
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--bits", type=int, choices=(8, 32), default=32, help="of AdamW's moments")
     ap.add_argument("--workload", default="tiny", choices=("tiny", "c1_768", "c2_768", "si_mask"))
+    ap.add_argument("--branches", type=int, default=0, help="branches that edges are routed to (0: one convolution)")
     a = ap.parse_args()
-    got = train(a.workload, a.steps, a.bits, report=max(1, a.steps // 10))
+    got = train(a.workload, a.steps, a.bits, report=max(1, a.steps // 10), branches=a.branches)
     print(f"loss {got[0]:.4f} -> {got[-1]:.4f}")

@@ -438,8 +438,9 @@ enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1, CGTP_ACT_GELU = 2 };
  * longest: rows of the longest sample, as far as the caller knows (0: not known).  It chooses
  * between launches, nothing else: a call with another value is as right, and slower where a
  * sample much longer than told falls to one workgroup.
- * workspace: 256-byte aligned, cgtp_group_norm_workspace_size bytes (0: NULL).  Rows of at
- * most 2^24 values.  No atomics: bitwise reproducible. */
+ * workspace: 256-byte aligned, cgtp_group_norm_workspace_size bytes (0: NULL); calls that may
+ * run at the same time, replayed graphs among them, need one each.  Rows of at most 2^24
+ * values.  No atomics: bitwise reproducible. */
 int cgtp_group_norm_workspace_size(int backward, int dtype, int64_t n_rows, int64_t width, int64_t n_groups,
                                    int64_t n_samples, const int32_t* offsets, int64_t longest, size_t* bytes);
 int cgtp_group_norm_forward(int dtype, int64_t n_rows, int64_t width, int64_t n_groups, int64_t n_samples,
@@ -475,7 +476,7 @@ int cgtp_group_norm_backward(int dtype, int64_t n_rows, int64_t width, int64_t n
  * A row whose logits hold NaN or +infinity has NaN gates and makes balance NaN.
  * 1 <= n <= 1024, 1 <= k <= min(n, 64).  Sums over rows in a fixed order, joined in fp64; no
  * atomics: bitwise reproducible.  workspace: 256-byte aligned, cgtp_route_workspace_size
- * bytes (0: NULL). */
+ * bytes; calls that may run at the same time need one each. */
 int cgtp_route_workspace_size(int64_t n_rows, int n, size_t* bytes);
 int cgtp_route_forward(int dtype, int64_t n_rows, int n, int k, const void* logits, int64_t ld, const uint8_t* mask,
                        int renormalise, int dense, int32_t* ids, float* gates, int32_t* counts, float* balance,

@@ -688,3 +688,19 @@ def test_argument_checks(dev):
         assert err.value.code == code
     ws = ctypes.c_size_t()
     assert C._lib.load().cgtp_group_norm_workspace_size(0, 0, 6, 8, 2, 1, None, 0, ctypes.byref(ws)) == 0
+
+
+def test_group_norm_of_small_values(dev):
+    # without eps, x 2^-60 has the same y and gradients 2^60 times as large, bit for bit: every step
+    # scales by a power of two, and nothing leaves fp32's normal range
+    rng = np.random.default_rng(13)
+    for longest in (None, 3000):
+        x, _ = _rows(rng, 3000, 24, F32, dev)
+        g, _ = _rows(rng, 3000, 24, F32, dev)
+        args = dict(samples=_offsets([0, 1000, 3000], dev), activation="silu", longest=longest)
+        y, st = C.group_norm_forward(x, 4, eps=0.0, **args)
+        y2, st2 = C.group_norm_forward(x * 2.0 ** -60, 4, eps=0.0, **args)
+        assert torch.equal(y, y2) and torch.equal(st[1] * 2.0 ** 60, st2[1])
+        gx, gw, gb = C.group_norm_backward(g, x, st, 4, **args)
+        gx2, gw2, gb2 = C.group_norm_backward(g, x * 2.0 ** -60, st2, 4, **args)
+        assert torch.equal(gx * 2.0 ** 60, gx2) and torch.equal(gw, gw2) and torch.equal(gb, gb2)
