@@ -229,12 +229,13 @@ __device__ inline void finish(const RouteCall& c, const RouteWork& w, double* ld
 
 // A workgroup's sums from its threads': lanes of a wave that hold the same branches, then
 // waves.  lds: B / kWave * L * E floats.
+// `sums`: 2 where the choices are counted in n_of, 1 where they are elsewhere.
 template <int B, int E, int L>
 __device__ inline void write_sums(const RouteCall& c, const RouteWork& w, const float (&p_sum)[E], const int (&n_of)[E],
-                                  int n_rows, int n_picks, float* lds, int32_t* lds_rows) {
+                                  int n_rows, int n_picks, float* lds, int32_t* lds_rows, int sums) {
   constexpr int kWaves = B / kWave;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  for (int what = 0; what < 2; ++what) {
+  for (int what = 0; what < sums; ++what) {
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const float v = same_sum<L>(what ? float(n_of[j]) : p_sum[j]);   // counts below 2^24: exact
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_fwd_kernel(RouteCall c, Rou
     __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
-  write_sums<kRouteBlock, E, L>(c, w, p_sum, n_of, n_rows, 0, lds, lds_rows);   // (the last step adds the choices itself)
+  write_sums<kRouteBlock, E, L>(c, w, p_sum, n_of, n_rows, 0, lds, lds_rows, 2);   // (the last step adds the choices itself)
   if (w.blocks == 1) finish<kRouteBlock>(c, w, room);   // the workgroup sees its own sums
 }
 
@@ -379,8 +380,20 @@ __device__ inline int wave_max(int v) {
   v = max_dpp<0x143, 0xc>(v);   // row_bcast 31: rows 2 and 3
   return __builtin_amdgcn_readlane(v, kWave - 1);
 }
-__device__ inline float scalar(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+template <int Ctrl, int Rows>
+__device__ inline float add_dpp(float v) {
+  const int b = __builtin_bit_cast(int, v);
+  if constexpr (Rows == 0xf) return v + dpp<Ctrl>(v);
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, Ctrl, Rows, 0xf, false));
+}
+__device__ inline float wave_total(float v) {
+  v = add_dpp<0xB1, 0xf>(v);
+  v = add_dpp<0x4E, 0xf>(v);
+  v = add_dpp<0x141, 0xf>(v);
+  v = add_dpp<0x140, 0xf>(v);
+  v = add_dpp<0x142, 0xa>(v);   // rows 1 and 3 are pairs of rows
+  v = add_dpp<0x143, 0xc>(v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), kWave - 1));
 }
 __device__ inline int wide_key(float z) {
   const int b = __builtin_bit_cast(int, z + 0.0f);
@@ -416,12 +429,14 @@ __global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void ro
   constexpr int B = wide_block(E), kWaves = B / kWave;
   __shared__ __align__(16) float lds[kWaves * kWave * E];
   __shared__ double room[2 * (B + kWave)];
-  __shared__ int32_t lds_rows[2 * kWaves];
+  __shared__ int32_t lds_rows[2 * kWaves], hist[kWave * E];   // hist: choices of each branch
   const int lane = threadIdx.x % kWave, first = lane * E;
   float p_sum[E];
-  int n_of[E], n_rows = 0, n_picks = 0;
+  int n_rows = 0, n_picks = 0;
 #pragma unroll
-  for (int j = 0; j < E; ++j) p_sum[j] = 0, n_of[j] = 0;
+  for (int j = 0; j < E; ++j) p_sum[j] = 0;
+  for (int e = threadIdx.x; e < c.n; e += B) hist[e] = 0;
+  __syncthreads();
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave);
   // the next row's logits are on their way while a row is routed
   const int64_t r0 = int64_t(blockIdx.x) * kWaves + wave, step = int64_t(gridDim.x) * kWaves;
@@ -435,12 +450,12 @@ __global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void ro
   for (int64_t r = r0; r < c.rows; r += step) {
     int id = -1;
     float gate = 0;
-    float z[E];            // then exp(z - top), of the chosen; 0 of the others
-    bool part = next_in;   // the row takes part
+    float z[E];
+    const bool in = next_in;
 #pragma unroll
     for (int j = 0; j < E; ++j) z[j] = next[j];
     read(r + step);
-    if (part) {
+    if (in) {
       int key[E], s[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) s[j] = key[j] = wide_key(z[j]);
@@ -453,7 +468,7 @@ __global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void ro
         e[j] = exp_f32(z[j] - top);
         sum += e[j];
       }
-      sum = scalar(lanes_sum<kWave>(sum));
+      sum = wave_total(sum);
       if (!(sum < __builtin_inff())) {
         // no number on top: NaN above infinity above the others, or all -infinity
 #pragma unroll
@@ -464,48 +479,24 @@ __global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void ro
         sort_keys(s);
         m = wave_max(s[0]);
       }
-      part = m > kMinusInf;
-      if (part) {
+      if (m > kMinusInf) {
         int got = kMinusInf, from = 0;   // lane i's: the i-th choice's key and lane
-        int found = 0, last = m;
+        int found = 0;
         do {
           const int at = __builtin_ctzll(__ballot(s[0] == m));
-          const bool mine = lane == at;
+          const bool mine = __builtin_amdgcn_inverse_ballot_w64(uint64_t(1) << at);
 #pragma unroll
           for (int j = 0; j + 1 < E; ++j) {
             const int above = s[j], below = s[j + 1];   // values: of two elements it would select the index
             s[j] = mine ? below : above;
           }
           if (mine) s[E - 1] = kLowest;
-          if (lane == found) got = m, from = at;
-          last = m;
+          const bool next_one = __builtin_amdgcn_inverse_ballot_w64(uint64_t(1) << found);
+          got = next_one ? m : got;
+          from = next_one ? at : from;
           if (++found == c.k) break;
           m = wave_max(s[0]);
         } while (m > kMinusInf);
-        // A lane's chosen keys are above the first that is left.  One that is left may equal the
-        // last choice's: of equal ones the lane's first are chosen then, as many as it gave.
-        uint32_t chosen = 0;
-        if (__ballot(s[0] == last)) {
-          int taken = 0, above = 0;
-          for (int i = 0; i < found; ++i) taken += __builtin_amdgcn_readlane(from, i) == lane;
-#pragma unroll
-          for (int j = 0; j < E; ++j) above += key[j] > s[0];
-#pragma unroll
-          for (int j = 0; j < E; ++j) {
-            const bool more = key[j] == s[0] && above < taken;
-            above += more;
-            chosen |= key[j] > s[0] || more ? 1u << j : 0u;
-          }
-#pragma unroll
-          for (int j = 0; j < E; ++j) n_of[j] += chosen >> j & 1;
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j) n_of[j] += key[j] > s[0];
-          if (c.dense) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) chosen |= key[j] > s[0] ? 1u << j : 0u;
-          }
-        }
         // a choice's branch is the first of its lane's that has the key, or the one behind where
         // the choice before was of the same lane and key
         const int got_before = __builtin_amdgcn_update_dpp(kLowest, got, 0x138, 0xf, 0xf, false);   // wave_shr 1
@@ -527,18 +518,15 @@ __global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void ro
             if (__builtin_amdgcn_ds_bpermute(from * 4, key[j]) == got) id = from * E + j;
         }
         id = lane < found ? id : -1;
+        if (lane < found) atomicAdd(hist + id, 1);   // whole numbers: in any order
         const float inv = __builtin_amdgcn_rcpf(sum);
         float mine = exp_f32(of_wide_key(got) - top);
         mine = sum != sum ? sum : mine;   // a NaN key's value is none
         mine = lane < found ? mine : 0.0f;
-        const float scale = c.renormalise ? __builtin_amdgcn_rcpf(lanes_sum<kWave>(mine)) : inv;
+        const float scale = c.renormalise ? __builtin_amdgcn_rcpf(wave_total(mine)) : inv;
         gate = mine * scale;
 #pragma unroll
         for (int j = 0; j < E; ++j) p_sum[j] += e[j] * inv;
-        if (c.dense) {
-#pragma unroll
-          for (int j = 0; j < E; ++j) z[j] = chosen >> j & 1 ? e[j] * scale : 0.0f;
-        }
         ++n_rows;
         n_picks += found;
       }
@@ -548,14 +536,26 @@ __global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void ro
       if (!c.dense) c.gates[r * c.k + lane] = gate;
     }
     if (c.dense) {
+      float out[E] = {};
+      for (int i = 0; i < c.k; ++i) {
+        const int of = __builtin_amdgcn_readlane(id, i);
+        const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, gate), i));
+#pragma unroll
+        for (int j = 0; j < E; ++j) out[j] = first + j == of ? v : out[j];
+      }
 #pragma unroll
       for (int j = 0; j < E; ++j)
-        if (first + j < c.n) c.gates[int64_t(first + j) * c.rows + r] = part ? z[j] : 0.0f;
+        if (first + j < c.n) c.gates[int64_t(first + j) * c.rows + r] = out[j];
     }
   }
   // rows were counted by every lane
-  write_sums<B, E, kWave>(c, w, p_sum, n_of, lane == 0 ? n_rows : 0, lane == 0 ? n_picks : 0, lds, lds_rows);
-  if (w.blocks == 1) finish<B>(c, w, room);
+  const int none[E] = {};
+  write_sums<B, E, kWave>(c, w, p_sum, none, lane == 0 ? n_rows : 0, lane == 0 ? n_picks : 0, lds, lds_rows, 1);
+  for (int e = threadIdx.x; e < c.n; e += B) w.chosen[int64_t(blockIdx.x) * c.n + e] = hist[e];
+  if (w.blocks == 1) {
+    __syncthreads();
+    finish<B>(c, w, room);
+  }
 }
 
 constexpr int kFinishBlock = 1024;
