@@ -167,7 +167,7 @@ def route_forward(logits, k: int, mask=None, renormalise: bool = False, dense: b
     if workspace is None:
         b = ctypes.c_size_t()
         check(lib.cgtp_route_workspace_size(rows, n, ctypes.byref(b)))
-        workspace = logits.new_empty(b.value, dtype=torch.uint8)
+        workspace = logits.new_empty(b.value, dtype=torch.uint8) if b.value else None
     if not 1 <= k <= n:
         raise ValueError(f"{k} of {n} branches: need 1 <= k <= n")
     ids = logits.new_empty((rows, k), dtype=torch.int32)

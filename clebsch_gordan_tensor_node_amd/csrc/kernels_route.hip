@@ -141,6 +141,15 @@ struct RouteWork {
   int blocks;
 };
 constexpr int kJoinColumns = 16;
+// One workgroup alone has its sums of up to N branches in LDS.
+template <int N>
+struct RouteOwn {
+  float p[N];
+  int32_t chosen[N], rows, picks;
+  __device__ RouteWork or_of(const RouteWork& w) {
+    return w.blocks > 1 ? w : RouteWork{nullptr, p, chosen, &rows, &picks, 1};
+  }
+};
 
 // Sum over a wave of a double, to every lane.
 __device__ inline double wave_sum(double v) {
@@ -269,13 +278,15 @@ __device__ inline void write_sums(const RouteCall& c, const RouteWork& w, const 
 }
 
 template <typename T, int E, int L>
-__global__ __launch_bounds__(kRouteBlock) void route_fwd_kernel(RouteCall c, RouteWork w) {
+__global__ __launch_bounds__(kRouteBlock) void route_fwd_kernel(RouteCall c, RouteWork work) {
   constexpr int kRows = kRouteBlock / L;   // at once
   constexpr int kMost = L * E < kMaxChosen ? L * E : kMaxChosen;
   constexpr int kSums = kRows * L * E, kPicks = kRows * kMost;
   __shared__ __align__(16) float lds[kSums > 2 * kPicks ? kSums : 2 * kPicks];
   __shared__ double room[2 * (kRouteBlock + kWave)];
   __shared__ int32_t lds_rows[2 * kRouteBlock / kWave];
+  __shared__ RouteOwn<L * E> own;
+  const RouteWork w = own.or_of(work);
   const int lane = threadIdx.x % L, first = lane * E, group = threadIdx.x / L;
   float* picked = lds + group * kMost;                                     // exp(z - top) of the choices
   int32_t* picked_id = reinterpret_cast<int32_t*>(lds) + kPicks + group * kMost;
@@ -424,12 +435,14 @@ __device__ inline void sort_keys(int (&s)[E]) {
 // rows to 8 of 256: 79 us, 93 with four), where the registers allow.
 constexpr int wide_block(int e) { return e <= 8 ? 1024 : 512; }
 template <typename T, int E>
-__global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void route_fwd_wide_kernel(RouteCall c,
-                                                                                                 RouteWork w) {
+__global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void route_fwd_wide_kernel(
+    RouteCall c, RouteWork work) {
   constexpr int B = wide_block(E), kWaves = B / kWave;
   __shared__ __align__(16) float lds[kWaves * kWave * E];
   __shared__ double room[2 * (B + kWave)];
   __shared__ int32_t lds_rows[2 * kWaves], hist[kWave * E];   // hist: choices of each branch
+  __shared__ RouteOwn<kWave * E> own;
+  const RouteWork w = own.or_of(work);
   const int lane = threadIdx.x % kWave, first = lane * E;
   float p_sum[E];
   int n_rows = 0, n_picks = 0;
@@ -864,7 +877,10 @@ __global__ __launch_bounds__(kGateBlock) void gate_bwd_kernel(GateCall c) {
 
 }  // namespace
 
-size_t route_floats(int64_t rows, int n) { return 2 * kWave + size_t(route_blocks(rows, n)) * (2 * size_t(n) + 2); }
+size_t route_floats(int64_t rows, int n) {
+  const size_t blocks = size_t(route_blocks(rows, n));
+  return blocks == 1 ? 0 : 2 * kWave + blocks * (2 * size_t(n) + 2);
+}
 hipError_t launch_route_forward(const RouteCall& c, Elem type, hipStream_t s) { return run(c, type, false, s); }
 hipError_t launch_route_backward(const RouteCall& c, Elem type, hipStream_t s) { return run(c, type, true, s); }
 

@@ -476,7 +476,7 @@ int cgtp_group_norm_backward(int dtype, int64_t n_rows, int64_t width, int64_t n
  * A row whose logits hold NaN or +infinity has NaN gates and makes balance NaN.
  * 1 <= n <= 1024, 1 <= k <= min(n, 64).  Sums over rows in a fixed order, joined in fp64; no
  * atomics: bitwise reproducible.  workspace: 256-byte aligned, cgtp_route_workspace_size
- * bytes; calls that may run at the same time need one each. */
+ * bytes (0: NULL); calls that may run at the same time need one each. */
 int cgtp_route_workspace_size(int64_t n_rows, int n, size_t* bytes);
 int cgtp_route_forward(int dtype, int64_t n_rows, int n, int k, const void* logits, int64_t ld, const uint8_t* mask,
                        int renormalise, int dense, int32_t* ids, float* gates, int32_t* counts, float* balance,

@@ -54,14 +54,14 @@ int main() {
   EXPECT(cgtp_group_norm_backward(CGTP_F32, 2, 8, 2, 1, nullptr, 0, buf, 8, buf, 8, buf, CGTP_F32, nullptr, nullptr, 0,
                                   nullptr, 8, nullptr, nullptr, nullptr, 0, nullptr) == CGTP_OK);
   for (int n : {1, 8, 17, 1024})
-    for (int64_t rows : {int64_t(0), int64_t(1), int64_t(1000), (int64_t(1) << 31) - 1})
-      EXPECT(cgtp_route_workspace_size(rows, n, &bytes) == CGTP_OK && bytes % 256 == 0 && bytes > 0);
+    for (int64_t rows : {int64_t(0), int64_t(1), int64_t(10000), (int64_t(1) << 31) - 1})
+      EXPECT(cgtp_route_workspace_size(rows, n, &bytes) == CGTP_OK && bytes % 256 == 0 && (bytes > 0) == (rows > 4096));
   EXPECT(cgtp_route_workspace_size(1, 0, &bytes) == CGTP_ERR_INVALID_ARG);
   EXPECT(cgtp_route_workspace_size(1, 2000, &bytes) == CGTP_ERR_UNSUPPORTED);
   int32_t ids[8];
   EXPECT(cgtp_route_forward(CGTP_F32, 2, 4, 5, buf, 4, nullptr, 0, 0, ids, buf, ids, buf, buf, buf, 4096, nullptr) ==
          CGTP_ERR_INVALID_ARG);
-  EXPECT(cgtp_route_forward(CGTP_F32, 2, 4, 2, buf, 4, nullptr, 0, 0, ids, buf, ids, buf, buf, nullptr, 0, nullptr) ==
+  EXPECT(cgtp_route_forward(CGTP_F32, 100000, 4, 2, buf, 4, nullptr, 0, 0, ids, buf, ids, buf, buf, nullptr, 0, nullptr) ==
          CGTP_ERR_WORKSPACE);
   EXPECT(cgtp_route_backward(CGTP_F32, 2, 4, 2, buf, 4, 0, 0, ids, nullptr, nullptr, buf, buf, 4, nullptr) ==
          CGTP_ERR_INVALID_ARG);

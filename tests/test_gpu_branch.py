@@ -682,7 +682,8 @@ def test_argument_checks(dev):
                                                   workspace=torch.empty(0, dtype=torch.uint8, device=dev)), -5),
                     (lambda: C.route_forward(torch.zeros(2, 1025, device=dev), 1), -3),
                     (lambda: C.route_forward(torch.zeros(2, 100, device=dev), 65), -3),
-                    (lambda: C.route_forward(x, 2, workspace=torch.empty(0, dtype=torch.uint8, device=dev)), -5)):
+                    (lambda: C.route_forward(torch.zeros(100000, 8, device=dev), 2,
+                                             workspace=torch.empty(0, dtype=torch.uint8, device=dev)), -5)):
         with pytest.raises(C.CgtpError) as err:
             f()
         assert err.value.code == code
