@@ -20,6 +20,16 @@
 // groups.  A sample that the registers of one workgroup hold is read once, in one launch.
 // Longer ones are cut into tiles of rows whose sums a second launch joins and a third applies,
 // reading the rows again.
+//
+// Both passes move 2 to 3 elements for each that they sum: the caches' and HBM's rate bounds
+// them, and in 16 bits the arithmetic of the activations beside it.  Measured, sums, join and
+// output in us: forward of 561680 x 128 fp32 in 28 samples 53 + 5 + 93 (5.4 and 6.2 TB/s), of
+// 114688 x 128 bf16 in one 9 + 4 + 14; backward of 20060 x 481 fp32 in 48 samples 20 + 6 + 23,
+// of 114688 x 128 bf16 with gelu 19 + 6 + 21 (its vector units 80 % busy: two transcendental
+// functions of four cycles each beside some 25 operations a value and pass).  418 x 64 in one
+// launch of 6.3.  Tried and not kept: loads of the next rows ahead of the sums (45 and 48 us
+// for the bf16 backward without and with), and 2, 4 and 8 columns a thread in 16 bits (30, 27
+// and 31 us for that forward: eight columns' statistics leave too few waves).
 #include <type_traits>
 
 #include "group_layout.hpp"
@@ -1063,11 +1073,33 @@ __global__ __launch_bounds__(B) void group_bwd_join_kernel(GroupCall c, GroupLay
   }
 }
 
-// The weights' gradients of kParamColumns columns from the samples' sums, by a workgroup of B,
-// in a fixed order.
+// Of many samples, runs of `fold` are summed first, each in the place of its first sample, by a
+// thread for each run and column: some 8 sqrt(samples) runs, so that its chain of additions and
+// those of sum_params' 64 lanes a column behind it have sqrt(samples) / 8 each.  The backward of
+// equal samples with it and without: 5000 (60000 x 64 fp32) 28 and 36 us, 100000 (600000 x 64)
+// 235 and 464, 8000 (32000 x 512) 93 and 113; 1200 (14400 x 64) 21 and 19.
+constexpr int64_t kFoldFrom = 2048;
+int64_t fold_of(const GroupCall& c) {
+  return c.samples > kFoldFrom ? int64_t(std::sqrt(double(c.samples)) / 8) : 1;
+}
+constexpr int kFoldBlock = 256;
+__global__ __launch_bounds__(kFoldBlock) void group_fold_kernel(GroupCall c, float* join, int64_t fold) {
+  const int64_t ld = 2 * c.width, all = (c.samples + fold - 1) / fold * ld;
+  for (int64_t i = int64_t(blockIdx.x) * kFoldBlock + threadIdx.x; i < all; i += int64_t(gridDim.x) * kFoldBlock) {
+    const int64_t first = i / ld * fold, last = min(first + fold, c.samples);
+    float* at = join + first * ld + i % ld;
+    float v = 0;
+#pragma unroll 8
+    for (int64_t s = 0; s < last - first; ++s) v += at[s * ld];
+    *at = v;
+  }
+}
+
+// The weights' gradients of kParamColumns columns from the (folded) samples' sums, by a workgroup
+// of B, in a fixed order.
 constexpr int kParamColumns = 16;
 template <typename T, int B>
-__device__ inline void sum_params(const GroupCall& c, const float* join, int block) {
+__device__ inline void sum_params(const GroupCall& c, const float* join, int64_t fold, int block) {
   constexpr int kSubs = B / kParamColumns;
   __shared__ float lds[2][B];
   const int sub = threadIdx.x / kParamColumns, lane = threadIdx.x % kParamColumns;
@@ -1075,7 +1107,7 @@ __device__ inline void sum_params(const GroupCall& c, const float* join, int blo
   float a = 0, b = 0;
   if (e < c.width) {
 #pragma unroll 8
-    for (int64_t s = sub; s < c.samples; s += kSubs) {
+    for (int64_t s = sub * fold; s < c.samples; s += kSubs * fold) {
       a += join[s * ld + e];
       b += join[s * ld + c.width + e];
     }
@@ -1098,9 +1130,9 @@ __device__ inline void sum_params(const GroupCall& c, const float* join, int blo
 // The first `params` workgroups sum the weights' gradients, the others have a tile each.
 template <typename T, int V>
 __global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c, GroupLayout y, const float* coef,
-                                                                     const float* join, int params) {
+                                                                     const float* join, int64_t fold, int params) {
   if (int(blockIdx.x) < params) {
-    sum_params<T, kTileBlock>(c, join, blockIdx.x);
+    sum_params<T, kTileBlock>(c, join, fold, blockIdx.x);
     return;
   }
   const int block = from_behind(blockIdx.x - params, y.tiles * y.chunks);
@@ -1136,14 +1168,23 @@ __global__ __launch_bounds__(kTileBlock) void group_bwd_apply_kernel(GroupCall c
 // The weights' gradients by themselves, behind whole samples.
 constexpr int kParamBlock = 1024;
 template <typename T>
-__global__ __launch_bounds__(kParamBlock) void group_param_kernel(GroupCall c, const float* join) {
-  sum_params<T, kParamBlock>(c, join, blockIdx.x);
+__global__ __launch_bounds__(kParamBlock) void group_param_kernel(GroupCall c, const float* join, int64_t fold) {
+  sum_params<T, kParamBlock>(c, join, fold, blockIdx.x);
 }
 
 // ---- launches ----------------------------------------------------------------------
 
 // Workgroups of one item each, as many as a launch takes.
 unsigned blocks_of(int64_t items, int threads) { return unsigned(std::min(items, kGroupGrid / threads - kZeroBlocks)); }
+
+unsigned param_blocks(const GroupCall& c) { return unsigned((c.width + kParamColumns - 1) / kParamColumns); }
+void fold(const GroupCall& c, float* join, hipStream_t s) {
+  const int64_t f = fold_of(c);
+  if (f == 1) return;
+  const int64_t threads = (c.samples + f - 1) / f * 2 * c.width;
+  hipLaunchKernelGGL(group_fold_kernel, dim3(blocks_of((threads + kFoldBlock - 1) / kFoldBlock, kFoldBlock)), dim3(kFoldBlock),
+                     0, s, c, join, f);
+}
 
 template <typename T, int V, int B>
 void whole(const GroupCall& c, const GroupLayout& y, bool backward, float* join, hipStream_t s) {
@@ -1194,10 +1235,11 @@ void tiles(const GroupCall& c, const GroupLayout& y, bool backward, bool sums, f
                        coef);
   else if (joins)
     hipLaunchKernelGGL((group_bwd_join_kernel<T, 64>), dim3(blocks_of(joins, 64)), dim3(64), 0, s, c, y, pieces, join, coef);
-  const unsigned params = sums ? unsigned((c.width + kParamColumns - 1) / kParamColumns) : 0u;
+  const unsigned params = sums ? param_blocks(c) : 0u;
+  if (sums) fold(c, join, s);
   if (params + (c.y ? back : 0))
     hipLaunchKernelGGL((group_bwd_apply_kernel<T, V>), dim3(params + (c.y ? back : 0)), block, 0, s, c, y, coef, join,
-                       int(params));
+                       fold_of(c), int(params));
 }
 
 template <typename T, int V>
@@ -1216,9 +1258,10 @@ hipError_t run(const GroupCall& c, const GroupLayout& y, bool backward, hipStrea
     whole<T, V, 256>(c, y, backward, join, s);
   else
     whole<T, V, 1024>(c, y, backward, join, s);
-  if (sums)
-    hipLaunchKernelGGL(group_param_kernel<T>, dim3(unsigned((c.width + kParamColumns - 1) / kParamColumns)),
-                       dim3(kParamBlock), 0, s, c, join);
+  if (sums) {
+    fold(c, join, s);
+    hipLaunchKernelGGL(group_param_kernel<T>, dim3(param_blocks(c)), dim3(kParamBlock), 0, s, c, join, fold_of(c));
+  }
   return hipGetLastError();
 }
 

@@ -705,3 +705,127 @@ def test_group_norm_of_small_values(dev):
         gx, gw, gb = C.group_norm_backward(g, x, st, 4, **args)
         gx2, gw2, gb2 = C.group_norm_backward(g, x * 2.0 ** -60, st2, 4, **args)
         assert torch.equal(gx * 2.0 ** 60, gx2) and torch.equal(gw, gw2) and torch.equal(gb, gb2)
+
+
+# ---- sizes and uses at the ends of what the documents allow -----------------------------
+
+@pytest.mark.parametrize("width,groups", [(1 << 20, 1), (1 << 20, 1 << 20), (1 << 20, 1 << 10), (1 << 24, 16)])
+def test_group_norm_of_the_widest_rows(width, groups, dev):
+    gen = torch.Generator(dev).manual_seed(15)
+    x = torch.randn(9, width, device=dev, generator=gen)
+    y, st = C.group_norm_forward(x, groups, samples=_offsets([0, 4, 9], dev), eps=1e-2)
+    g = torch.randn(9, width, device=dev, generator=gen)
+    gx, gw, gb = C.group_norm_backward(g, x, st, groups, samples=_offsets([0, 4, 9], dev))
+    rw, rb = 0, 0
+    for s, (i, j) in enumerate(((0, 4), (4, 9))):
+        v, d = (t[i:j].double().view(j - i, groups, -1) for t in (x, g))
+        mean = v.mean((0, 2), keepdim=True)
+        rstd = ((v - mean).square().mean((0, 2), keepdim=True) + 1e-2).rsqrt()
+        h = (v - mean) * rstd
+        # as above, with rstd up to 10: h below 3 10 and its errors ten times
+        assert (y[i:j] - h.view(j - i, -1)).abs().max() < 2e-3
+        want = rstd * (d - d.mean((0, 2), keepdim=True) - h * (d * h).mean((0, 2), keepdim=True))
+        assert (gx[i:j] - want.view(j - i, -1)).abs().max() < 2e-2
+        rw, rb = rw + (d * h).sum(0).view(-1), rb + d.sum(0).view(-1)
+    assert (gw - rw).abs().max() < 2e-2 and (gb - rb).abs().max() < 1e-4
+
+
+def test_group_norm_of_millions_of_samples(dev):
+    # one row each, in one group: a layer norm
+    x = torch.randn(3000000, 8, device=dev, generator=torch.Generator(dev).manual_seed(16))
+    y, st = C.group_norm_forward(x, 1, samples=3000000, eps=1e-2)
+    z, st2 = C.layer_norm_forward(x, eps=1e-2)
+    assert (y - z).abs().max() < 1e-4 and (st[0, :, 0] - st2[0]).abs().max() < 1e-5
+    g = torch.randn(3000000, 8, device=dev, generator=torch.Generator(dev).manual_seed(17))
+    gx, gw, _ = C.group_norm_backward(g, x, st, 1, samples=3000000)
+    ref = C.layer_norm_backward(g, x, st2)
+    assert (gx - ref[0]).abs().max() < 1e-2
+    # 3e6 terms: both sums' chains stay below 3e6 / 1e4 + 100 additions
+    assert (gw.double() - (g.double() * z.double()).sum(0)).abs().max() < 400 * U * 3e6
+
+
+def test_group_norm_without_stats(dev):
+    # the C entry point alone takes no stats; y is the same
+    lib, stream = C._lib.load(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rng = np.random.default_rng(18)
+    for rows in (300, 60000):
+        x, _ = _rows(rng, rows, 40, F32, dev)
+        want, _ = C.group_norm_forward(x, 4, samples=1, activation="gelu")
+        y, size = torch.empty_like(x), ctypes.c_size_t()
+        assert lib.cgtp_group_norm_workspace_size(0, 0, rows, 40, 4, 1, None, 0, ctypes.byref(size)) == 0
+        ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=dev)
+        assert lib.cgtp_group_norm_forward(0, rows, 40, 4, 1, None, 0, x.data_ptr(), 40, 0, None, None, 2, 1e-5, 0, y.data_ptr(),
+                                           40, None, ws.data_ptr(), size.value, stream) == 0
+        assert torch.equal(y, want)
+
+
+def test_calls_that_run_at_the_same_time(dev):
+    # two streams, each with results and workspaces of its own, against the same calls alone
+    rng = np.random.default_rng(19)
+    sets = [(_rows(rng, 50000, 96, F32, dev)[0], _rows(rng, 50000, 96, F32, dev)[0]) for _ in range(2)]
+    logits = [torch.from_numpy(rng.normal(size=(50000, n))).float().to(dev) for n in (8, 100)]
+
+    def once(i):
+        x, g = sets[i]
+        y, st = C.group_norm_forward(x, 6, samples=5, activation="silu")
+        r = C.route_forward(logits[i], 3, dense=True)
+        return (y, st, *C.group_norm_backward(g, x, st, 6, samples=5, activation="silu"), *r[:5],
+                C.route_backward(logits[i], r, r.gates, r.balance), C.conv_gate_backward(x, g, r.gates[0]))
+
+    alone = [once(i) for i in range(2)]
+    torch.cuda.synchronize()
+    sides, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(4):
+        for i, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                got[i].append(once(i))
+    torch.cuda.synchronize()
+    for want, runs in zip(alone, got):
+        for run in runs:
+            assert all(torch.equal(a, c) for a, c in zip(want, run))
+
+
+def test_route_of_many_rows(dev):
+    # counts past 2^24 are whole; every workgroup takes many turns
+    rows = 20000003
+    logits = torch.zeros(rows, 2, dtype=BF16, device=dev)
+    logits[-5:, 1] = 1
+    r = C.route_forward(logits, 1)
+    assert r.counts.tolist() == [rows - 5, 5] and (r.ids[:-5] == 0).all() and (r.ids[-5:] == 1).all()
+    p = torch.softmax(logits.double(), 1).sum(0).cpu()
+    balance = 2 * float((r.counts.cpu().double() * p).sum()) / rows ** 2
+    # a thread's chain has rows / 2^18 = 77 additions, its workgroup's 8 steps
+    assert abs(float(r.balance) - balance) < 200 * U * balance
+
+
+def test_route_places_past_32_bits(dev):
+    # logits' and dense gates' places above 2^32 bytes and 2^31 elements
+    rows, n = 2200000, 1000
+    logits = torch.zeros(rows, n, dtype=BF16, device=dev)
+    logits[-3:, 997] = 30
+    logits[-1, 3] = 29
+    r = C.route_forward(logits, 2, dense=True)
+    assert r.ids[-3:].tolist() == [[997, 0], [997, 0], [997, 3]] and (r.ids[:-3] == torch.tensor([0, 1], device=dev)).all()
+    assert r.counts[[0, 1, 3, 997]].tolist() == [rows - 1, rows - 3, 1, 3]
+    assert (r.gates[997, -3:] > 0.5).all() and (r.gates[997, :-3] == 0).all() and (r.gates[0, :-3] - 1e-3).abs().max() < 1e-8
+    up = torch.zeros_like(r.gates)
+    up[997, -1] = 1
+    grad = C.route_backward(logits, r, up)
+    p = torch.softmax(logits[-1].double(), 0)
+    want = -p * p[997]
+    want[997] += p[997]
+    # 100 u of p (|u| + sum |u| p), twice, and the rounding to bf16
+    assert ((grad[-1].double() - want).abs() <= 2.0 ** -8 * want.abs() + 400 * U).all()
+    assert (grad[:-1] == 0).all()
+
+
+def test_gate_backward_places_past_32_bits(dev):
+    # rows of masked edges are not read, nor ever written here
+    edges, width = 2300000, 1000
+    w, g = (torch.empty(edges, width, device=dev) for _ in range(2))
+    mask = torch.zeros(edges, dtype=torch.uint8, device=dev)
+    gate = torch.full((edges,), 0.5, device=dev)
+    for e in (0, 2147484, edges - 1):
+        mask[e], w[e], g[e] = 1, 2.0, 3.0
+    out = C.conv_gate_backward(w, g, gate, mask)
+    assert out.nonzero().flatten().tolist() == [0, 2147484, edges - 1] and out[-1].item() == 12000.0
