@@ -744,7 +744,7 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (i < left) add(unpack<T, V>(hx[i]), unpack<T, V>(hg[i]));
-    sum.done(k);
+    if (rows > 0) sum.done(k);   // without rows rstd may be infinite
     const int n = column_sums(p, q, y.slices, sum.d, sum.h, lds);
     // the columns' sums, for the weights' gradients
     for (int e = threadIdx.x; e < q.cw; e += B) {

@@ -709,6 +709,23 @@ def test_group_norm_of_small_values(dev):
 
 # ---- sizes and uses at the ends of what the documents allow -----------------------------
 
+def test_group_norm_without_eps_and_an_empty_sample(dev):
+    # 1/sqrt(0) of a sample without rows reaches no gradient
+    rng = np.random.default_rng(14)
+    for longest in (None, 700):
+        x, xr = _rows(rng, 700, 24, F32, dev)
+        g, gr = _rows(rng, 700, 24, F32, dev)
+        cuts = [0, 0, 300, 300, 700, 700]
+        args = dict(samples=_offsets(cuts, dev), activation="silu", longest=longest)
+        y, st = C.group_norm_forward(x, 3, eps=0.0, **args)
+        assert y.isfinite().all() and (st[1, ::2] == float("inf")).all() and (st[0, ::2] == 0).all()
+        full = C.group_norm_backward(g, x, st, 3, **args)
+        ref = C.group_norm_backward(g, x, st[:, 1::2].contiguous(), 3, samples=_offsets([0, 300, 700], dev),
+                                    activation="silu", longest=longest)
+        for a, c in zip(full, ref):
+            assert a.isfinite().all() and (a - c).abs().max() <= 1e-3 * (1 + c.abs().max())
+
+
 @pytest.mark.parametrize("width,groups", [(1 << 20, 1), (1 << 20, 1 << 20), (1 << 20, 1 << 10), (1 << 24, 16)])
 def test_group_norm_of_the_widest_rows(width, groups, dev):
     gen = torch.Generator(dev).manual_seed(15)
