@@ -8,7 +8,7 @@
 // joined in a fixed order by one last workgroup (up to 64 branches) or several.
 //
 // Up to 16 branches a row is one lane's, and the two launches' latency bounds the call: 114688
-// masked bf16 rows to 2 of 8 branches 7 + 6 us.  131072 fp32 rows to 8 of 256 take 73 + 5 + 4 us
+// masked bf16 rows to 2 of 8 branches 7 + 6 us.  131072 fp32 rows to 8 of 256 take 70 + 5 + 4 us
 // for 138 MB: the vector units are 95 % busy with 276 operations a row, half of them the eight
 // choices (16 each: six steps of a maximum over the wave, the ballot, the keys' move).  A way
 // by keys alone, four rows a wave and 72 operations a choice, took 169 us.  Backward: 114688
