@@ -36,9 +36,12 @@ struct GroupLayout {
 // (forward of 114688 x 128 bf16 27 us with four, 31 with eight, 30 with two).
 constexpr int kGroupVec = 4;
 
-// Rows that a thread holds of a whole sample: 64 registers of x, or 48 of x and grad_out (64
-// of them spill in workgroups of 1024).
+// Rows that a thread holds of a whole sample: 64 registers of x, or 48 of x and grad_out.
 constexpr int kHeldFew = 4;
+// Most rows that a thread reads of a whole sample.  With 64, that 16-bit rows allow, the forward of
+// 96000 x 128 bf16 in 24 samples took 44 us as whole samples, 26 as tiles; of 48000 x 128 (31 rows
+// a thread) it takes 22.
+constexpr int kWholeTurns = 32;
 constexpr int held_most(int elem_bytes, bool backward) { return (backward ? 24 : 64) / elem_bytes; }
 
 // Workgroups with a tile each: one for every place that the device has for them (some 1000), or,
@@ -69,25 +72,24 @@ inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backwa
   const int most = held_most(elem_bytes, backward);
   // A workgroup for a whole sample: 64 threads with the widest chunk that leaves kWant
   // workgroups, else 256 with chunks down to 32 bytes of a row; both hold half of the longest
-  // sample at least, and read the rest again.  1024 threads that hold it whole, one workgroup to
-  // a compute unit, only where there are no more of them than units.  Else tiles.  Measured, us
-  // of whole samples and of tiles: forward of 40000 x 64 fp32 in 100 samples 14 and 21 (in
-  // workgroups that hold all 17), of 600000 x 64 in 1500 75 and 114 (86; 124 where a quarter is
-  // held); 1024 threads: of 8000 x 128 in 4 16 and 20, but of 20060 x 481 in 48 (624 workgroups)
-  // 62 and 35, of 128000 x 128 bf16 in 64 (512) 44 and 31.
-  constexpr int64_t kWant = 512, kUnits = 256;
-  for (const int block : {64, 256, 1024}) {
+  // sample at least, and read the rest again.  Else tiles.  Measured, us of whole samples and of
+  // tiles: forward of 40000 x 64 fp32 in 100 samples 14 and 21 (in workgroups that hold all 17),
+  // of 600000 x 64 in 1500 75 and 114 (86; 124 where a quarter is held).  Workgroups of 1024
+  // threads, for samples that less do not hold: 18 and 21 for the backward of 4000 x 128 fp32 in
+  // 4, but 41 and 31 for the forward of 144000 x 128 bf16 in 24, 40 and 24 for 96808 x 60 in 38.
+  constexpr int64_t kWant = 512;
+  for (const int block : {64, 256}) {
     y.block = block;
     int64_t take = 0, items = 0;
     for (int64_t m = std::min(c.groups, block * int64_t(y.vec) / cg); m >= 1; m = m == 1 ? 0 : (m + 1) / 2) {
       set_lanes(y, m * cg);
-      if (int64_t(y.slices) * most * (block < 1024 ? 2 : 1) < longest) continue;
+      if (int64_t(y.slices) * std::min(2 * most, kWholeTurns) < longest) continue;
       if (take && m * cg * elem_bytes < 32) break;
       take = m;
       items = c.samples * ((c.groups + m - 1) / m);
       if (items >= kWant) break;
     }
-    if (!take || (block == 64 && items < kWant) || (block == 1024 && items > kUnits)) continue;
+    if (!take || (block == 64 && items < kWant)) continue;
     y.whole = 1;
     y.per_chunk = int(take);
     y.chunks = int((c.groups + take - 1) / take);

@@ -1254,10 +1254,8 @@ hipError_t run(const GroupCall& c, const GroupLayout& y, bool backward, hipStrea
   }
   if (y.block == 64)
     whole<T, V, 64>(c, y, backward, join, s);
-  else if (y.block == 256)
-    whole<T, V, 256>(c, y, backward, join, s);
   else
-    whole<T, V, 1024>(c, y, backward, join, s);
+    whole<T, V, 256>(c, y, backward, join, s);
   if (sums) {
     fold(c, join, s);
     hipLaunchKernelGGL(group_param_kernel<T>, dim3(param_blocks(c)), dim3(kParamBlock), 0, s, c, join, fold_of(c));
