@@ -725,7 +725,7 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
     int group[V];
     place_groups(y, p, group);
     Back<T, V> k(c, p);
-    k.sample(c, group, s);
+    if (rows > 0) k.sample(c, group, s);   // without rows there may be no statistics
     Sums<T, V> sum;
     auto add = [&](const Vec<T, V>& vx, const Vec<T, V>& vg) { sum.add(k, c.act, vx, vg); };
     if (own.most > N) for_row_pairs<T, V, kBeside>(c, p, y.slices, rest, end, add);

@@ -453,7 +453,8 @@ int cgtp_group_norm_forward(int dtype, int64_t n_rows, int64_t width, int64_t n_
  *   grad_x = rstd (a - sum(a)/M - h sum(a h)/M)               0 for rows outside every sample
  *   grad_weight[c] = sum over rows of d h, grad_bias[c] = sum over rows of d
  * Each output may be NULL to skip it, and is overwritten; it may not overlap an input.
- * grad_weight and grad_bias are of type weight_dtype. */
+ * grad_weight and grad_bias are of type weight_dtype.  stats of a sample without rows are not
+ * read, and may be NULL where n_rows = 0. */
 int cgtp_group_norm_backward(int dtype, int64_t n_rows, int64_t width, int64_t n_groups, int64_t n_samples,
                              const int32_t* offsets, int64_t longest, const void* grad_out, int64_t ld_g,
                              const void* x, int64_t ld_x, const float* stats, int weight_dtype, const void* weight,

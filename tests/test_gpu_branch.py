@@ -846,3 +846,19 @@ def test_gate_backward_places_past_32_bits(dev):
         mask[e], w[e], g[e] = 1, 2.0, 3.0
     out = C.conv_gate_backward(w, g, gate, mask)
     assert out.nonzero().flatten().tolist() == [0, 2147484, edges - 1] and out[-1].item() == 12000.0
+
+
+@pytest.mark.parametrize("width,groups", [(12, 3), (3, 1), (5000, 1)])
+def test_group_norm_backward_without_rows_or_stats(width, groups, dev):
+    # the C entry point alone takes no stats: without rows there are none to read
+    lib, stream = C._lib.load(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    size = ctypes.c_size_t()
+    for n in (1, 3, 3000):
+        for off in (None, torch.zeros(n + 1, dtype=torch.int32, device=dev)):
+            at = None if off is None else off.data_ptr()
+            assert lib.cgtp_group_norm_workspace_size(1, 0, 0, width, groups, n, at, 0, ctypes.byref(size)) == 0
+            ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=dev)
+            grads = torch.full((2, width), 7.0, device=dev)
+            assert lib.cgtp_group_norm_backward(0, 0, width, groups, n, at, 0, None, width, None, width, None, 0, None, None, 1, None,
+                                                width, grads[0].data_ptr(), grads[1].data_ptr(), ws.data_ptr(), size.value, stream) == 0
+            assert (grads == 0).all()
