@@ -862,3 +862,43 @@ def test_group_norm_backward_without_rows_or_stats(width, groups, dev):
             assert lib.cgtp_group_norm_backward(0, 0, width, groups, n, at, 0, None, width, None, width, None, 0, None, None, 1, None,
                                                 width, grads[0].data_ptr(), grads[1].data_ptr(), ws.data_ptr(), size.value, stream) == 0
             assert (grads == 0).all()
+
+
+@pytest.mark.parametrize("rows,width,groups,dtype,longest,lead", [
+    (60000, 1024, 1, F32, 1, 8), (200000, 64, 4, F32, 1, 400), (60000, 1024, 1, BF16, 1, 40), (300000, 1024, 2, F32, None, 8),
+    (400000, 1024, 1, BF16, None, 8)], ids=str)
+def test_group_norm_threads_of_many_rows(rows, width, groups, dtype, longest, lead, dev):
+    """Samples far longer than told, and tiles of more than 64 rows a thread, with first rows 100
+    deviations off: threads' first values, about which they sum.
+
+    A thread's sums are chains of 64 additions, closed about the mean so far, then of n / 64.  Of
+    |x - K| < 110: the first run's sum is below 7000, off by 64 u 7000 = 0.03, the later ones' by less
+    (K nears the mean as 1 / runs: 0.2 in all), the mean by 0.2 / 3000 at the most, 2e-5 where n =
+    60000.  Squares: a run's are below 8e5, off by 64 u 8e5 = 3, the moves of K by as much, in all
+    some 10 of the n + 1e4 (lead / slices) that they sum to: 1e-3 for n = 3000 + 6e4 / 64 at the
+    worst, where 64 threads' errors of both signs are joined; 1e-4 + n u / 64 otherwise.  rstd is off
+    by half of that.  grad_bias of equal terms: (64 + n / 64 + 30) u of their sum."""
+    gen = torch.Generator(dev).manual_seed(21)
+    x = torch.randn(rows, width, device=dev, generator=gen)
+    x[:lead] += 100
+    x = x.to(dtype)
+    y, st = C.group_norm_forward(x, groups, samples=1, longest=longest)
+    v = x.double().view(rows, groups, -1)
+    mean = v.mean((0, 2), keepdim=True)
+    var = (v - mean).square().mean((0, 2), keepdim=True)
+    rstd = (var + 1e-5).rsqrt()
+    assert (st[0, 0] - mean.flatten()).abs().max() < 3e-5
+    assert (st[1, 0] / rstd.flatten() - 1).abs().max() < 2e-4
+    # the rounding of y, of at most some 100, and rstd's error of it
+    h = ((v - mean) * rstd).view(rows, width)
+    assert ((y.double() - h).abs() <= (torch.finfo(dtype).eps / 2 + 2e-4) * h.abs() + 5e-5).all()
+    del v
+    # the same bounds for the sums of the backward: all of one sign, and equal
+    g = torch.full_like(x, 0.1)
+    gx, gw, gb = C.group_norm_backward(g, x, st, groups, samples=1, longest=longest)
+    d = float(g[0, 0])
+    assert (gb.double() / (d * rows) - 1).abs().max() < (64 + rows / 64 + 30) * U
+    # h within 2e-4 of itself and 5e-5, and the chains, of sum |d h|
+    assert ((gw.double() - d * h.sum(0)).abs() <= d * ((2e-4 + (94 + rows / 64) * U) * h.abs().sum(0) + 5e-5 * rows)).all()
+    # d - mean(d) - h mean(d h) = -h mean(d h), and mean(d h) is 0 but for its error
+    assert (gx.double().abs() <= rstd.max() * d * (1 + rows / 64) * 2 * U + (h.abs() + 1) * d * 3e-4).all()
