@@ -14,6 +14,7 @@
 // by keys alone, four rows a wave and 72 operations a choice, took 169 us.  Backward: 114688
 // rows of 8 branches 5 us, 65536 bf16 rows of 64 11 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch_branch.hpp"
 #include "vec.hpp"
@@ -646,6 +647,10 @@ __device__ inline void wave_in_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// The bits of a float that number() does not return.
+constexpr uint32_t kNotChosen = 0xffffffffu;
+__device__ inline float number(float v) { return v == v ? v : __builtin_nanf(""); }
+
 // dz = p (u - sum(u p)), u the gradient with respect to p: grad_balance slope, and at the
 // chosen the gates' gradients.  Renormalised gates q = p / (sum of the chosen p) are a
 // softmax of the chosen alone: dz gets q (v - sum(v q)) there instead, v the gates' gradients.
@@ -654,14 +659,14 @@ __global__ __launch_bounds__(kRouteBlock) void route_bwd_kernel(RouteCall c) {
   constexpr int kRows = kRouteBlock / L;
   // where a row has many lanes, the choices' gradients reach their branches' lanes through LDS
   constexpr bool kScatter = L > 1;
-  __shared__ __align__(16) float lds[kScatter ? kRows * L * E : 1];
-  __shared__ uint32_t lds_bits[kScatter ? kRouteBlock : 1];
+  __shared__ __align__(16) uint32_t lds[kScatter ? kRows * L * E : 1];
   const int lane = threadIdx.x % L, first = lane * E;
   float slope[E];
 #pragma unroll
   for (int j = 0; j < E; ++j)
     slope[j] = c.grad_balance && first + j < c.n ? c.grad_balance[0] * c.slope[first + j] : 0.0f;
-  for (int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / L; r < c.rows; r += int64_t(gridDim.x) * kRows) {
+  bool twice = false;   // a branch twice in a row
+  auto one_row = [&](int64_t r, auto in_order) {
     T* out = static_cast<T*>(c.grad_logits) + r * c.ld_g;
     const int32_t* ids = c.ids + r * c.k;
     float z[E], d[E];
@@ -669,7 +674,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_bwd_kernel(RouteCall c) {
 #pragma unroll
       for (int j = 0; j < E; ++j) d[j] = 0;
       write_logits(out, first, c.n, d);
-      continue;
+      return;
     }
     read_logits(static_cast<const T*>(c.logits) + r * c.ld, first, c.n, z);
     float top = z[0];   // NaN and infinity show in the sum
@@ -687,24 +692,38 @@ __global__ __launch_bounds__(kRouteBlock) void route_bwd_kernel(RouteCall c) {
     const float inv = __builtin_amdgcn_rcpf(group_sum<L>(s));
     if constexpr (kScatter) {
       if (c.grad_gates) {
-        float* row = lds + threadIdx.x / L * (L * E);
-        uint32_t* bits = lds_bits + threadIdx.x / L * L;
+        uint32_t* row = lds + threadIdx.x / L * (L * E);
+        auto gate_grad = [&](int id, int i) { return c.grad_gates[c.dense ? int64_t(id) * c.rows + r : r * c.k + i]; };
 #pragma unroll
-        for (int j = 0; j < E; ++j) row[first + j] = 0;
-        bits[lane] = 0;
+        for (int j = 0; j < E; ++j) row[first + j] = kNotChosen;
         wave_in_order();
-        for (int i = lane; i < c.k; i += L) {
-          const int id = ids[i];
-          if (unsigned(id) >= unsigned(c.n)) continue;
-          const float v = c.grad_gates[c.dense ? int64_t(id) * c.rows + r : r * c.k + i];
-          // (a choice is one of its kind: the order of two equal ones' sum does not matter)
-          __hip_atomic_fetch_add(row + id, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
-          __hip_atomic_fetch_or(bits + id / E, 1u << (id % E), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+        int given = 0, found = 0;   // choices of the wave's rows, and branches that have one
+        if constexpr (in_order()) {
+          for (int i = 0; lane == 0 && i < c.k; ++i) {
+            const int id = ids[i];
+            if (unsigned(id) >= unsigned(c.n)) continue;
+            const uint32_t b = row[id];
+            const float sum = b == kNotChosen ? 0.0f : __builtin_bit_cast(float, b);
+            row[id] = __builtin_bit_cast(uint32_t, number(sum + gate_grad(id, i)));
+          }
+        } else {
+          for (int i0 = 0; i0 < c.k; i0 += L) {
+            const int i = i0 + lane, id = i < c.k ? ids[i] : -1;
+            const bool some = unsigned(id) < unsigned(c.n);
+            if (some) row[id] = __builtin_bit_cast(uint32_t, number(gate_grad(id, i) + 0.0f));   // as a sum that begins with 0
+            given += __popcll(__ballot(some));
+          }
         }
         wave_in_order();
 #pragma unroll
-        for (int j = 0; j < E; ++j) up[j] = row[first + j];
-        chosen = bits[lane];
+        for (int j = 0; j < E; ++j) {
+          const uint32_t b = row[first + j];
+          const bool in = b != kNotChosen;
+          up[j] = in ? __builtin_bit_cast(float, b) : 0.0f;
+          chosen |= uint32_t(in) << j;
+          found += __popcll(__ballot(in));
+        }
+        if constexpr (!in_order()) twice |= found != given;
         wave_in_order();
       }
     } else if (c.grad_gates) {
@@ -754,7 +773,18 @@ __global__ __launch_bounds__(kRouteBlock) void route_bwd_kernel(RouteCall c) {
         if (chosen >> j & 1) d[j] += z[j] * q * (up[j] - v);
     }
     write_logits(out, first, c.n, d);
-  }
+  };
+  auto rows = [&](auto in_order) {
+    uint32_t t = threadIdx.x;
+    if constexpr (in_order()) asm volatile("" : "+v"(t));   // computed again, not held meanwhile
+    for (int64_t r = int64_t(blockIdx.x) * kRows + t / L; r < c.rows; r += int64_t(gridDim.x) * kRows) one_row(r, in_order);
+  };
+  rows(std::false_type{});
+  // A branch twice in a row, which the forward does not write: the rows again, with gradients added
+  // in the choices' order by a row's first lane.  (Done within the loop it made the loop slower:
+  // 131072 rows of 256 83 us, 67 so.)
+  if constexpr (kScatter)
+    if (twice) rows(std::true_type{});
 }
 
 // ---- launches ----------------------------------------------------------------------

@@ -487,7 +487,8 @@ int cgtp_route_forward(int dtype, int64_t n_rows, int n, int k, const void* logi
  * the gates and the balance loss: grad_gates = dL/dgates (as the forward's gates are laid
  * out; only the entries of chosen branches are read; NULL: 0), grad_balance [1] =
  * dL/dbalance (NULL: 0).  ids and slope are the forward's: choices and counts are held
- * fixed.  Rows without part receive 0.  Ids outside -1 to n - 1 count as -1. */
+ * fixed.  Rows without part receive 0.  Ids outside -1 to n - 1 count as -1; the gradients of a
+ * branch that is twice in a row (the forward writes none) are added in the choices' order. */
 int cgtp_route_backward(int dtype, int64_t n_rows, int n, int k, const void* logits, int64_t ld, int renormalise,
                         int dense, const int32_t* ids, const float* slope, const float* grad_gates,
                         const float* grad_balance, void* grad_logits, int64_t ld_g, void* stream);

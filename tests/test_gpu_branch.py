@@ -902,3 +902,36 @@ def test_group_norm_threads_of_many_rows(rows, width, groups, dtype, longest, le
     assert ((gw.double() - d * h.sum(0)).abs() <= d * ((2e-4 + (94 + rows / 64) * U) * h.abs().sum(0) + 5e-5 * rows)).all()
     # d - mean(d) - h mean(d h) = -h mean(d h), and mean(d h) is 0 but for its error
     assert (gx.double().abs() <= rstd.max() * d * (1 + rows / 64) * 2 * U + (h.abs() + 1) * d * 3e-4).all()
+
+
+@pytest.mark.parametrize("n", [6, 16, 20, 64, 100, 200, 400, 1000])
+def test_route_backward_of_a_branch_twice_in_a_row(n, dev):
+    # ids that no forward writes: the gates' gradients of one branch are added in the choices' order,
+    # which shows in 2^24 + 1 - 2^24 (0, and 1 in another order)
+    z = torch.randn(300, n, device=dev, generator=torch.Generator(dev).manual_seed(22))
+    r = C.route_forward(z, 6)
+    ids = torch.tensor([n - 1, 2, n - 1, 2, n - 1, 2], dtype=torch.int32, device=dev).repeat(300, 1)
+    ids[::3] = r.ids[::3]   # among rows as the forward leaves them
+    up = torch.randn(300, 6, device=dev, generator=torch.Generator(dev).manual_seed(23))
+    big = 2.0 ** 24
+    up[1::3] = torch.tensor([big, 1, 1, big, -big, -big], device=dev)
+    total = up.clone()
+    for i in (2, 4):
+        total[:, 0] += up[:, i]   # in fp32, in order
+        total[:, 1] += up[:, i + 1]
+    once = torch.stack([torch.where(torch.arange(300, device=dev) % 3 == 0, r.ids[:, i], i and 2 if i else n - 1) for i in range(2)], 1).int()
+    for dense in (False, True):
+        if dense:   # one gradient for a branch and row, added as often as it is there
+            u = torch.randn(n, 300, device=dev, generator=torch.Generator(dev).manual_seed(24))
+            got = C.route_backward(z, r._replace(ids=ids, dense=True), u)
+            at = ids.long()
+            flat = torch.gather(u.t(), 1, at)
+            want_up = torch.stack([flat[:, 0] + flat[:, 2] + flat[:, 4], flat[:, 1] + flat[:, 3] + flat[:, 5]], 1)
+        else:
+            got = C.route_backward(z, r._replace(ids=ids), up)
+            want_up = total[:, :2]
+        want = C.route_backward(z, r._replace(ids=once.contiguous()), want_up.contiguous())
+        rows = torch.arange(300, device=dev) % 3 != 0
+        assert torch.equal(got[rows], want[rows])
+        as_forward = C.route_backward(z, r._replace(dense=dense), u if dense else up)
+        assert torch.equal(got[~rows], as_forward[~rows])
