@@ -55,20 +55,36 @@ __device__ inline float exp_of(float x) {
   const float t = x * kLog2e;
   return __builtin_amdgcn_exp2f(t) * (1.0f + fmaf(t, -kLn2, x));
 }
-// (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2).  Of x = |z| / sqrt 2, 1 - erf(x) = exp(-x^2) times a
-// polynomial in 1 / (1 + 0.3275911 x) to 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical
-// Functions, 7.1.26), some 2.5 of fp32's roundings of 1.
+// (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2), by q = exp(-z^2 / 2) times a polynomial in t = 1 /
+// (1 + p |z|): q where z < 0, else 1 - q.  In 16 bits Abramowitz and Stegun's (Handbook of
+// Mathematical Functions, 7.1.26), to 7.5e-8 of 1: nothing beside their rounding.  In 32 bits one of
+// degree 9, fitted to the least greatest error of q itself, 3.2e-8.  GELU is off by 1.6e-8 in the
+// mean over normal z, by erff 1.5e-8 (which loses all digits of the far negative ones; these keep
+// theirs to 1.3e-6), by the shorter polynomial 3.9e-8; the slope by 2.9e-8, 2.0e-8 and 5.4e-8.
+// 561680 x 128 fp32 in 28 samples, forward: 151.8 us, with erff 153.9, the shorter 151.0; 24000 x
+// 128 in 24: 15.7, 18.2, 15.6; backward of 20060 x 481 in 48: 52.9, 59.3, 52.0.
 template <bool Exact>
 __device__ inline float normal_cdf(float z, float& density) {
-  if constexpr (Exact)
+  float t, q;
+  if constexpr (Exact) {
     density = exp_of<true>(-0.5f * z * z);
-  else
+    t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.35f, 1.0f));
+    q = fmaf(t, -0.0291652586f, 0.144067422f);
+    q = fmaf(t, q, -0.25591585f);
+    q = fmaf(t, q, 0.159409285f);
+    q = fmaf(t, q, -0.0232754126f);
+    q = fmaf(t, q, 0.105579846f);
+    q = fmaf(t, q, 0.11981418f);
+    q = fmaf(t, q, 0.139864519f);
+    q = fmaf(t, q, 0.139621243f);
+  } else {
     density = __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.44269504f));
-  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.707106781f, 1.0f));
-  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-  q = fmaf(t, q, 0.5f * 1.421413741f);
-  q = fmaf(t, q, 0.5f * -0.284496736f);
-  q = fmaf(t, q, 0.5f * 0.254829592f);
+    t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.707106781f, 1.0f));
+    q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    q = fmaf(t, q, 0.5f * 1.421413741f);
+    q = fmaf(t, q, 0.5f * -0.284496736f);
+    q = fmaf(t, q, 0.5f * 0.254829592f);
+  }
   q *= t * density;
   return z < 0 ? q : 1.0f - q;
 }

@@ -935,3 +935,29 @@ def test_route_backward_of_a_branch_twice_in_a_row(n, dev):
         assert torch.equal(got[rows], want[rows])
         as_forward = C.route_backward(z, r._replace(dense=dense), u if dense else up)
         assert torch.equal(got[~rows], as_forward[~rows])
+
+
+@pytest.mark.parametrize("groups", [1, 4096])
+def test_group_norm_gelu_in_32_bits(groups, dev):
+    """z of two rows, 1 and -1 times the weight: mean 0 and rstd 1 exactly, so that z is exact.
+    q = 1 - cdf(|z|): exp's roundings 4 u and z^2 / 2 u of its argument, the reciprocal's 2 u twice,
+    the polynomial's (partial sums below 1) 2 u, its fit 0.5 u, products 2 u: (13 + z^2 / 2) u of q
+    itself, one more for y; the rounding of 1 - q where z > 0."""
+    n = 1 << 16
+    gen = torch.Generator(dev).manual_seed(25)
+    z = torch.cat([torch.randn(n // 2, device=dev, generator=gen), 16 * torch.rand(n // 2, device=dev, generator=gen) - 8])
+    x = torch.ones(2, n, device=dev)
+    x[1] = -1
+    y, st = C.group_norm_forward(x, groups, z, activation="gelu", eps=0.0)
+    assert (st[0] == 0).all() and (st[1] == 1).all()
+    zz = torch.stack([z, -z]).double()
+    q = torch.special.erfc(zz.abs() * 0.5 ** 0.5) / 2
+    cdf = torch.where(zz < 0, q, 1 - q)
+    off = (14 + zz.square() / 2) * U * q + (zz > 0) * 2 * U
+    assert ((y.double() - zz * cdf).abs() <= zz.abs() * off + 1e-37).all()
+    g = torch.tensor([[1.0], [0.0]], device=dev).expand(2, n).contiguous()
+    grad_bias = C.group_norm_backward(g, x, st, groups, z, activation="gelu")[2].double()
+    density = torch.exp(-zz[0].square() / 2) * (2 * torch.pi) ** -0.5
+    # the slope cdf + z density: the density's 4 u and z^2 / 2 u, and a product's and a sum's rounding
+    tol = off[0] + zz[0].abs() * density * (6 + zz[0].square() / 2) * U + 2 * U * (cdf[0] + zz[0] * density).abs() + 1e-37
+    assert ((grad_bias - (cdf[0] + zz[0] * density)).abs() <= tol).all()
