@@ -131,7 +131,7 @@ def group_norm_backward(grad_out, x, stats, groups: int, weight=None, bias=None,
     gx = torch.empty_like(x, memory_format=torch.contiguous_format) if "x" in need else None
     gw = x.new_empty(x.shape[1], dtype=wt) if "weight" in need else None
     gb = x.new_empty(x.shape[1], dtype=wt) if "bias" in need else None
-    workspace = _group_room(1, head, workspace, x)
+    workspace = _group_room(1 if gw is not None or gb is not None else 2, head, workspace, x)
     check(load().cgtp_group_norm_backward(*head, grad_out.data_ptr(), ld_g, x.data_ptr(), ld, st, ELEM[wt], w, b, act,
                                           _at(gx), x.shape[1], _at(gw), _at(gb), *_room(workspace, dev),
                                           _raw_stream(dev)))

@@ -101,7 +101,7 @@ int cgtp_group_norm_workspace_size(int backward, int dtype, int64_t n_rows, int6
   if (!bytes) return fail(CGTP_ERR_INVALID_ARG, "NULL argument");
   GroupCall a;
   if (int rc = fill_sizes(a, dtype, n_rows, width, n_groups, n_samples, offsets, longest)) return rc;
-  *bytes = (group_norm_floats(a, Elem(dtype), backward != 0) * sizeof(float) + 255) / 256 * 256;
+  *bytes = (group_norm_floats(a, Elem(dtype), backward != 0, backward != 2) * sizeof(float) + 255) / 256 * 256;
   return ok();
 }
 
@@ -116,7 +116,7 @@ int cgtp_group_norm_forward(int dtype, int64_t n_rows, int64_t width, int64_t n_
   if (n_rows > 0 && !y) return fail(CGTP_ERR_INVALID_ARG, "y is NULL");
   if (n_rows > 1 && ld_y < width) return fail(CGTP_ERR_INVALID_ARG, "row stride of y below the row's width");
   if (!aligned(y, size_t(elem_size(dtype))) || !aligned(stats, 4)) return fail(CGTP_ERR_INVALID_ARG, "misaligned pointer");
-  if (int rc = check_workspace(workspace, ws_bytes, group_norm_floats(a, Elem(dtype), false))) return rc;
+  if (int rc = check_workspace(workspace, ws_bytes, group_norm_floats(a, Elem(dtype), false, false))) return rc;
   a.y = y;
   a.ld_y = ld_y;
   a.stats = stats;
@@ -143,7 +143,8 @@ int cgtp_group_norm_backward(int dtype, int64_t n_rows, int64_t width, int64_t n
       !aligned(grad_bias, ws))
     return fail(CGTP_ERR_INVALID_ARG, "misaligned pointer");
   if (!grad_x && !grad_weight && !grad_bias) return ok();
-  if (int rc = check_workspace(workspace, ws_bytes, group_norm_floats(a, Elem(dtype), true))) return rc;
+  const bool sums = grad_weight || grad_bias;
+  if (int rc = check_workspace(workspace, ws_bytes, group_norm_floats(a, Elem(dtype), true, sums))) return rc;
   a.grad_out = grad_out;
   a.ld_g = ld_g;
   a.stats = const_cast<float*>(stats);

@@ -140,15 +140,16 @@ inline GroupLayout lay_out_group(const GroupCall& c, int elem_bytes, bool backwa
 struct GroupWork {
   int64_t pieces, join, coef, total;   // floats before each, and of all
 };
-inline GroupWork group_work(const GroupCall& c, const GroupLayout& y, bool backward) {
+// sums: the backward's weights' gradients are wanted.
+inline GroupWork group_work(const GroupCall& c, const GroupLayout& y, bool backward, bool sums = true) {
   GroupWork w{};
   const int64_t pieces = y.whole ? 0 : y.tiles + c.samples;
   const int64_t per_piece = backward ? 2 * c.width : 2 * c.groups * y.split;
   w.pieces = 0;
   w.join = pieces * per_piece;
-  // backward: [samples][2][width] sums per channel (of one whole sample: none), then
+  // backward: [samples][2][width] sums per channel (one sample's are the gradients), then
   // [samples][groups][2] means; forward: the statistics, if the caller wants none
-  w.coef = w.join + (backward && !(y.whole && c.samples <= 1) ? c.samples * 2 * c.width : 0);
+  w.coef = w.join + (backward && sums && c.samples > 1 ? c.samples * 2 * c.width : 0);
   w.total = w.coef + (y.whole ? 0 : c.samples * c.groups * 2);
   return w;
 }

@@ -1315,7 +1315,7 @@ void whole(const GroupCall& c, const GroupLayout& y, bool backward, float* join,
 
 template <typename T, int V>
 void tiles(const GroupCall& c, const GroupLayout& y, bool backward, bool sums, float* join, hipStream_t s) {
-  const GroupWork at = group_work(c, y, backward);
+  const GroupWork at = group_work(c, y, backward, sums);
   float *pieces = c.work + at.pieces, *coef = c.work + at.coef;
   const unsigned blocks = unsigned(y.tiles * y.chunks), back = (blocks + kDies - 1) / kDies * kDies;
   const dim3 block{kTileBlock};
@@ -1382,8 +1382,8 @@ hipError_t run(const GroupCall& c, Elem type, bool backward, hipStream_t s) {
 
 }  // namespace
 
-size_t group_norm_floats(const GroupCall& c, Elem type, bool backward) {
-  return size_t(group_work(c, lay_out_group(c, type == Elem::f32 ? 4 : 2, backward), backward).total);
+size_t group_norm_floats(const GroupCall& c, Elem type, bool backward, bool sums) {
+  return size_t(group_work(c, lay_out_group(c, type == Elem::f32 ? 4 : 2, backward), backward, sums).total);
 }
 
 hipError_t launch_group_norm_forward(const GroupCall& c, Elem type, hipStream_t s) { return run(c, type, false, s); }

@@ -32,8 +32,9 @@ struct GroupCall {
   int zero_outside;         // rows outside every sample are written as zeros (else left)
 };
 
-// Floats of workspace that a call needs (x, offsets: whether they are given is looked at).
-size_t group_norm_floats(const GroupCall& c, Elem type, bool backward);
+// Floats of workspace that a call needs (offsets: whether they are given is looked at); sums:
+// whether the backward's weights' gradients are wanted.
+size_t group_norm_floats(const GroupCall& c, Elem type, bool backward, bool sums);
 hipError_t launch_group_norm_forward(const GroupCall& c, Elem type, hipStream_t s);
 hipError_t launch_group_norm_backward(const GroupCall& c, Elem type, hipStream_t s);
 

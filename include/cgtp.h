@@ -438,7 +438,8 @@ enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1, CGTP_ACT_GELU = 2 };
  * longest: rows of the longest sample, as far as the caller knows (0: not known).  It chooses
  * between launches, nothing else: a call with another value is as right, and slower where a
  * sample much longer than told falls to one workgroup.
- * workspace: 256-byte aligned, cgtp_group_norm_workspace_size bytes (0: NULL); calls that may
+ * workspace: 256-byte aligned, cgtp_group_norm_workspace_size bytes (0: NULL), whose `backward`
+ * is 0 for the forward, 1 for the backward, or 2 for a backward of grad_x alone; calls that may
  * run at the same time, replayed graphs among them, need one each.  Rows of at most 2^24
  * values.  No atomics: bitwise reproducible. */
 int cgtp_group_norm_workspace_size(int backward, int dtype, int64_t n_rows, int64_t width, int64_t n_groups,

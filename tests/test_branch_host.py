@@ -130,3 +130,18 @@ def test_python_refuses_host_tensors():
               lambda: C.route_backward(x, route), lambda: C.conv_gate_backward(x, x, e), lambda: C.conv_gate_backward(None, x, e)):
         with pytest.raises(TypeError):
             f()
+
+
+def test_group_norm_workspace_of_what_is_asked_for(lib):
+    ws = ctypes.c_size_t()
+
+    def size(backward, rows, width, groups, samples, off, longest=0):
+        assert lib.cgtp_group_norm_workspace_size(backward, F32, rows, width, groups, samples, off, longest, ctypes.byref(ws)) == 0
+        return ws.value
+
+    # the weights' gradients alone need a sum for each sample and column: not grad_x, nor one sample
+    some = ctypes.c_void_p(64)
+    assert size(1, 3000000, 8, 1, 3000000, None) == 3000000 * 2 * 8 * 4 and size(2, 3000000, 8, 1, 3000000, None) == 0
+    for rows, samples in ((100000, 4), (4000, 10)):
+        assert size(1, rows, 64, 8, samples, some) - size(2, rows, 64, 8, samples, some) in (samples * 2 * 64 * 4 + k for k in (-256, 0, 256))
+    assert size(1, 100000, 64, 8, 1, None) == size(2, 100000, 64, 8, 1, None)

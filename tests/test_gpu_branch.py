@@ -961,3 +961,23 @@ def test_group_norm_gelu_in_32_bits(groups, dev):
     # the slope cdf + z density: the density's 4 u and z^2 / 2 u, and a product's and a sum's rounding
     tol = off[0] + zz[0].abs() * density * (6 + zz[0].square() / 2) * U + 2 * U * (cdf[0] + zz[0] * density).abs() + 1e-37
     assert ((grad_bias - (cdf[0] + zz[0] * density)).abs() <= tol).all()
+
+
+def test_group_norm_backward_of_x_alone_needs_less_room(dev):
+    lib, stream = C._lib.load(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rng = np.random.default_rng(26)
+    for rows, width, groups, samples, longest in ((30000, 8, 1, 30000, 0), (9000, 64, 4, 30, 0), (9000, 64, 4, 30, 9000), (60000, 64, 4, 1, 0)):
+        x, _ = _rows(rng, rows, width, F32, dev)
+        g, _ = _rows(rng, rows, width, F32, dev)
+        args = dict(samples=samples, activation="silu", longest=longest)
+        _, st = C.group_norm_forward(x, groups, eps=1e-2, **args)
+        want = C.group_norm_backward(g, x, st, groups, **args)[0]
+        size = ctypes.c_size_t()
+        assert lib.cgtp_group_norm_workspace_size(2, 0, rows, width, groups, samples, None, longest, ctypes.byref(size)) == 0
+        room = torch.full((size.value + 512,), 77, dtype=torch.uint8, device=dev)
+        gx = torch.empty_like(x)
+        at = room.data_ptr() if size.value else None
+        assert lib.cgtp_group_norm_backward(0, rows, width, groups, samples, None, longest, g.data_ptr(), width, x.data_ptr(), width,
+                                            st.data_ptr(), 0, None, None, 1, gx.data_ptr(), width, None, None, at, size.value, stream) == 0
+        assert torch.equal(gx, want) and (room[size.value:] == 77).all()
+        assert torch.equal(C.group_norm_backward(g, x, st, groups, need=("x",), **args)[0], want)
