@@ -28,20 +28,14 @@ template <int Ctrl>
 __device__ inline uint32_t dpp_u32(uint32_t v) {
   return uint32_t(__builtin_amdgcn_mov_dpp(int(v), Ctrl, 0xf, 0xf, true));
 }
-// Largest of L neighbouring lanes' values (1, 4, 16 or 64), to each of them.
+// Largest of L neighbouring lanes' values, to each of them: of keys 1 or 4 (the forward's wide
+// rows have wave_max), of floats 1, 4, 16 or 64.
 template <int L>
 __device__ inline uint32_t lanes_max(uint32_t v) {
-  if constexpr (L >= 4) {
+  static_assert(L == 1 || L == 4, "");
+  if constexpr (L == 4) {
     v = max(v, dpp_u32<0xB1>(v));   // quad_perm 1 0 3 2
     v = max(v, dpp_u32<0x4E>(v));   // quad_perm 2 3 0 1
-  }
-  if constexpr (L >= 16) {
-    v = max(v, dpp_u32<0x141>(v));  // row_half_mirror
-    v = max(v, dpp_u32<0x140>(v));  // row_mirror
-  }
-  if constexpr (L >= 64) {
-    v = max(v, uint32_t(__shfl_xor(int(v), 16)));
-    v = max(v, uint32_t(__shfl_xor(int(v), 32)));
   }
   return v;
 }
@@ -52,8 +46,8 @@ __device__ inline float lanes_fmax(float v) {
     v = fmaxf(v, dpp<0x4E>(v));
   }
   if constexpr (L >= 16) {
-    v = fmaxf(v, dpp<0x141>(v));
-    v = fmaxf(v, dpp<0x140>(v));
+    v = fmaxf(v, dpp<0x141>(v));    // row_half_mirror
+    v = fmaxf(v, dpp<0x140>(v));    // row_mirror
   }
   if constexpr (L >= 64) {
     v = fmaxf(v, __shfl_xor(v, 16));
@@ -232,17 +226,8 @@ __device__ inline void finish(const RouteCall& c, const RouteWork& w, double* ld
   if (t == 0) c.balance[0] = float(factor > 0 ? factor * weighted : 0.0);
   for (int e = t; e < c.n; e += B) c.slope[e] = float(factor * double(c.counts[e]));
 }
-template <int B>
-__device__ inline void finish(const RouteCall& c, const RouteWork& w, double* lds) {
-  if (c.n <= 4)
-    finish<B, 4>(c, w, lds);
-  else if (c.n <= 16)
-    finish<B, 16>(c, w, lds);
-  else if (c.n <= 64)
-    finish<B, 64>(c, w, lds);
-  else
-    finish<B, 256>(c, w, lds);
-}
+// Branches at once, of n.
+__host__ __device__ constexpr int columns_of(int n) { return n <= 4 ? 4 : n <= 16 ? 16 : n <= 64 ? 64 : 256; }
 
 // A workgroup's sums from its threads': lanes of a wave that hold the same branches, then
 // waves.  lds: B / kWave * L * E floats.
@@ -374,7 +359,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_fwd_kernel(RouteCall c, Rou
   }
   __syncthreads();
   write_sums<kRouteBlock, E, L>(c, w, p_sum, n_of, n_rows, 0, lds, lds_rows, 2);   // (the last step adds the choices itself)
-  if (w.blocks == 1) finish<kRouteBlock>(c, w, room);   // the workgroup sees its own sums
+  if (w.blocks == 1) finish<kRouteBlock, columns_of(L * E)>(c, w, room);   // the workgroup sees its own sums
 }
 
 // A row to a wave, n > 64.  Each lane sorts its E keys once; then the largest of the lanes'
@@ -575,14 +560,20 @@ __global__ __launch_bounds__(wide_block(E), E <= 4 ? 8 : E <= 8 ? 4 : 2) void ro
   for (int e = threadIdx.x; e < c.n; e += B) w.chosen[int64_t(blockIdx.x) * c.n + e] = hist[e];
   if (w.blocks == 1) {
     __syncthreads();
-    finish<B>(c, w, room);
+    finish<B, columns_of(kWave * E)>(c, w, room);
   }
 }
 
+// n <= 64.
 constexpr int kFinishBlock = 1024;
 __global__ __launch_bounds__(kFinishBlock) void route_finish_kernel(RouteCall c, RouteWork w) {
   __shared__ double room[2 * (kFinishBlock + kWave)];
-  finish<kFinishBlock>(c, w, room);
+  if (c.n <= 4)
+    finish<kFinishBlock, 4>(c, w, room);
+  else if (c.n <= 16)
+    finish<kFinishBlock, 16>(c, w, room);
+  else
+    finish<kFinishBlock, 64>(c, w, room);
 }
 
 // The same in many workgroups, kJoinColumns branches each, where there are many sums: counts,
