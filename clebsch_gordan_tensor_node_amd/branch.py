@@ -153,7 +153,8 @@ def route_forward(logits, k: int, mask=None, renormalise: bool = False, dense: b
     """Routes each row (edge) to the k of its n branches with the largest logits [rows, n].
 
     gates are the softmax probabilities of the chosen branches, divided by their sum if
-    `renormalise`; with `dense`, gates[b] [rows] is the gate argument of branch b's conv_forward.
+    `renormalise`; with `dense`, gates[b] [rows] is the gate argument of branch b's conv_forward
+    (a form for few branches: of more than 64 it is written one float at a time, slowly).
     balance = n sum over branches of (share of the choices) (mean probability): 1 where both are
     even, n where one branch has everything.  Rows with mask 0 (uint8 [rows]), or whose logits
     are all -inf, take no part; ties go to the lowest index.  logits are fp32, bf16 or fp16, rows

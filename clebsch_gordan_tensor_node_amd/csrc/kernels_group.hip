@@ -30,8 +30,8 @@
 // Both passes move 2 to 3 elements for each that they sum: the caches' and HBM's rate bounds
 // them, and in 16 bits the arithmetic of the activations beside it.  Measured, sums, join and
 // output in us: forward of 561680 x 128 fp32 in 28 samples 53 + 5 + 93 (5.4 and 6.2 TB/s), of
-// 114688 x 128 bf16 in one 9 + 4 + 14; backward of 20060 x 481 fp32 in 48 samples 20 + 6 + 23,
-// of 114688 x 128 bf16 with gelu 19 + 6 + 21 (its vector units 80 % busy: two transcendental
+// 114688 x 128 bf16 in one 9 + 4 + 14; backward of 20060 x 481 fp32 in 48 samples 21 + 6 + 24,
+// of 114688 x 128 bf16 with gelu 20 + 6 + 22 (its vector units 75 % busy: two transcendental
 // functions of four cycles each beside some 25 operations a value and pass).  418 x 64 in one
 // launch of 6.3.  Tried and not kept: loads of the next rows ahead of the sums (45 and 48 us
 // for the bf16 backward without and with), and 2, 4 and 8 columns a thread in 16 bits (30, 27
@@ -906,9 +906,14 @@ __global__ __launch_bounds__(B) void group_bwd_kernel(GroupCall c, GroupLayout y
 
 // ---- tiles -------------------------------------------------------------------------
 
-// A workgroup's tile and chunk.  Workgroups go to the eight dies (XCDs) by turns, and each has an
-// L2 of its own: the second reading's workgroup of a tile has the first's place among eight.  It
-// comes last first, as what was read last is what the caches still hold.
+// A workgroup's tile and chunk.  The second reading comes last first, as what was read last is
+// what the 256 MB cache behind the L2s still holds: forward of 561680 x 128 fp32 150 us, 160 in the
+// first reading's order, backward 288 and 305; calls that fit it take the same either way.
+// Workgroups go to the eight dies (XCDs) by turns, each with an L2 of its own, and a tile keeps its
+// place among eight: 0.4 us of 26 for 114688 x 128 bf16 and 0.6 for 96000 x 128 against a plain
+// reversal, nothing in 32 bits.  It is not the L2's contents (the second reading fetches past it
+// as much as the first), and behind the weights' gradients' workgroups, where their number is no
+// multiple of eight, tiles move to other dies at no cost.
 struct Tile {
   int tile, chunk, r0, r1;
   __device__ Tile(const GroupCall& c, const GroupLayout& y, int block) {

@@ -8,11 +8,11 @@
 // joined in a fixed order by one last workgroup (up to 64 branches) or several.
 //
 // Up to 16 branches a row is one lane's, and the two launches' latency bounds the call: 114688
-// masked bf16 rows to 2 of 8 branches 7 + 6 us.  131072 fp32 rows to 8 of 256 take 70 + 5 + 4 us
+// masked bf16 rows to 2 of 8 branches 7 + 6 us.  131072 fp32 rows to 8 of 256 take 70 + 5 + 5 us
 // for 138 MB: the vector units are 95 % busy with 276 operations a row, half of them the eight
 // choices (16 each: six steps of a maximum over the wave, the ballot, the keys' move).  A way
 // by keys alone, four rows a wave and 72 operations a choice, took 169 us.  Backward: 114688
-// rows of 8 branches 5 us, 65536 bf16 rows of 64 11 us.
+// rows of 8 branches 5 us, 65536 bf16 rows of 64 12 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -797,8 +797,10 @@ RouteWork route_work(const RouteCall& c) {
   w.picks = w.rows + w.blocks;
   return w;
 }
-// One workgroup joins up to 2^14 sums; measured with 256 blocks of 256 branches (2^16) it takes
-// 9.4 us, the two launches of many 7.
+// Of up to 64 branches one workgroup joins the sums, 2^16 of them at most; of more, many do.
+// Traced, us of the one and of the two launches for many: 448 workgroups' sums of 8 branches 5.9
+// and 6.8, 1024 of 32 8.6 and 6.8, 1024 of 64 9.4 and 7 to 9.6 (whole calls 19.0 and 21.9, 21.5 and
+// 21.3, 36.1 and 34.3); 512 of 256, by the two, 10.
 void finish(const RouteCall& c, const RouteWork& w, hipStream_t s) {
   if (w.blocks == 1) return;
   if (c.n <= 64) {
@@ -833,7 +835,8 @@ void run_wide(const RouteCall& c, bool back, hipStream_t s) {
   finish(c, w, s);
 }
 // The backward keeps no sums: four branches a lane take less time than sixteen (131072 rows of 64
-// fp32 logits 17 us, 24; of 256 68 us, 93; but 65536 of 64 in bf16 11.6 us, 10.7).
+// fp32 logits 17 us, 24; of 256 68 us, 93).  One rule for all types: 65536 rows of 64 in bf16 would
+// take 10.7 us by sixteen, 11.6 by four.
 template <typename T>
 hipError_t run(const RouteCall& c, bool backward, hipStream_t s) {
   if (c.n <= 4)

@@ -470,7 +470,8 @@ int cgtp_group_norm_backward(int dtype, int64_t n_rows, int64_t width, int64_t n
  *   ids [n_rows, k]: the chosen, largest first, -1 where there is none (further);
  *   gates: p of the chosen; with renormalise != 0 divided by their sum.  [n_rows, k] beside
  *     the ids (0 where there is none), or with dense != 0 [n, n_rows], 0 for what a row did
- *     not choose: row b is the gate argument of branch b's convolution;
+ *     not choose: row b is the gate argument of branch b's convolution (for few branches: of
+ *     more than 64 they are written one float at a time, far below the memory's rate);
  *   counts [n]: the rows that chose each branch;
  *   balance [1] and slope [n]: with C the sum of the counts and R the rows that take part,
  *     slope[e] = n counts[e] / (C R), balance = sum over e and rows of slope[e] p[e]: 1 where
